@@ -255,6 +255,59 @@ int moe_fused(const void* X_dev, int x_dtype, int T, const float* W_router_dev, 
               size_t ws_bytes, void* stream);
 
 /*
+ * Norms before and after a block, fused with its gate and residual scale: what
+ * reads the residual stream before a MoE layer and adds the layer's output to
+ * it. With rms(v) = 1 / sqrt(mean(v^2) + eps) over a row of H elements,
+ *   u = o rms(o) gamma_post       (u = o where gamma_post_dev is NULL)
+ *   y = r + scale * sigmoid(gate) * u     (no factor for MPB_GATE_NONE)
+ *   r_out = y,  x_out = y rms(y) gamma_next
+ * in fp32, each output rounded once (x_out is formed from the unrounded y).
+ *   o_dev       [T][H] fp32, the block's output as moe_ffn writes it, or NULL:
+ *               nothing is added (y = r), r_out_dev must be NULL and only x_out
+ *               is written (the norm before the first block)
+ *   r_dev       [T][H] x_dtype residual stream
+ *   gate_dev    MPB_GATE_TOKEN: [T] fp32; MPB_GATE_FULL: [T][H] x_dtype; NULL
+ *               for MPB_GATE_NONE. Gate values before the sigmoid.
+ *   gamma_post_dev, gamma_next_dev   [H] fp32 multipliers (a model that stores
+ *               gamma - 1 passes 1 + its weights), or NULL: no norm of o, no
+ *               x_out. gamma_next_dev and x_out_dev go together.
+ *   r_out_dev, x_out_dev   [T][H] x_dtype; r_out may be r itself.
+ * Row pointers and gammas are 16-byte aligned. scale finite, eps > 0. Needs H a
+ * multiple of 64 up to 65536, T <= 2^20; T == 0 is a no-op. Rows beyond T are
+ * not touched. Squares are summed in fp32: a row whose sum of squares passes
+ * 3.4e38 has rms 0.
+ * Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_HIP. Does not need mpb_init.
+ */
+enum { MPB_GATE_NONE = 0, MPB_GATE_TOKEN = 1, MPB_GATE_FULL = 2 };
+int moe_block_norm(const float* o_dev, const void* r_dev, int x_dtype, int T, int H, const void* gate_dev,
+                   int gate_kind, const float* gamma_post_dev, const float* gamma_next_dev, float scale, float eps,
+                   void* r_out_dev, void* x_out_dev, void* stream);
+
+/*
+ * Backward pass of moe_block_norm. y_dev is the stream after the block (the
+ * r_out it wrote; r itself for a call with o NULL); dr_out_dev and dx_dev are
+ * the gradients of r_out and x_out ([T][H] x_dtype; either may be NULL: zeros,
+ * and dx NULL means that the forward call had no x_out: gamma_next is NULL too
+ * and y_dev may be). Writes
+ *   dr_dev      [T][H] x_dtype, the gradient of r
+ *   do_dev      [T][H] fp32, the gradient of o, or NULL
+ *   dgate_dev   in the gate's form and type, or NULL
+ *   dgamma_post_dev, dgamma_next_dev   [H] fp32 sums over the T rows, or NULL
+ * o_dev is read only with a gate or gamma_post and may be NULL otherwise.
+ * dr may be dr_out or dx itself, and do may be o. Every sum is in fp32 and in
+ * a fixed order (deterministic). ws_dev (16-byte aligned): at least
+ * moe_block_norm_grad_workspace_bytes(T, H) bytes, needed only for the gamma
+ * gradients; contents not preserved. T == 0 zeroes the gamma gradients.
+ * Limits and errors as above, plus MPB_E_WS.
+ */
+size_t moe_block_norm_grad_workspace_bytes(int T, int H);
+int moe_block_norm_grad(const float* o_dev, const void* y_dev, int x_dtype, int T, int H, const void* gate_dev,
+                        int gate_kind, const float* gamma_post_dev, const float* gamma_next_dev, float scale,
+                        float eps, const void* dr_out_dev, const void* dx_dev, void* dr_dev, float* do_dev,
+                        void* dgate_dev, float* dgamma_post_dev, float* dgamma_next_dev, void* ws_dev,
+                        size_t ws_bytes, void* stream);
+
+/*
  * Commit bitwidth b for linear-block i (§3.1 and §3.3: the planner lowers or
  * raises q_i at a safe boundary; a reload raises q_i only once its pages are
  * GPU-resident). Validates 0 <= i < 2*(E+S), b in 3..8 and that planes 0..b-1

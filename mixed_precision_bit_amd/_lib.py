@@ -10,6 +10,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmpb.so")
 
 MPB_F16, MPB_BF16 = 0, 1
+MPB_GATE_NONE, MPB_GATE_TOKEN, MPB_GATE_FULL = 0, 1, 2
 ERRORS = {-1: "MPB_E_ARG", -2: "MPB_E_SHAPE", -3: "MPB_E_RANGE", -4: "MPB_E_NOT_RESIDENT",
           -5: "MPB_E_WS", -6: "MPB_E_HIP", -7: "MPB_E_UNINIT", -8: "MPB_E_BUSY"}
 MPB_PAGE_GPU, MPB_PAGE_CPU, MPB_PAGE_IN_TRANSFER = 0, 1, 2
@@ -52,6 +53,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -75,6 +77,10 @@ def lib() -> ctypes.CDLL:
             "moe_fused": (_I, [_P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
             "moe_ffn": (_I, [_P, _I, _I, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
             "moe_ffn_static": (_I, [_P, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+            "moe_block_norm": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _P, _F, _F, _P, _P, _P]),
+            "moe_block_norm_grad_workspace_bytes": (_SZ, [_I, _I]),
+            "moe_block_norm_grad": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _P, _F, _F, _P, _P, _P, _P, _P, _P, _P, _P,
+                                         _SZ, _P]),
             "set_committed_bits": (_I, [_I, _I]),
             "mpb_committed_bytes": (ctypes.c_int64, [_P]),
             "mpb_get_committed_bits": (_I, [_I]),
@@ -192,6 +198,108 @@ def moe_fused(X, x_dtype, W_router, bias, topk_idx, topk_w, planes_table, luts_t
     return _check("moe_fused", lib().moe_fused(_ptr(X), x_dtype, T, _ptr(W_router), _ptr(bias), _ptr(topk_idx),
                                                _ptr(topk_w), _ptr(planes_table), _ptr(luts_table), _ptr(q),
                                                _ptr(out), _ptr(ws), nbytes, _stream(stream)))
+
+
+_XT = {MPB_F16: torch.float16, MPB_BF16: torch.bfloat16}
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+
+class _Args:
+    """Checks the tensors of one call against the shapes and types the C entry
+    takes them for (a C caller answers for these itself) and hands out their
+    device pointers. Raw 16-bit tensors (int16) stand for either activation
+    type. The call runs with the tensors' device current."""
+
+    def __init__(self, name, device):
+        self.name, self.device = name, device
+
+    def fail(self, msg, code=-1):
+        raise MpbError(self.name, code, msg)
+
+    def __call__(self, what, t, dtype, *shape):
+        if t is None:
+            return None
+        if t.dtype is not dtype and not (dtype.itemsize == 2 and t.dtype is torch.int16):
+            self.fail(f"{what} is {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            self.fail(f"{what} has shape {tuple(t.shape)}, not {shape}", -2)
+        if not t.is_contiguous():
+            self.fail(f"{what} is not contiguous")
+        if t.device != self.device:
+            self.fail(f"{what} is on {t.device}, not {self.device}")
+        return t.data_ptr()
+
+    def bytes(self, ws):
+        """(pointer, bytes) of a workspace."""
+        if ws is None:
+            return None, 0
+        if not ws.is_contiguous() or ws.device != self.device:
+            self.fail(f"the workspace is not contiguous on {self.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+    def run(self, fn, stream, *args):
+        if self.device.type != "cuda":
+            self.fail(f"tensors are on {self.device}")
+        if self.device.index == torch.cuda.current_device():
+            return self.call(fn, stream, args)
+        with torch.cuda.device(self.device):
+            return self.call(fn, stream, args)
+
+    def call(self, fn, stream, args):
+        rc = fn(*args, _stream(stream))
+        return rc if rc >= 0 else _check(self.name, rc)
+
+
+def _xtype(name, x_dtype):
+    if x_dtype not in _XT:
+        raise MpbError(name, -1, f"bad x_dtype {x_dtype!r}")
+    return _XT[x_dtype]
+
+
+def _gate(a, gate, xt, T, H, what="gate"):
+    """(pointer, kind) of a gate: None, [T] fp32 or [T][H] activations."""
+    if gate is None:
+        return None, MPB_GATE_NONE
+    if gate.dim() == 1:
+        return a(what, gate, _F32, T), MPB_GATE_TOKEN
+    return a(what, gate, xt, T, H), MPB_GATE_FULL
+
+
+def moe_block_norm(o, r, x_dtype, gate, gamma_post, gamma_next, scale, eps, r_out, x_out, stream=None):
+    """r_out = r + scale * sigmoid(gate) * norm(o), x_out = norm(r_out); gate: None, [T] fp32 or [T][H]."""
+    a = _Args("moe_block_norm", r.device)
+    xt = _xtype(a.name, x_dtype)
+    if r.dim() != 2:
+        a.fail("r is not [T][H]", -2)
+    T, H = r.shape
+    gp, kind = _gate(a, gate, xt, T, H)
+    return a.run(lib().moe_block_norm, stream, a("o", o, _F32, T, H), a("r", r, xt, T, H), x_dtype, T, H, gp, kind,
+                 a("gamma_post", gamma_post, _F32, H), a("gamma_next", gamma_next, _F32, H), scale, eps,
+                 a("r_out", r_out, xt, T, H), a("x_out", x_out, xt, T, H))
+
+
+def moe_block_norm_grad_workspace_bytes(T, H) -> int:
+    return lib().moe_block_norm_grad_workspace_bytes(T, H)
+
+
+def moe_block_norm_grad(o, y, x_dtype, gate, gamma_post, gamma_next, scale, eps, dr_out, dx, dr, d_o, dgate,
+                        dgamma_post, dgamma_next, ws, stream=None):
+    """Gradients of moe_block_norm from the stream y after the block and the gradients of r_out and x_out."""
+    a = _Args("moe_block_norm_grad", dr.device)
+    xt = _xtype(a.name, x_dtype)
+    if dr.dim() != 2:
+        a.fail("dr is not [T][H]", -2)
+    T, H = dr.shape
+    gp, kind = _gate(a, gate, xt, T, H)
+    dgp, dkind = _gate(a, dgate, xt, T, H, "dgate")
+    if dgate is not None and dkind != kind:
+        a.fail("dgate and gate have different forms")
+    wsp, wsn = a.bytes(ws)
+    return a.run(lib().moe_block_norm_grad, stream, a("o", o, _F32, T, H), a("y", y, xt, T, H), x_dtype, T, H, gp, kind,
+                 a("gamma_post", gamma_post, _F32, H), a("gamma_next", gamma_next, _F32, H), scale, eps,
+                 a("dr_out", dr_out, xt, T, H), a("dx", dx, xt, T, H), a("dr", dr, xt, T, H),
+                 a("do", d_o, _F32, T, H), dgp, a("dgamma_post", dgamma_post, _F32, H),
+                 a("dgamma_next", dgamma_next, _F32, H), wsp, wsn)
 
 
 def set_committed_bits(i, b):

@@ -1,0 +1,75 @@
+// Device helpers shared by the operators around the packed experts (block
+// norms, router losses, request adapters): 8-element vectors of the two
+// activation types and workgroup sums.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mpb {
+
+typedef float fx4 __attribute__((ext_vector_type(4)));
+typedef float fx8 __attribute__((ext_vector_type(8)));
+typedef _Float16 hx8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bx8 __attribute__((ext_vector_type(8)));
+
+struct F16 {
+  typedef _Float16 elem;
+  typedef hx8 vec;
+};
+struct BF16 {
+  typedef __bf16 elem;
+  typedef bx8 vec;
+};
+
+// 8 consecutive activations as fp32 (exact) and back (one rounding, to nearest even).
+template <class D>
+__device__ __forceinline__ fx8 widen(typename D::vec v) {
+  return __builtin_convertvector(v, fx8);
+}
+template <class D>
+__device__ __forceinline__ typename D::vec narrow(fx8 v) {
+  return __builtin_convertvector(v, typename D::vec);
+}
+
+__device__ __forceinline__ fx8 load8(const float* p) {
+  const fx4 a = *(const fx4*)p, b = *(const fx4*)(p + 4);
+  return fx8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+__device__ __forceinline__ void store8(float* p, fx8 v) {
+  *(fx4*)p = fx4{v[0], v[1], v[2], v[3]};
+  *(fx4*)(p + 4) = fx4{v[4], v[5], v[6], v[7]};
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// Sums of N values over the workgroup, the same bits in every thread (each
+// wave's sum by butterflies, then the waves' sums in wave order). buf holds
+// N * 16 floats and is free again after the next barrier.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float* buf) {
+  const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (nw == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[i * 16 + wave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = buf[i * 16];
+    for (int w = 1; w < nw; ++w) s += buf[i * 16 + w];
+    v[i] = s;
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + __expf(-x)); }
+
+}  // namespace mpb

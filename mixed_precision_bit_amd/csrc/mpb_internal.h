@@ -211,6 +211,42 @@ struct FusedLaunch {
 size_t fused_counter_bytes();
 hipError_t launch_fused(const FusedLaunch& L, hipStream_t s);
 
+// Norms before and after a block with its gate and residual scale (k_block_norm.hip).
+struct BlockNormParams {
+  const float* o;       // [T][H] the block's output, or null (norm only)
+  const void* r;        // [T][H] residual stream
+  const void* gate;     // per gate_kind, or null
+  const float* g_post;  // [H] or null
+  const float* g_next;  // [H] (with x)
+  void* r_out;          // [T][H] (with o)
+  void* x;              // [T][H] or null
+  float scale, eps;
+  int gate_kind;        // 0 none, 1 [T] fp32, 2 [T][H] activations
+  int T, H;
+};
+struct BlockNormGradParams {
+  const float* o;       // [T][H] (with a gate or g_post), or null
+  const void* y;        // [T][H] residual stream after the block (with dx)
+  const void* gate;
+  const float* g_post;
+  const float* g_next;
+  const void* dr_out;   // [T][H] or null (zeros)
+  const void* dx;       // [T][H] or null
+  void* dr;             // [T][H]
+  float* d_o;           // [T][H] or null
+  void* dgate;          // as gate, or null
+  float* dg_post;       // [H] or null
+  float* dg_next;       // [H] or null
+  float* part;          // [2][block_norm_grad_groups][H] partial column sums
+  float scale, eps;
+  int gate_kind;
+  int T, H;
+};
+hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s);
+// workgroups of the backward kernel (decided from the shapes only: the workspace depends on it)
+int block_norm_grad_groups(int T, int H);
+hipError_t launch_block_norm_grad(const BlockNormGradParams& p, bool bf16, hipStream_t s);
+
 // Records msg as the calling thread's last error and returns code.
 int set_error(int code, const char* msg);
 // Checks a layer geometry against the ranges the library supports; on failure
