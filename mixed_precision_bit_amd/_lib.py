@@ -210,8 +210,8 @@ class _Args:
     device pointers. Raw 16-bit tensors (int16) stand for either activation
     type. The call runs with the tensors' device current."""
 
-    def __init__(self, name, device):
-        self.name, self.device = name, device
+    def __init__(self, name, t):
+        self.name, self.index = name, t.get_device()  # -1: not on a GPU
 
     def fail(self, msg, code=-1):
         raise MpbError(self.name, code, msg)
@@ -225,28 +225,28 @@ class _Args:
             self.fail(f"{what} has shape {tuple(t.shape)}, not {shape}", -2)
         if not t.is_contiguous():
             self.fail(f"{what} is not contiguous")
-        if t.device != self.device:
-            self.fail(f"{what} is on {t.device}, not {self.device}")
+        if t.get_device() != self.index:
+            self.fail(f"{what} is on {t.device}, other tensors on device {self.index}")
         return t.data_ptr()
 
     def bytes(self, ws):
         """(pointer, bytes) of a workspace."""
         if ws is None:
             return None, 0
-        if not ws.is_contiguous() or ws.device != self.device:
-            self.fail(f"the workspace is not contiguous on {self.device}")
+        if not ws.is_contiguous() or ws.get_device() != self.index:
+            self.fail(f"the workspace is not contiguous on device {self.index}")
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def run(self, fn, stream, *args):
-        if self.device.type != "cuda":
-            self.fail(f"tensors are on {self.device}")
-        if self.device.index == torch.cuda.current_device():
-            return self.call(fn, stream, args)
-        with torch.cuda.device(self.device):
-            return self.call(fn, stream, args)
+        if self.index < 0:
+            self.fail("tensors are on the CPU")
+        if self.index != torch.cuda.current_device():
+            with torch.cuda.device(self.index):
+                return self.call(fn, stream, args)
+        return self.call(fn, stream, args)
 
     def call(self, fn, stream, args):
-        rc = fn(*args, _stream(stream))
+        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
         return rc if rc >= 0 else _check(self.name, rc)
 
 
@@ -267,7 +267,7 @@ def _gate(a, gate, xt, T, H, what="gate"):
 
 def moe_block_norm(o, r, x_dtype, gate, gamma_post, gamma_next, scale, eps, r_out, x_out, stream=None):
     """r_out = r + scale * sigmoid(gate) * norm(o), x_out = norm(r_out); gate: None, [T] fp32 or [T][H]."""
-    a = _Args("moe_block_norm", r.device)
+    a = _Args("moe_block_norm", r)
     xt = _xtype(a.name, x_dtype)
     if r.dim() != 2:
         a.fail("r is not [T][H]", -2)
@@ -285,7 +285,7 @@ def moe_block_norm_grad_workspace_bytes(T, H) -> int:
 def moe_block_norm_grad(o, y, x_dtype, gate, gamma_post, gamma_next, scale, eps, dr_out, dx, dr, d_o, dgate,
                         dgamma_post, dgamma_next, ws, stream=None):
     """Gradients of moe_block_norm from the stream y after the block and the gradients of r_out and x_out."""
-    a = _Args("moe_block_norm_grad", dr.device)
+    a = _Args("moe_block_norm_grad", dr)
     xt = _xtype(a.name, x_dtype)
     if dr.dim() != 2:
         a.fail("dr is not [T][H]", -2)

@@ -96,98 +96,132 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormParams p) {
   }
 }
 
+// One row of the backward pass's inputs as loaded.
 template <class D, int NV>
-__global__ __launch_bounds__(1024) void k_block_norm_grad(BlockNormGradParams p) {
+struct GradRow {
+  fx8 o[NV];
+  typename D::vec y[NV], dx[NV], dr[NV], gate[NV];
+
+  __device__ __forceinline__ void load(const BlockNormGradParams& p, int t) {
+    typedef typename D::vec vec;
+    typedef typename D::elem elem;
+    const size_t row = (size_t)t * p.H;
+    const int nvec = p.H / 8;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      o[j] = (fx8)(0.0f);
+      y[j] = dx[j] = dr[j] = gate[j] = (vec)(typename D::elem)0.0f;
+      if (v < nvec) {
+        const size_t at = row + 8 * v;
+        if (p.dx) {
+          y[j] = *(const vec*)((const elem*)p.y + at);
+          dx[j] = *(const vec*)((const elem*)p.dx + at);
+        }
+        if (p.o) o[j] = load8(p.o + at);
+        if (p.dr_out) dr[j] = *(const vec*)((const elem*)p.dr_out + at);
+        if (p.gate_kind == 2) gate[j] = *(const vec*)((const elem*)p.gate + at);
+      }
+    }
+  }
+};
+
+// THREADS: most threads a launch may have. AHEAD: a row's loads are issued
+// before the row before it is worked on, so that memory stays busy through the
+// two workgroup sums.
+template <class D, int NV, int THREADS, bool AHEAD>
+__global__ __launch_bounds__(THREADS) void k_block_norm_grad(BlockNormGradParams p) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
   __shared__ float buf[2][3 * 16];
   const int tid = threadIdx.x, nt = blockDim.x, nvec = p.H / 8;
-  const bool post = p.g_post != nullptr, next = p.dx != nullptr, need_o = p.o != nullptr;
+  const bool post = p.g_post != nullptr, next = p.dx != nullptr;
   const float inv_h = 1.0f / (float)p.H;
   fx8 gp[NV], gn[NV];  // column sums of dg_post, dg_next
 #pragma unroll
   for (int j = 0; j < NV; ++j) gp[j] = gn[j] = (fx8)(0.0f);
+  GradRow<D, NV> ahead;
+  if (AHEAD) ahead.load(p, blockIdx.x);
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    GradRow<D, NV> in;
+    if (AHEAD) {
+      in = ahead;
+      if (t + (int)gridDim.x < p.T) ahead.load(p, t + gridDim.x);
+    } else {
+      in.load(p, t);
+    }
     const size_t row = (size_t)t * p.H;
-    fx8 o[NV], y[NV], d[NV], dy[NV];
     float s1[3] = {0.0f, 0.0f, 0.0f};  // sums of y^2, d y, o^2
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = tid + j * nt;
-      o[j] = y[j] = d[j] = dy[j] = (fx8)(0.0f);
-      if (v < nvec) {
-        if (p.dr_out) dy[j] = widen<D>(*(const vec*)((const elem*)p.dr_out + row + 8 * v));
-        if (next) {
-          y[j] = widen<D>(*(const vec*)((const elem*)p.y + row + 8 * v));
-          d[j] = widen<D>(*(const vec*)((const elem*)p.dx + row + 8 * v));
-        }
-        if (need_o) o[j] = load8(p.o + row + 8 * v);
-        if (next) {
-          const fx8 e = d[j] * load8(p.g_next + 8 * v);
+      if (next && v < nvec) {
+        const fx8 y = widen<D>(in.y[j]), e = widen<D>(in.dx[j]) * load8(p.g_next + 8 * v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s1[0] += y[j][i] * y[j][i];
-            s1[1] += e[i] * y[j][i];
-          }
-        }
-        if (post) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s1[2] += o[j][i] * o[j][i];
+        for (int i = 0; i < 8; ++i) {
+          s1[0] += y[i] * y[i];
+          s1[1] += e[i] * y[i];
         }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s1[2] += in.o[j][i] * in.o[j][i];
     }
     block_sum<3>(s1, buf[0]);
     const float ry = rsqrtf(s1[0] * inv_h + p.eps), ro = post ? rsqrtf(s1[2] * inv_h + p.eps) : 1.0f;
     const float my = s1[1] * ry * inv_h;  // mean(d yh)
     float k = p.scale, dsig = 0.0f;
     if (p.gate_kind == 1) {
-      const float g = ((const float*)p.gate)[t], sg = sigmoid(g);
-      k *= sg;
+      const float g = ((const float*)p.gate)[t];
+      k *= sigmoid(g);
       dsig = sigmoid(-g);  // sigmoid' = sigmoid(g) sigmoid(-g)
     }
-    float s2[1] = {0.0f};  // sum of du g_post o, and with a token gate of du u
+    float s2[1] = {0.0f};  // sum of du g_post o (with a token gate also that of dv u, but for factors)
+    fx8 dw[NV];            // du g_post
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = tid + j * nt;
+      dw[j] = (fx8)(0.0f);
       if (v < nvec) {
+        fx8 dy = widen<D>(in.dr[j]);
         if (next) {
-          const fx8 yh = y[j] * ry;
-          gn[j] += d[j] * yh;
-          dy[j] += (d[j] * load8(p.g_next + 8 * v) - yh * my) * ry;
+          const fx8 yh = widen<D>(in.y[j]) * ry, d = widen<D>(in.dx[j]);
+          gn[j] += d * yh;
+          dy += (d * load8(p.g_next + 8 * v) - yh * my) * ry;
         }
-        *(vec*)((elem*)p.dr + row + 8 * v) = narrow<D>(dy[j]);
+        *(vec*)((elem*)p.dr + row + 8 * v) = narrow<D>(dy);
         fx8 w = (fx8)(1.0f);
         if (post) w = load8(p.g_post + 8 * v);
-        fx8 du = dy[j] * k;  // with a token gate's sigmoid
+        fx8 du = dy * k;  // with a token gate's sigmoid
         if (p.gate_kind == 2) {
-          const fx8 g = widen<D>(*(const vec*)((const elem*)p.gate + row + 8 * v));
+          const fx8 g = widen<D>(in.gate[j]);
           fx8 dg;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             du[i] *= sigmoid(g[i]);
-            dg[i] = du[i] * o[j][i] * ro * w[i] * sigmoid(-g[i]);
+            dg[i] = du[i] * in.o[j][i] * ro * w[i] * sigmoid(-g[i]);
           }
           if (p.dgate) *(vec*)((elem*)p.dgate + row + 8 * v) = narrow<D>(dg);
         }
-        if (post) gp[j] += du * o[j] * ro;
-        dy[j] = du * w;
+        if (post) gp[j] += du * in.o[j] * ro;
+        dw[j] = du * w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s2[0] += dy[j][i] * o[j][i];
+        for (int i = 0; i < 8; ++i) s2[0] += dw[j][i] * in.o[j][i];
       }
     }
     if (post || p.gate_kind == 1) {
       block_sum<1>(s2, buf[1]);
       if (p.gate_kind == 1 && p.dgate && tid == 0) ((float*)p.dgate)[t] = s2[0] * ro * dsig;
+    } else {
+      __syncthreads();  // buf[0] is free again, as in the forward kernel
     }
     if (p.d_o) {
       const float mo = post ? s2[0] * ro * inv_h * ro : 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int v = tid + j * nt;
-        if (v < nvec) store8(p.d_o + row + 8 * v, post ? (dy[j] - o[j] * mo) * ro : dy[j]);
+        if (v < nvec) store8(p.d_o + row + 8 * v, post ? (dw[j] - in.o[j] * mo) * ro : dw[j]);
       }
     }
-    if (!(post || p.gate_kind == 1)) __syncthreads();  // buf[0], as in the forward kernel
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -208,7 +242,15 @@ __global__ __launch_bounds__(1024) void k_col_sum(const float* part, int n, int 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = blockIdx.x * 64 + lane;
   const float* src = part + (size_t)blockIdx.y * n * H + h;
   float s = 0.0f;
-  for (int i = wave; i < n; i += 16) s += src[(size_t)i * H];
+  int i = wave;
+  for (; i + 7 * 16 < n; i += 8 * 16) {  // eight loads in flight
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = src[(size_t)(i + 16 * j) * H];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[j];
+  }
+  for (; i < n; i += 16) s += src[(size_t)i * H];
   buf[wave][lane] = s;
   __syncthreads();
   if (wave == 0) {
@@ -242,18 +284,19 @@ int block_norm_grad_groups(int T, int H) {
   return T < most ? T : most;
 }
 
+template <class D>
+static void grad_rows(const BlockNormGradParams& p, int grid, hipStream_t s) {
+  if (p.H < 4096) k_block_norm_grad<D, 1, 512, true><<<grid, norm_threads(p.H, 1), 0, s>>>(p);
+  else if (p.H <= 8192) k_block_norm_grad<D, 2, 512, true><<<grid, norm_threads(p.H, 2), 0, s>>>(p);
+  else if (p.H <= 16384) k_block_norm_grad<D, 2, 1024, false><<<grid, norm_threads(p.H, 2), 0, s>>>(p);
+  else k_block_norm_grad<D, 8, 1024, false><<<grid, norm_threads(p.H, 8), 0, s>>>(p);
+}
+
 hipError_t launch_block_norm_grad(const BlockNormGradParams& p, bool bf16, hipStream_t s) {
   const int grid = block_norm_grad_groups(p.T, p.H);
   if (grid) {
-    if (p.H <= 16384) {
-      const int nt = norm_threads(p.H, 2);
-      if (bf16) k_block_norm_grad<BF16, 2><<<grid, nt, 0, s>>>(p);
-      else k_block_norm_grad<F16, 2><<<grid, nt, 0, s>>>(p);
-    } else {
-      const int nt = norm_threads(p.H, 8);
-      if (bf16) k_block_norm_grad<BF16, 8><<<grid, nt, 0, s>>>(p);
-      else k_block_norm_grad<F16, 8><<<grid, nt, 0, s>>>(p);
-    }
+    if (bf16) grad_rows<BF16>(p, grid, s);
+    else grad_rows<F16>(p, grid, s);
   }
   if (p.dg_post || p.dg_next) k_col_sum<<<dim3(p.H / 64, 2), 1024, 0, s>>>(p.part, grid, p.H, p.dg_post, p.dg_next);
   return hipGetLastError();

@@ -361,7 +361,7 @@ def test_tensor_refusals():
             M.moe_block_norm(o, r, xd, gate, gp, gn, 1.0, 1e-6, ro, x)
         return e.value.code, str(e.value)
 
-    assert "tensors are on cpu" in code()[1]
+    assert "on the CPU" in code()[1]
     assert code(o=o.half())[0] == -1 and code(xd=M.MPB_BF16)[0] == -1 and code(xd=7)[0] == -1
     assert code(o=o[:3])[0] == -2 and code(gp=g[:64])[0] == -2 and code(gate=torch.zeros(5))[0] == -2
     assert "contiguous" in code(o=torch.zeros(256, 4).t())[1]
