@@ -308,6 +308,65 @@ int moe_block_norm_grad(const float* o_dev, const void* y_dev, int x_dtype, int 
                         size_t ws_bytes, void* stream);
 
 /*
+ * Router losses of a batch: the load-balance loss and the z loss that train or
+ * watch a router, with the per-expert counts. Over the live tokens (mask_dev[t]
+ * != 0, or all where mask_dev is NULL; a token all of whose logits are -inf is
+ * not live either),
+ *   l = X W_router^T + bias, lse = log sum_e exp(l), p = exp(l - lse)
+ *   counts[e] = live (token, slot) pairs with topk_idx = e,  counts[E] = N =
+ *               live tokens,  prob[e] = sum_t p_te
+ *   balance = E / (K N^2) sum_e counts[e] prob[e]   (1 for a uniform router)
+ *   z = 1/N sum_t lse_t^2
+ *   loss[0..2] = alpha balance + beta z, balance, z
+ *   X_dev, W_router_dev, bias_dev, topk_idx_dev   as for moe_route (16-byte
+ *               aligned X and W_router); ids outside [0, E) are not counted
+ *   logits_dev  [T][E] fp32, lse_dev [T] fp32: kept for the gradient. Rows of
+ *               masked tokens are zeros (what X holds there is not used); a
+ *               token that is not live for its logits has lse -inf.
+ *   counts_dev  [E + 1] int32, prob_dev [E] fp32, loss_dev [3] fp32
+ * Sums over a data-parallel group: counts and prob add up over ranks, and the
+ * gradient below takes the added counts (the balance loss of the global batch).
+ * The logits are exact products accumulated in fp32, in an order other than
+ * moe_route's fp64 one; every sum has a fixed order (deterministic). No live
+ * token: losses 0. ws_dev (16-byte aligned): at least
+ * moe_router_loss_workspace_bytes(T, H, E) bytes, contents not preserved.
+ * Limits as for moe_route. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS,
+ * MPB_E_HIP. Does not need mpb_init.
+ */
+size_t moe_router_loss_workspace_bytes(int T, int H, int E);
+int moe_router_loss(const void* X_dev, int x_dtype, const float* W_router_dev, const float* bias_dev,
+                    const int32_t* topk_idx_dev, const uint8_t* mask_dev, int T, int H, int E, int K, float alpha,
+                    float beta, float* logits_dev, float* lse_dev, int32_t* counts_dev, float* prob_dev,
+                    float* loss_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of moe_router_loss's loss[0], and of whatever used the routing
+ * weights, with respect to X, W_router and bias. With f_e = counts[e] / (K N)
+ * (the counts have no gradient) and w the routing weights (the softmax over the
+ * token's K winning logits, as moe_route writes them),
+ *   dl_te = gloss p_te (alpha E / N (f_e - sum_j f_j p_tj) + 2 beta / N lse_t)
+ *         + sum over slots k with topk_idx = e of w_k (gw_k - sum_j w_j gw_j)
+ *   dX = dl W_router, dW_router = dl^T X, dbias = sum_t dl
+ * for live tokens; a token that is not live has dl = 0, a zero row of dX, and
+ * its X is not used.
+ *   logits_dev, lse_dev   as moe_router_loss wrote them
+ *   counts_dev  as it wrote them, or their sum over a data-parallel group
+ *   gw_dev      [T][K] fp32 gradient of the routing weights, or NULL (zeros);
+ *               slots whose id is outside [0, E) are left out of w
+ *   gloss_dev   device fp32 scalar, the gradient of loss[0], or NULL (1)
+ *   dX_dev [T][H], dW_dev [E][H], dbias_dev [E]   fp32 (the gradients of a
+ *               mean over a batch fall below fp16's range), each may be NULL
+ * Products of exact fp32 parts accumulated in fp32, every sum in a fixed
+ * order. Workspace (the forward call's may be reused), limits and errors as
+ * above.
+ */
+int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_dev, const int32_t* topk_idx_dev,
+                         const uint8_t* mask_dev, const float* logits_dev, const float* lse_dev,
+                         const int32_t* counts_dev, int T, int H, int E, int K, float alpha, float beta,
+                         const float* gw_dev, const float* gloss_dev, float* dX_dev, float* dW_dev, float* dbias_dev,
+                         void* ws_dev, size_t ws_bytes, void* stream);
+
+/*
  * Commit bitwidth b for linear-block i (§3.1 and §3.3: the planner lowers or
  * raises q_i at a safe boundary; a reload raises q_i only once its pages are
  * GPU-resident). Validates 0 <= i < 2*(E+S), b in 3..8 and that planes 0..b-1

@@ -81,6 +81,10 @@ def lib() -> ctypes.CDLL:
             "moe_block_norm_grad_workspace_bytes": (_SZ, [_I, _I]),
             "moe_block_norm_grad": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _P, _F, _F, _P, _P, _P, _P, _P, _P, _P, _P,
                                          _SZ, _P]),
+            "moe_router_loss_workspace_bytes": (_SZ, [_I, _I, _I]),
+            "moe_router_loss": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+            "moe_router_loss_grad": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P,
+                                          _P, _SZ, _P]),
             "set_committed_bits": (_I, [_I, _I]),
             "mpb_committed_bytes": (ctypes.c_int64, [_P]),
             "mpb_get_committed_bits": (_I, [_I]),
@@ -300,6 +304,43 @@ def moe_block_norm_grad(o, y, x_dtype, gate, gamma_post, gamma_next, scale, eps,
                  a("dr_out", dr_out, xt, T, H), a("dx", dx, xt, T, H), a("dr", dr, xt, T, H),
                  a("do", d_o, _F32, T, H), dgp, a("dgamma_post", dgamma_post, _F32, H),
                  a("dgamma_next", dgamma_next, _F32, H), wsp, wsn)
+
+
+def _router_args(name, X, x_dtype, W_router, topk_idx, mask):
+    a = _Args(name, X)
+    xt = _xtype(name, x_dtype)
+    if X.dim() != 2 or W_router.dim() != 2 or topk_idx.dim() != 2:
+        a.fail("X is [T][H], W_router [E][H], topk_idx [T][K]", -2)
+    (T, H), E, K = X.shape, W_router.shape[0], topk_idx.shape[1]
+    if mask is not None and mask.dtype is torch.bool:
+        mask = mask.view(_U8)
+    return a, T, H, E, K, (a("X", X, xt, T, H), x_dtype, a("W_router", W_router, _F32, E, H)), (
+        a("topk_idx", topk_idx, _I32, T, K), a("mask", mask, _U8, T))
+
+
+def moe_router_loss_workspace_bytes(T, H, E) -> int:
+    return lib().moe_router_loss_workspace_bytes(T, H, E)
+
+
+def moe_router_loss(X, x_dtype, W_router, bias, topk_idx, mask, alpha, beta, logits, lse, counts, prob, loss, ws,
+                    stream=None):
+    """Balance and z loss of a batch with the per-expert counts; mask: None or [T] uint8 or bool, 0 for padding."""
+    a, T, H, E, K, head, ids = _router_args("moe_router_loss", X, x_dtype, W_router, topk_idx, mask)
+    return a.run(lib().moe_router_loss, stream, *head, a("bias", bias, _F32, E), *ids, T, H, E, K, alpha, beta,
+                 a("logits", logits, _F32, T, E), a("lse", lse, _F32, T), a("counts", counts, _I32, E + 1),
+                 a("prob", prob, _F32, E), a("loss", loss, _F32, 3), *a.bytes(ws))
+
+
+def moe_router_loss_grad(X, x_dtype, W_router, topk_idx, mask, logits, lse, counts, alpha, beta, gw, gloss, dX, dW,
+                         dbias, ws, stream=None):
+    """Gradients of the loss (times the scalar tensor gloss, if given) and of the routing weights (gw)."""
+    a, T, H, E, K, head, ids = _router_args("moe_router_loss_grad", X, x_dtype, W_router, topk_idx, mask)
+    if gloss is not None and gloss.dim():
+        gloss = gloss.reshape(())
+    return a.run(lib().moe_router_loss_grad, stream, *head, *ids, a("logits", logits, _F32, T, E),
+                 a("lse", lse, _F32, T), a("counts", counts, _I32, E + 1), T, H, E, K, alpha, beta,
+                 a("gw", gw, _F32, T, K), a("gloss", gloss, _F32), a("dX", dX, _F32, T, H),
+                 a("dW", dW, _F32, E, H), a("dbias", dbias, _F32, E), *a.bytes(ws))
 
 
 def set_committed_bits(i, b):

@@ -38,6 +38,41 @@ int check_norm(const std::string& n, int gate_kind, float scale, float eps) {
   return MPB_OK;
 }
 
+int check_router(const std::string& n, int x_dtype, int T, int H, int E, int K, float alpha, float beta) {
+  const int rc = check_rows(n, x_dtype, T, H);
+  if (rc) return rc;
+  if (E < 1 || E > 512) return fail(MPB_E_SHAPE, n + ": E must be in 1..512");
+  if (K < 1 || K > 16 || K > E) return fail(MPB_E_SHAPE, n + ": K must be in 1..min(E,16)");
+  if (!std::isfinite(alpha) || !std::isfinite(beta)) return fail(MPB_E_ARG, n + ": alpha and beta must be finite");
+  return MPB_OK;
+}
+
+int check_ws(const std::string& n, const void* ws, size_t bytes, size_t need) {
+  if (!ws) return fail(MPB_E_ARG, n + ": null workspace");
+  if (!aligned16(ws)) return fail(MPB_E_ARG, n + ": the workspace must be 16-byte aligned");
+  if (bytes < need) return fail(MPB_E_WS, n + ": workspace " + std::to_string(bytes) + " < " + std::to_string(need));
+  return MPB_OK;
+}
+
+mpb::RouterLossParams router_params(const void* X, const float* W, const int32_t* idx, const uint8_t* mask, int T, int H,
+                                    int E, int K, float alpha, float beta, void* ws_dev) {
+  const mpb::RouterLossWs w = mpb::router_loss_ws(T, H, E);
+  char* ws = (char*)ws_dev;
+  mpb::RouterLossParams p{};
+  p.X = X; p.W = W; p.idx = idx; p.mask = mask;
+  p.T = T; p.H = H; p.E = E; p.K = K; p.alpha = alpha; p.beta = beta;
+  p.part = (float*)(ws + w.part);
+  p.stat_f = (float*)(ws + w.stat_f);
+  p.stat_i = (int32_t*)(ws + w.stat_i);
+  p.dl_a = (uint16_t*)(ws + w.dl_a);
+  p.dl_t = (uint16_t*)(ws + w.dl_t);
+  p.w_t = (uint16_t*)(ws + w.w_t);
+  p.db_part = (float*)(ws + w.db_part);
+  p.dw_part = (float*)(ws + w.dw_part);
+  p.splits = w.splits; p.groups = w.groups; p.chunks = w.chunks; p.Tp = w.Tp; p.Ep = w.Ep;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -118,6 +153,64 @@ int moe_block_norm_grad(const float* o_dev, const void* y_dev, int x_dtype, int 
   return MPB_OK;
 } catch (...) {
   return mpb::set_error(MPB_E_HIP, "moe_block_norm_grad: unexpected exception");
+}
+
+size_t moe_router_loss_workspace_bytes(int T, int H, int E) {
+  if (T < 0 || T > (1 << 20) || H <= 0 || H % 64 || H > 65536 || E < 1 || E > 512) return 0;
+  return mpb::router_loss_ws(T, H, E).total;
+}
+
+int moe_router_loss(const void* X_dev, int x_dtype, const float* W_router_dev, const float* bias_dev,
+                    const int32_t* topk_idx_dev, const uint8_t* mask_dev, int T, int H, int E, int K, float alpha,
+                    float beta, float* logits_dev, float* lse_dev, int32_t* counts_dev, float* prob_dev,
+                    float* loss_dev, void* ws_dev, size_t ws_bytes, void* stream) try {
+  const std::string n("moe_router_loss");
+  int rc = check_router(n, x_dtype, T, H, E, K, alpha, beta);
+  if (rc) return rc;
+  if (!counts_dev || !prob_dev || !loss_dev) return fail(MPB_E_ARG, n + ": null pointer");
+  if (T > 0 && (!X_dev || !W_router_dev || !topk_idx_dev || !logits_dev || !lse_dev))
+    return fail(MPB_E_ARG, n + ": null pointer");
+  if (!all_aligned16(X_dev, W_router_dev)) return fail(MPB_E_ARG, n + ": rows must be 16-byte aligned");
+  rc = check_ws(n, ws_dev, ws_bytes, moe_router_loss_workspace_bytes(T, H, E));
+  if (rc) return rc;
+  mpb::RouterLossParams p = router_params(X_dev, W_router_dev, topk_idx_dev, mask_dev, T, H, E, K, alpha, beta, ws_dev);
+  p.bias = bias_dev;
+  p.logits = logits_dev; p.lse = lse_dev; p.counts = counts_dev; p.prob = prob_dev; p.loss = loss_dev;
+  const hipError_t e = mpb::launch_router_loss(p, x_dtype == MPB_BF16, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_router_loss");
+  return MPB_OK;
+} catch (...) {
+  return mpb::set_error(MPB_E_HIP, "moe_router_loss: unexpected exception");
+}
+
+int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_dev, const int32_t* topk_idx_dev,
+                         const uint8_t* mask_dev, const float* logits_dev, const float* lse_dev,
+                         const int32_t* counts_dev, int T, int H, int E, int K, float alpha, float beta,
+                         const float* gw_dev, const float* gloss_dev, float* dX_dev, float* dW_dev, float* dbias_dev,
+                         void* ws_dev, size_t ws_bytes, void* stream) try {
+  const std::string n("moe_router_loss_grad");
+  int rc = check_router(n, x_dtype, T, H, E, K, alpha, beta);
+  if (rc) return rc;
+  if (T > 0 && (!logits_dev || !lse_dev || !counts_dev || (dX_dev && !W_router_dev) || (dW_dev && !X_dev) ||
+                (gw_dev && !topk_idx_dev)))
+    return fail(MPB_E_ARG, n + ": null pointer");
+  if (!all_aligned16(X_dev, W_router_dev, dX_dev, dW_dev)) return fail(MPB_E_ARG, n + ": rows must be 16-byte aligned");
+  if (!dX_dev && !dW_dev && !dbias_dev) {
+    if (T > 0) return fail(MPB_E_ARG, n + ": no gradient asked for");
+    return MPB_OK;
+  }
+  rc = check_ws(n, ws_dev, ws_bytes, moe_router_loss_workspace_bytes(T, H, E));
+  if (rc) return rc;
+  mpb::RouterLossParams p = router_params(X_dev, W_router_dev, topk_idx_dev, mask_dev, T, H, E, K, alpha, beta, ws_dev);
+  p.logits = const_cast<float*>(logits_dev);
+  p.lse = const_cast<float*>(lse_dev);
+  p.counts = const_cast<int32_t*>(counts_dev);
+  p.gw = gw_dev; p.gloss = gloss_dev; p.dX = T > 0 ? dX_dev : nullptr; p.dW = dW_dev; p.dbias = dbias_dev;
+  const hipError_t e = mpb::launch_router_loss_grad(p, x_dtype == MPB_BF16, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_router_loss_grad");
+  return MPB_OK;
+} catch (...) {
+  return mpb::set_error(MPB_E_HIP, "moe_router_loss_grad: unexpected exception");
 }
 
 }  // extern "C"

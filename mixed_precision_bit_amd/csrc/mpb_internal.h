@@ -247,6 +247,47 @@ hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s)
 int block_norm_grad_groups(int T, int H);
 hipError_t launch_block_norm_grad(const BlockNormGradParams& p, bool bf16, hipStream_t s);
 
+// Router losses and their gradients (k_router_loss.hip).
+struct RouterLossParams {
+  const void* X;         // [T][H] activations
+  const float* W;        // [E][H]
+  const float* bias;     // [E] or null
+  const int32_t* idx;    // [T][K]
+  const uint8_t* mask;   // [T] or null
+  int T, H, E, K;
+  float alpha, beta;
+  float* logits;         // [T][E]
+  float* lse;            // [T]
+  int32_t* counts;       // [E + 1]
+  float* prob;           // [E]
+  float* loss;           // [3]
+  // backward
+  const float* gw;       // [T][K] or null
+  const float* gloss;    // scalar or null (1)
+  float* dX;             // [T][H] or null
+  float* dW;             // [E][H] or null
+  float* dbias;          // [E] or null
+  // workspace
+  float* part;           // [splits][T][E] partial logits
+  float* stat_f;         // [groups][E + 1] sums of p, sum of lse^2
+  int32_t* stat_i;       // [groups][E + 1] counts, live tokens
+  uint16_t* dl_a;        // operand fragments, see the kernels
+  uint16_t* dl_t;
+  uint16_t* w_t;
+  float* db_part;        // [Tp / 32][E]
+  float* dw_part;        // [chunks][E][H]
+  int splits, groups, chunks, Tp, Ep;
+};
+// Regions of the workspace (the forward and the backward pass each use all of
+// it) and the launch shapes they go with, from the sizes only.
+struct RouterLossWs {
+  size_t part, stat_f, stat_i, dl_a, dl_t, w_t, db_part, dw_part, total;
+  int splits, groups, chunks, Tp, Ep;  // Tp, Ep: T and E rounded up to 64
+};
+RouterLossWs router_loss_ws(int T, int H, int E);
+hipError_t launch_router_loss(const RouterLossParams& p, bool bf16, hipStream_t s);
+hipError_t launch_router_loss_grad(const RouterLossParams& p, bool bf16, hipStream_t s);
+
 // Records msg as the calling thread's last error and returns code.
 int set_error(int code, const char* msg);
 // Checks a layer geometry against the ranges the library supports; on failure
