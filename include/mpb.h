@@ -367,6 +367,36 @@ int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_d
                          void* ws_dev, size_t ws_bytes, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a projection that all of them
+ * share: for token t with adapter a = adapter_dev[t],
+ *   out_t = base_t + scales[a] * B_a (A_a x_t)
+ * and out_t = base_t for a token whose id is outside [0, n) (none).
+ *   X_dev       [T][Kd] x_dtype
+ *   A_dev       [n][R][Kd] x_dtype, B_dev [n][N][R] x_dtype: n adapters stacked
+ *               for rank up to R. Rows of A and columns of B past an adapter's
+ *               own rank are not used, whatever they hold.
+ *   ranks_dev   [n] int32 or NULL (all R); values are clamped to 0..R, an
+ *               adapter of rank 0 adds nothing
+ *   scales_dev  [n] fp32 or NULL (1)
+ *   adapter_dev [T] int32, in any order
+ *   base_dev    [T][N] fp32, e.g. what moe_ffn wrote, or NULL (zeros)
+ *   out_dev     [T][N] fp32; may be base_dev (tokens without an adapter are
+ *               then not touched)
+ * Tokens are gathered by adapter on the device, so ids may change from call to
+ * call (also under graph replay). Products are exact, sums fp32 in a fixed
+ * order (deterministic), and A_a x_t is not rounded below fp32. Needs Kd and N
+ * multiples of 64 (Kd <= 65536, N <= 131072), R a multiple of 8 in 8..128, n in
+ * 1..4096, T <= 2^20, 16-byte aligned rows; T == 0 is a no-op. ws_dev (16-byte
+ * aligned): at least moe_adapters_workspace_bytes(T, Kd, n, R) bytes, contents
+ * not preserved; calls that may overlap need a workspace each. Errors:
+ * MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS, MPB_E_HIP. Does not need mpb_init.
+ */
+size_t moe_adapters_workspace_bytes(int T, int Kd, int n, int R);
+int moe_adapters(const void* X_dev, int x_dtype, int T, int Kd, const void* A_dev, const void* B_dev,
+                 const int32_t* ranks_dev, const float* scales_dev, int n, int R, int N, const int32_t* adapter_dev,
+                 const float* base_dev, float* out_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/*
  * Commit bitwidth b for linear-block i (§3.1 and §3.3: the planner lowers or
  * raises q_i at a safe boundary; a reload raises q_i only once its pages are
  * GPU-resident). Validates 0 <= i < 2*(E+S), b in 3..8 and that planes 0..b-1

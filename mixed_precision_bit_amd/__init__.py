@@ -4,7 +4,8 @@ The compute path is libmpb.so (HIP kernels for gfx950 behind the C ABI in
 include/mpb.h); this package holds its build script and a thin ctypes binding.
 """
 from . import _lib  # noqa: F401
-from ._lib import (MPB_GATE_FULL, MPB_GATE_NONE, MPB_GATE_TOKEN, moe_block_norm, moe_block_norm_grad,  # noqa: F401
+from ._lib import (MPB_GATE_FULL, MPB_GATE_NONE, MPB_GATE_TOKEN, moe_adapters, moe_adapters_workspace_bytes,  # noqa: F401
+                   moe_block_norm, moe_block_norm_grad,
                    moe_block_norm_grad_workspace_bytes, moe_router_loss, moe_router_loss_grad,
                    moe_router_loss_workspace_bytes)
 from ._lib import (MPB_BF16, MPB_F16, moe_fused, moe_fused_workspace_bytes, MPB_PAGE_CPU, MPB_PAGE_GPU, MPB_PAGE_IN_TRANSFER, MpbError, moe_ffn, moe_ffn_workspace_bytes, moe_route,  # noqa: F401

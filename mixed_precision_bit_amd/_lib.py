@@ -85,6 +85,8 @@ def lib() -> ctypes.CDLL:
             "moe_router_loss": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _SZ, _P]),
             "moe_router_loss_grad": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P,
                                           _P, _SZ, _P]),
+            "moe_adapters_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+            "moe_adapters": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
             "set_committed_bits": (_I, [_I, _I]),
             "mpb_committed_bytes": (ctypes.c_int64, [_P]),
             "mpb_get_committed_bits": (_I, [_I]),
@@ -341,6 +343,22 @@ def moe_router_loss_grad(X, x_dtype, W_router, topk_idx, mask, logits, lse, coun
                  a("lse", lse, _F32, T), a("counts", counts, _I32, E + 1), T, H, E, K, alpha, beta,
                  a("gw", gw, _F32, T, K), a("gloss", gloss, _F32), a("dX", dX, _F32, T, H),
                  a("dW", dW, _F32, E, H), a("dbias", dbias, _F32, E), *a.bytes(ws))
+
+
+def moe_adapters_workspace_bytes(T, Kd, n, R) -> int:
+    return lib().moe_adapters_workspace_bytes(T, Kd, n, R)
+
+
+def moe_adapters(X, x_dtype, A, B, ranks, scales, adapter, base, out, ws, stream=None):
+    """out = base + scales[a] * B[a] (A[a] x) with a = adapter[t] per token; A [n][R][Kd], B [n][N][R]."""
+    a = _Args("moe_adapters", X)
+    xt = _xtype(a.name, x_dtype)
+    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        a.fail("X is [T][Kd], A [n][R][Kd], B [n][N][R]", -2)
+    (T, Kd), (n, R, _), N = X.shape, A.shape, B.shape[1]
+    return a.run(lib().moe_adapters, stream, a("X", X, xt, T, Kd), x_dtype, T, Kd, a("A", A, xt, n, R, Kd),
+                 a("B", B, xt, n, N, R), a("ranks", ranks, _I32, n), a("scales", scales, _F32, n), n, R, N,
+                 a("adapter", adapter, _I32, T), a("base", base, _F32, T, N), a("out", out, _F32, T, N), *a.bytes(ws))
 
 
 def set_committed_bits(i, b):

@@ -1,0 +1,355 @@
+// Low-rank adapters of many requests: out_t = base_t + s_a B_a (A_a x_t) for
+// the adapter a of token t, one batch holding tokens of many adapters.
+//
+// Tokens are gathered by adapter into tiles of up to 16 MT tokens of one
+// adapter, so that an adapter's weights are read once per tile:
+//   k_plan     (batches above kScanT) counting sort of the tokens by adapter,
+//              and the tile list; smaller batches are gathered by every
+//              workgroup for itself, which costs less than a launch
+//   k_shrink   z = A_a x for a tile over one range of Kd; the partial sums go
+//              to z [range][T][R] in fp32
+//   k_expand   z's ranges added in order, scaled, and multiplied by B_a; base
+//              is read and out written once
+// Both products run on the matrix cores with exact products and fp32
+// accumulation: x and the weights as they are, z (fp32) as three bf16 parts
+// (24 bits; an fp16 B_a as two), so that nothing between the two products is
+// rounded below fp32. A token's arithmetic does not depend on the tile it is
+// in: its results are the same in any batch of the same launch shape.
+// Rows past an adapter's rank are never read, columns past it never used.
+#include "k_block_common.h"
+#include "mpb.h"
+#include "mpb_internal.h"
+
+namespace mpb {
+
+namespace {
+
+__device__ __forceinline__ acc4 mfma16(bx8 a, bx8 b, acc4 c) { return mfma(a, b, c); }
+__device__ __forceinline__ acc4 mfma16(hx8 a, hx8 b, acc4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Group of a token: its adapter, or n for none.
+__device__ __forceinline__ int group_of(const AdapterParams& p, int t) {
+  const int a = p.adapter[t];
+  return a >= 0 && a < p.n ? a : p.n;
+}
+
+__device__ __forceinline__ int rank_of(const AdapterParams& p, int a) {
+  if (a >= p.n) return 0;
+  const int r = p.ranks ? p.ranks[a] : p.R;
+  return r < 0 ? 0 : r < p.R ? r : p.R;
+}
+
+// The tile of a workgroup: its adapter and tokens (toks[i] = -1 past its end).
+// Returns the adapter (n: none), or -1 if there is no such tile.
+struct TileLds {
+  int ids[kAdapterScanT];
+  int toks[64];
+  int waves[kAdapterScanT / 64];
+  int adapter;
+};
+
+template <int ROWS>
+__device__ __forceinline__ int find_tile(const AdapterParams& p, int tile, TileLds& s) {
+  const int tid = threadIdx.x;
+  if (p.perm) {
+    if (tile >= p.tiles[0]) return -1;
+    const int* d = p.tiles + 4 + 4 * (size_t)tile;  // adapter, first, count
+    if (tid < ROWS) s.toks[tid] = tid < d[2] ? p.perm[d[1] + tid] : -1;
+    __syncthreads();
+    return d[0];
+  }
+  // one thread per token: pos = earlier tokens of the same group; every ROWS-th
+  // token of a group starts a tile, tiles numbered by their first token
+  const int id = tid < p.T ? group_of(p, tid) : -1;
+  s.ids[tid] = id;
+  if (tid < 64) s.toks[tid] = -1;
+  if (tid == 0) s.adapter = -1;
+  __syncthreads();
+  int pos = 0;
+  for (int i = 0; i < p.T; ++i) pos += i < tid && s.ids[i] == id ? 1 : 0;
+  const bool first = id >= 0 && pos % ROWS == 0;
+  const unsigned long long m = __ballot(first);
+  if ((tid & 63) == 0) s.waves[tid >> 6] = __popcll(m);
+  __syncthreads();
+  int before = __popcll(m & ((1ull << (tid & 63)) - 1));
+  for (int w = 0; w < (tid >> 6); ++w) before += s.waves[w];
+  if (first && before == tile) s.adapter = id | (pos / ROWS) << 16;
+  __syncthreads();
+  const int found = s.adapter;
+  if (found < 0) return -1;
+  const int a = found & 0xffff, part = found >> 16;
+  if (id == a && pos / ROWS == part) s.toks[pos % ROWS] = tid;
+  __syncthreads();
+  return a;
+}
+
+// Counting sort of the tokens by group and the tile list, one workgroup. Lanes
+// of one wave with the same group take their places together (runs of one
+// request's tokens would otherwise meet at one counter).
+__global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
+  __shared__ int cnt[kAdapterMaxN + 1];
+  __shared__ int wsum[2][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = p.n + 1;
+  for (int i = tid; i < G; i += 1024) cnt[i] = 0;
+  __syncthreads();
+  const int T64 = (p.T + 63) / 64 * 64;
+  auto take = [&](int id) {  // this lane's place among the tokens of its group
+    int at = 0;
+    unsigned long long todo = __ballot(id >= 0);
+    while (todo) {
+      const int lead = __ffsll(todo) - 1, g = __shfl(id, lead);
+      const unsigned long long same = __ballot(id == g);
+      int base = 0;
+      if (lane == lead) base = atomicAdd(&cnt[g], __popcll(same));
+      base = __shfl(base, lead);
+      if (id == g) at = base + __popcll(same & ((1ull << lane) - 1));
+      todo &= ~same;
+    }
+    return at;
+  };
+  for (int t = tid; t < T64; t += 1024) take(t < p.T ? group_of(p, t) : -1);
+  __syncthreads();
+  // first token and first tile of each group: a thread scans a run of groups
+  const int per = (G + 1023) / 1024, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
+  int c = 0, n = 0;
+  for (int g = g0; g < g1; ++g) {
+    c += cnt[g];
+    n += (cnt[g] + rows - 1) / rows;
+  }
+  int ci = c, ni = n;  // inclusive over the wave
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int a = __shfl_up(ci, d), b = __shfl_up(ni, d);
+    if (lane >= d) {
+      ci += a;
+      ni += b;
+    }
+  }
+  if (lane == 63) {
+    wsum[0][wave] = ci;
+    wsum[1][wave] = ni;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    ci += wsum[0][w];
+    ni += wsum[1][w];
+  }
+  int first = ci - c, tile = ni - n;
+  for (int g = g0; g < g1; ++g) {
+    const int k = cnt[g];
+    for (int i = 0; i < k; i += rows, ++tile) {
+      int* d = p.tiles + 4 + 4 * (size_t)tile;
+      d[0] = g;
+      d[1] = first + i;
+      d[2] = k - i < rows ? k - i : rows;
+    }
+    cnt[g] = first;
+    first += k;
+  }
+  if (tid == 1023) p.tiles[0] = ni;
+  __syncthreads();
+  for (int t = tid; t < T64; t += 1024) {
+    const int id = t < p.T ? group_of(p, t) : -1;
+    const int at = take(id);
+    if (id >= 0) p.perm[at] = t;
+  }
+}
+
+// z of one tile over one range of Kd. The four waves take steps of 32 in turn;
+// their sums meet in LDS in wave order. RT: rank tiles of 16.
+template <class D, int MT, int RT>
+__global__ __launch_bounds__(256) void k_shrink(AdapterParams p) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
+  __shared__ TileLds tl;
+  __shared__ float sum[16 * MT][16 * RT + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+  const int a = find_tile<16 * MT>(p, blockIdx.x, tl);
+  if (a < 0) return;
+  const int rank = rank_of(p, a);
+  if (rank == 0) return;
+  const int steps = p.Kd / 32, s0 = (int)((long long)steps * blockIdx.y / gridDim.y),
+            s1 = (int)((long long)steps * (blockIdx.y + 1) / gridDim.y);
+  int tok[MT];
+  const elem* x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    tok[m] = tl.toks[16 * m + n];
+    x[m] = (const elem*)p.X + (size_t)(tok[m] < 0 ? 0 : tok[m]) * p.Kd + 8 * g;
+  }
+  const elem* w = (const elem*)p.A + ((size_t)a * p.R + n) * p.Kd + 8 * g;
+  acc4 acc[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] = (acc4)(0.0f);
+#pragma unroll 2
+  for (int s = s0 + wave; s < s1; s += 4) {
+    vec xv[MT], av[RT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      xv[m] = (vec)(elem)0.0f;
+      if (tok[m] >= 0) xv[m] = *(const vec*)(x[m] + 32 * s);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      av[r] = (vec)(elem)0.0f;
+      if (16 * r + n < rank) av[r] = *(const vec*)(w + (size_t)(16 * r) * p.Kd + 32 * s);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[m][r] = mfma16(xv[m], av[r], acc[m][r]);
+  }
+  for (int v = 0; v < 4; ++v) {
+    if (wave == v) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* at = &sum[16 * m + 4 * g + i][16 * r + n];
+            *at = v ? *at + acc[m][r][i] : acc[m][r][i];
+          }
+    }
+    __syncthreads();
+  }
+  float* z = p.z + (size_t)blockIdx.y * p.T * p.R;
+  for (int i = tid; i < 16 * MT * 16 * RT; i += 256) {
+    const int row = i / (16 * RT), r = i % (16 * RT), t = tl.toks[row];
+    if (t >= 0 && r < p.R) z[(size_t)t * p.R + r] = sum[row][r];
+  }
+}
+
+// out of one tile: a wave holds 16 tokens and 64 columns at a time. With MT = 4
+// the waves take the tile's four rows of 16 tokens, with MT = 1 the columns in
+// turn. RK: rank tiles of 32. The columns are the products' rows, so that a
+// lane ends with four consecutive columns of one token.
+constexpr int kExpandCols = 256;
+
+template <class D, int MT, int RK>
+__global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
+  constexpr int NP = Parts<D>::N;
+  __shared__ TileLds tl;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+  const int a = find_tile<16 * MT>(p, blockIdx.x, tl);
+  if (a < 0) return;
+  const int rank = rank_of(p, a);
+  if (rank == 0 && p.base == p.out) return;
+  if (MT == 4 && tl.toks[16 * wave] < 0) return;  // this wave's rows are past the tile's end
+  const int t = tl.toks[(MT == 4 ? 16 * wave : 0) + n];
+  bx8 z[RK][3];
+  if (rank > 0) {
+    const float scale = p.scales ? p.scales[a] : 1.0f;
+#pragma unroll
+    for (int k = 0; k < RK; ++k) {
+      fx8 v = (fx8)(0.0f);
+      const int r = 32 * k + 8 * g;
+      if (t >= 0 && r < rank) {
+        const float* src = p.z + (size_t)t * p.R + r;
+        for (int s = 0; s < p.ranges; ++s) v += load8(src + (size_t)s * p.T * p.R);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r + i < rank ? v[i] * scale : 0.0f;
+      }
+      cut<3>(v, z[k]);
+    }
+  }
+  const int c1 = (int)(blockIdx.y + 1) * kExpandCols < p.N ? (int)(blockIdx.y + 1) * kExpandCols : p.N;
+  for (int c = blockIdx.y * kExpandCols + (MT == 4 ? 0 : 64 * wave); c < c1; c += MT == 4 ? 64 : 256) {
+    acc4 acc[4];
+    const size_t at = (size_t)(t < 0 ? 0 : t) * p.N + c + 4 * g;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[j] = (acc4)(0.0f);
+      if (p.base && t >= 0) acc[j] = *(const acc4*)(p.base + at + 16 * j);
+    }
+    if (rank > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc4 d = (acc4)(0.0f);
+        const elem* b = (const elem*)p.B + ((size_t)a * p.N + c + 16 * j + n) * p.R + 8 * g;
+#pragma unroll
+        for (int k = 0; k < RK; ++k) {
+          vec v = (vec)(elem)0.0f;
+          const int r = 32 * k + 8 * g;
+          if (r < rank) {
+            v = *(const vec*)(b + 32 * k);
+            if (r + 8 > rank) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = r + i < rank ? v[i] : (elem)0.0f;
+            }
+          }
+          bx8 q[NP];
+          Parts<D>::of(v, q);
+#pragma unroll
+          for (int u = NP - 1; u >= 0; --u)
+#pragma unroll
+            for (int i = 2 - u; i >= 0; --i) d = mfma(q[u], z[k][i], d);
+        }
+        acc[j] += d;
+      }
+    }
+    if (t >= 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(acc4*)(p.out + at + 16 * j) = acc[j];
+    }
+  }
+}
+
+template <class D, int MT>
+void shrink_expand(const AdapterParams& p, int tiles, hipStream_t s) {
+  const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + kExpandCols - 1) / kExpandCols);
+  if (p.R <= 16) k_shrink<D, MT, 1><<<gs, 256, 0, s>>>(p);
+  else if (p.R <= 32) k_shrink<D, MT, 2><<<gs, 256, 0, s>>>(p);
+  else if (p.R <= 64) k_shrink<D, MT, 4><<<gs, 256, 0, s>>>(p);
+  else k_shrink<D, MT, 8><<<gs, 256, 0, s>>>(p);
+  if (p.R <= 32) k_expand<D, MT, 1><<<ge, 256, 0, s>>>(p);
+  else if (p.R <= 64) k_expand<D, MT, 2><<<ge, 256, 0, s>>>(p);
+  else k_expand<D, MT, 4><<<ge, 256, 0, s>>>(p);
+}
+
+}  // namespace
+
+AdapterWs adapter_ws(int T, int Kd, int n, int R) {
+  AdapterWs w{};
+  w.scan = T <= kAdapterScanT;
+  // 64-token tiles where adapters hold that many tokens on average, else 16
+  w.mt = !w.scan && T / (n + 1) >= 32 ? 4 : 1;
+  const int rows = 16 * w.mt;
+  w.max_tiles = (n + 1 < T ? n + 1 : T) + T / rows;
+  // ranges of Kd: about 512 workgroups, at least 4 steps of 32 (one per wave) each
+  w.ranges = w.max_tiles > 0 ? 512 / w.max_tiles : 1;
+  if (w.ranges > Kd / 128) w.ranges = Kd / 128;
+  if (w.ranges > 16) w.ranges = 16;
+  if (w.ranges < 1) w.ranges = 1;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) & ~(size_t)255;
+    return at;
+  };
+  w.z = take((size_t)w.ranges * T * R * 4);
+  w.perm = take(w.scan ? 0 : (size_t)T * 4);
+  w.tiles = take(w.scan ? 0 : ((size_t)w.max_tiles + 1) * 16);
+  w.total = off < 256 ? 256 : off;
+  return w;
+}
+
+hipError_t launch_adapters(const AdapterParams& p, const AdapterWs& w, bool bf16, hipStream_t s) {
+  if (!w.scan) k_plan<<<1, 1024, 0, s>>>(p, 16 * w.mt);
+  if (bf16) {
+    if (w.mt == 4) shrink_expand<BF16, 4>(p, w.max_tiles, s);
+    else shrink_expand<BF16, 1>(p, w.max_tiles, s);
+  } else {
+    if (w.mt == 4) shrink_expand<F16, 4>(p, w.max_tiles, s);
+    else shrink_expand<F16, 1>(p, w.max_tiles, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mpb

@@ -25,55 +25,6 @@ namespace mpb {
 
 namespace {
 
-typedef unsigned int ux4 __attribute__((ext_vector_type(4)));
-typedef float acc4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ acc4 mfma(bx8 a, bx8 b, acc4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// Cuts 8 fp32 values into N bf16 parts each: part i holds the next 8 bits, cut
-// off by truncation, so x - part is exact. A part of inf or nan leaves zeros
-// (inf - inf would turn an infinite sum into nan).
-template <int N>
-__device__ __forceinline__ void cut(fx8 x, bx8 (&part)[N]) {
-  if (N > 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __builtin_canonicalizef(x[i]);  // a quiet nan stays one when cut
-  }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    ux4 u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned a = __float_as_uint(x[2 * i]), b = __float_as_uint(x[2 * i + 1]);
-      u[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-      if (n + 1 < N) {
-        x[2 * i] -= __uint_as_float(a & 0xffff0000u);
-        x[2 * i + 1] -= __uint_as_float(b & 0xffff0000u);
-      }
-    }
-    part[n] = __builtin_bit_cast(bx8, u);
-    if (n == 0 && N > 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] : 0.0f;
-    }
-  }
-}
-
-template <class D>
-struct Parts;  // parts of an activation
-template <>
-struct Parts<BF16> {
-  static constexpr int N = 1;
-  static __device__ __forceinline__ void of(bx8 v, bx8 (&p)[1]) { p[0] = v; }
-};
-template <>
-struct Parts<F16> {
-  static constexpr int N = 2;
-  static __device__ __forceinline__ void of(hx8 v, bx8 (&p)[2]) { cut<2>(widen<F16>(v), p); }
-};
-
 __device__ __forceinline__ bool is_live(const RouterLossParams& p, int t) {
   return t < p.T && (!p.mask || p.mask[t]);
 }

@@ -213,4 +213,38 @@ int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_d
   return mpb::set_error(MPB_E_HIP, "moe_router_loss_grad: unexpected exception");
 }
 
+size_t moe_adapters_workspace_bytes(int T, int Kd, int n, int R) {
+  if (T < 0 || T > (1 << 20) || Kd <= 0 || Kd % 64 || Kd > 65536 || n < 1 || n > mpb::kAdapterMaxN || R < 8 || R > 128 ||
+      R % 8)
+    return 0;
+  return mpb::adapter_ws(T, Kd, n, R).total;
+}
+
+int moe_adapters(const void* X_dev, int x_dtype, int T, int Kd, const void* A_dev, const void* B_dev,
+                 const int32_t* ranks_dev, const float* scales_dev, int n, int R, int N, const int32_t* adapter_dev,
+                 const float* base_dev, float* out_dev, void* ws_dev, size_t ws_bytes, void* stream) try {
+  const std::string nm("moe_adapters");
+  int rc = check_rows(nm, x_dtype, T, Kd);
+  if (rc) return rc;
+  if (N <= 0 || N % 64 || N > 131072) return fail(MPB_E_SHAPE, nm + ": N must be a multiple of 64 in 64..131072");
+  if (n < 1 || n > mpb::kAdapterMaxN) return fail(MPB_E_SHAPE, nm + ": n must be in 1..4096");
+  if (R < 8 || R > 128 || R % 8) return fail(MPB_E_SHAPE, nm + ": R must be a multiple of 8 in 8..128");
+  if (T == 0) return MPB_OK;
+  if (!X_dev || !A_dev || !B_dev || !adapter_dev || !out_dev) return fail(MPB_E_ARG, nm + ": null pointer");
+  if (!all_aligned16(X_dev, A_dev, B_dev, base_dev, out_dev))
+    return fail(MPB_E_ARG, nm + ": rows must be 16-byte aligned");
+  const mpb::AdapterWs w = mpb::adapter_ws(T, Kd, n, R);
+  rc = check_ws(nm, ws_dev, ws_bytes, w.total);
+  if (rc) return rc;
+  char* ws = (char*)ws_dev;
+  mpb::AdapterParams p{X_dev, A_dev, B_dev, ranks_dev, scales_dev, adapter_dev, base_dev, out_dev, T, Kd, N, n, R,
+                       (float*)(ws + w.z), w.scan ? nullptr : (int32_t*)(ws + w.perm),
+                       w.scan ? nullptr : (int32_t*)(ws + w.tiles), w.ranges};
+  const hipError_t e = mpb::launch_adapters(p, w, x_dtype == MPB_BF16, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_adapters");
+  return MPB_OK;
+} catch (...) {
+  return mpb::set_error(MPB_E_HIP, "moe_adapters: unexpected exception");
+}
+
 }  // extern "C"

@@ -288,6 +288,32 @@ RouterLossWs router_loss_ws(int T, int H, int E);
 hipError_t launch_router_loss(const RouterLossParams& p, bool bf16, hipStream_t s);
 hipError_t launch_router_loss_grad(const RouterLossParams& p, bool bf16, hipStream_t s);
 
+// Low-rank adapters (k_adapters.hip).
+constexpr int kAdapterScanT = 256;   // batches up to this are gathered without a plan launch
+constexpr int kAdapterMaxN = 4096;   // most adapters of a call (the plan's counters in LDS)
+struct AdapterParams {
+  const void* X;           // [T][Kd]
+  const void* A;           // [n][R][Kd]
+  const void* B;           // [n][N][R]
+  const int32_t* ranks;    // [n] or null (R)
+  const float* scales;     // [n] or null (1)
+  const int32_t* adapter;  // [T]
+  const float* base;       // [T][N] or null (zeros)
+  float* out;              // [T][N]
+  int T, Kd, N, n, R;
+  float* z;                // [ranges][T][R]
+  int32_t* perm;           // [T] tokens by adapter, or null (no plan)
+  int32_t* tiles;          // count, then 4 words per tile: adapter, first, tokens
+  int ranges;
+};
+struct AdapterWs {
+  size_t z, perm, tiles, total;
+  int ranges, max_tiles, mt;
+  bool scan;
+};
+AdapterWs adapter_ws(int T, int Kd, int n, int R);
+hipError_t launch_adapters(const AdapterParams& p, const AdapterWs& w, bool bf16, hipStream_t s);
+
 // Records msg as the calling thread's last error and returns code.
 int set_error(int code, const char* msg);
 // Checks a layer geometry against the ranges the library supports; on failure
