@@ -81,14 +81,10 @@ __device__ __forceinline__ acc4 mfma(bx8 a, bx8 b, acc4 c) {
 }
 
 // Cuts 8 fp32 values into N bf16 parts each: part i holds the next 8 bits, cut
-// off by truncation, so x - part is exact. A part of inf or nan leaves zeros
-// (inf - inf would turn an infinite sum into nan).
+// off by truncation, so x - part is exact. What is not finite stays so: inf
+// leaves nan for its second part (and a nan whose first part reads as inf, too).
 template <int N>
 __device__ __forceinline__ void cut(fx8 x, bx8 (&part)[N]) {
-  if (N > 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __builtin_canonicalizef(x[i]);  // a quiet nan stays one when cut
-  }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     ux4 u;
@@ -102,10 +98,6 @@ __device__ __forceinline__ void cut(fx8 x, bx8 (&part)[N]) {
       }
     }
     part[n] = __builtin_bit_cast(bx8, u);
-    if (n == 0 && N > 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] : 0.0f;
-    }
   }
 }
 

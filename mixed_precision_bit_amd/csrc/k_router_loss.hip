@@ -29,89 +29,115 @@ __device__ __forceinline__ bool is_live(const RouterLossParams& p, int t) {
   return t < p.T && (!p.mask || p.mask[t]);
 }
 
-// Whether token t takes part in the loss, after the forward pass.
-__device__ __forceinline__ bool is_on(const RouterLossParams& p, int t) {
-  return is_live(p, t) && !(p.lse[t] == -INFINITY);
+// Workgroups go round the 8 XCDs by their linear index. The n expert tiles that
+// read the same activations are given to one XCD, one after the other, so that
+// its L2 serves all but the first: splits linear index b of `count * n` into
+// (tile, rest).
+__device__ __forceinline__ void xcd_pairs(int b, int n, int count, int& tile, int& rest) {
+  const int full = count / 8 * 8 * n;
+  if (b < full) {
+    tile = (b >> 3) % n;
+    rest = (b >> 3) / n * 8 + (b & 7);
+  } else {  // the last count % 8
+    tile = (b - full) % n;
+    rest = full / n + (b - full) / n;
+  }
 }
 
 // ---------------------------------------------------------------- logits
-// 64 tokens x 64 experts x one range of H per workgroup of 4 waves; a wave
-// holds 16 experts, whose W it reads straight into fragments and cuts there
-// (each W value is read by one wave of the workgroup); the tokens' activations
-// are staged in LDS for all four waves, 64 elements of H at a time, the next
-// stage's loads in flight during the products. Partial sums go to
-// part[range][T][E].
-constexpr int kLT = 64, kLE = 64, kLK = 64, kLRow = kLK + 8;  // 16 bytes of padding per LDS row
+// 16 MT tokens x 64 ET experts x one range of H per workgroup of 4 waves; a
+// wave holds 16 ET experts, whose W it reads straight into fragments and cuts
+// there (each W value is read by one wave of the workgroup, so that the cutting
+// is shared by MT products); the tokens' activations are staged in LDS for all
+// four waves, 64 elements of H at a time, the next stage's loads in flight
+// during the products. Partial sums go to part[range][T][E].
+constexpr int kLK = 64, kLRow = kLK + 8;  // 16 bytes of padding per LDS row
 
-template <class D>
-__global__ __launch_bounds__(256) void k_router_logits(RouterLossParams p) {
+template <class D, int MT, int ET>
+__global__ __launch_bounds__(256, 2) void k_router_logits(RouterLossParams p) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
-  constexpr int NP = Parts<D>::N;
-  __shared__ __align__(16) __bf16 xs[2][NP][kLT * kLRow];
+  constexpr int NP = Parts<D>::N, NX = MT / 2;  // vectors that a thread stages
+  __shared__ __align__(16) __bf16 xs[2][NP][16 * MT * kLRow];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.x * kLT, e = blockIdx.y * kLE + wave * 16 + n;
-  const int steps = p.H / kLK, s0 = (int)((long long)steps * blockIdx.z / gridDim.z),
-            s1 = (int)((long long)steps * (blockIdx.z + 1) / gridDim.z);
-  const float* wrow = p.W + (size_t)(e < p.E ? e : 0) * p.H + 8 * g;
-  // a thread stages two vectors: rows tid/8 and tid/8 + 32, columns 8 (tid % 8)
+  const int et = (p.E + 64 * ET - 1) / (64 * ET);
+  int ey, tx;
+  xcd_pairs(blockIdx.x, et, gridDim.x / et, ey, tx);
+  const int t0 = tx * 16 * MT, e0 = ey * 64 * ET + wave * 16 * ET + n;
+  const int steps = p.H / kLK, s0 = (int)((long long)steps * blockIdx.y / gridDim.y),
+            s1 = (int)((long long)steps * (blockIdx.y + 1) / gridDim.y);
+  const float* wrow = p.W + (size_t)(e0 < p.E ? e0 : 0) * p.H + 8 * g;
+  // a thread stages rows tid / 8 + 32 i, columns 8 (tid % 8)
   const int r0 = tid >> 3, c0 = (tid & 7) * 8;
-  const bool live[2] = {is_live(p, t0 + r0), is_live(p, t0 + r0 + 32)};
-  const elem* xrow[2] = {(const elem*)p.X + (size_t)(t0 + r0) * p.H + c0,
-                         (const elem*)p.X + (size_t)(t0 + r0 + 32) * p.H + c0};
-  vec xv[2];
-  fx8 wv[2];
+  unsigned live = 0;
+#pragma unroll
+  for (int i = 0; i < NX; ++i) live |= (is_live(p, t0 + r0 + 32 * i) ? 1u : 0u) << i;
+  const elem* xrow = (const elem*)p.X + (size_t)(t0 + r0) * p.H + c0;
+  vec xv[NX];
+  fx8 wv[2][ET];
   auto load = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NX; ++i) {
       xv[i] = (vec)(elem)0.0f;
-      if (live[i]) xv[i] = *(const vec*)(xrow[i] + s * kLK);
-      wv[i] = (fx8)(0.0f);
-      if (e < p.E) wv[i] = load8(wrow + s * kLK + 32 * i);
+      if (live >> i & 1) xv[i] = *(const vec*)(xrow + (size_t)(32 * i) * p.H + s * kLK);
     }
-  };
-  auto stage = [&](int b) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < ET; ++e) {
+        wv[i][e] = (fx8)(0.0f);
+        if (e0 + 16 * e < p.E) wv[i][e] = load8(wrow + (size_t)(16 * e) * p.H + s * kLK + 32 * i);
+      }
+    }
+  };
+  acc4 acc[MT][ET];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < ET; ++e) acc[m][e] = (acc4)(0.0f);
+  load(s0);
+  for (int s = s0; s < s1; ++s) {
+    const int b = (s - s0) & 1;
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
       bx8 q[NP];
       Parts<D>::of(xv[i], q);
 #pragma unroll
       for (int k = 0; k < NP; ++k) *(bx8*)&xs[b][k][(r0 + 32 * i) * kLRow + c0] = q[k];
     }
-  };
-  acc4 acc[4];
+    bx8 w[2][ET][3];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) acc[m] = (acc4)(0.0f);
-  load(s0);
-  for (int s = s0; s < s1; ++s) {
-    const int b = (s - s0) & 1;
-    stage(b);
-    bx8 w[2][3];
-    cut<3>(wv[0], w[0]);
-    cut<3>(wv[1], w[1]);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < ET; ++e) cut<3>(wv[i][e], w[i][e]);
     if (s + 1 < s1) load(s + 1);
     __syncthreads();  // xs[b] is written; the other half was read before the barrier of the step before
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
+      for (int m = 0; m < MT; ++m) {
 #pragma unroll
         for (int k = NP - 1; k >= 0; --k) {
           const bx8 x = *(const bx8*)&xs[b][k][(16 * m + n) * kLRow + 32 * i + 8 * g];
 #pragma unroll
-          for (int j = 2 - k; j >= 0; --j) acc[m] = mfma(x, w[i][j], acc[m]);  // smallest parts first
+          for (int j = 2 - k; j >= 0; --j)  // smallest parts first
+#pragma unroll
+            for (int e = 0; e < ET; ++e) acc[m][e] = mfma(x, w[i][e][j], acc[m][e]);
         }
       }
     }
   }
-  if (e < p.E) {
-    float* out = p.part + (size_t)blockIdx.z * p.T * p.E + e;
+  float* out = p.part + (size_t)blockIdx.y * p.T * p.E;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+  for (int e = 0; e < ET; ++e) {
+    if (e0 + 16 * e < p.E) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = t0 + 16 * m + 4 * g + r;
-        if (t < p.T) out[(size_t)t * p.E] = acc[m][r];
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = t0 + 16 * m + 4 * g + r;
+          if (t < p.T) out[(size_t)t * p.E + e0 + 16 * e] = acc[m][e][r];
+        }
       }
     }
   }
@@ -124,22 +150,21 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-constexpr int kEJ = 8;  // experts of a lane: e = lane + 64 j, E <= 512
-
 // One wave per token: adds the ranges of H, writes logits and lse, and keeps
-// its share of P_e, z and N in registers; a workgroup (8 waves) writes one row
-// of each to stat_f [groups][E + 1] and stat_i [groups][E + 1].
+// its share of P_e, z and N in registers; a workgroup (16 waves) writes one row
+// of them to stat [groups][E + 1] (sum and count of each expert, then z and N).
+// EJ: experts of a lane, e = lane + 64 j.
 template <int EJ>
-__global__ __launch_bounds__(512) void k_router_stats(RouterLossParams p) {
+__global__ __launch_bounds__(1024) void k_router_stats(RouterLossParams p) {
   __shared__ int cnt[513];
-  __shared__ float pr[8][513];
+  __shared__ float pr[16][64 * EJ + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = p.E;
-  for (int i = tid; i <= E; i += 512) cnt[i] = 0;
+  for (int i = tid; i <= E; i += 1024) cnt[i] = 0;
   __syncthreads();
   float psum[EJ], z = 0.0f;
 #pragma unroll
   for (int j = 0; j < EJ; ++j) psum[j] = 0.0f;
-  for (int t = blockIdx.x * 8 + wave; t < p.T; t += gridDim.x * 8) {
+  for (int t = blockIdx.x * 16 + wave; t < p.T; t += gridDim.x * 16) {
     const bool on = is_live(p, t);
     float l[EJ], m = -INFINITY;
 #pragma unroll
@@ -150,6 +175,7 @@ __global__ __launch_bounds__(512) void k_router_stats(RouterLossParams p) {
         float v = 0.0f;
         if (on) {
           const float* src = p.part + (size_t)t * E + e;
+#pragma unroll 8
           for (int s = 0; s < p.splits; ++s) v += src[(size_t)s * p.T * E];
           if (p.bias) v += p.bias[e];
         }
@@ -191,11 +217,10 @@ __global__ __launch_bounds__(512) void k_router_stats(RouterLossParams p) {
     if (lane + 64 * j < E) pr[wave][lane + 64 * j] = psum[j];
   if (lane == 0) pr[wave][E] = z;
   __syncthreads();
-  for (int i = tid; i <= E; i += 512) {
+  for (int i = tid; i <= E; i += 1024) {
     float s = pr[0][i];
-    for (int w = 1; w < 8; ++w) s += pr[w][i];
-    p.stat_f[(size_t)blockIdx.x * (E + 1) + i] = s;
-    p.stat_i[(size_t)blockIdx.x * (E + 1) + i] = cnt[i];
+    for (int w = 1; w < 16; ++w) s += pr[w][i];
+    p.stat[(size_t)blockIdx.x * (E + 1) + i] = make_int2(__float_as_int(s), cnt[i]);
   }
 }
 
@@ -214,9 +239,11 @@ __global__ __launch_bounds__(1024) void k_router_finish(RouterLossParams p) {
     double f = 0.0;
     int n = 0;
     if (c < W) {
+#pragma unroll 8
       for (int i = sl; i < p.groups; i += 16) {
-        f += (double)p.stat_f[(size_t)i * W + c];
-        n += p.stat_i[(size_t)i * W + c];
+        const int2 v = p.stat[(size_t)i * W + c];
+        f += (double)__int_as_float(v.x);
+        n += v.y;
       }
     }
     fs[tid] = f;
@@ -252,55 +279,41 @@ __global__ __launch_bounds__(1024) void k_router_finish(RouterLossParams p) {
 }
 
 // ---------------------------------------------------------------- gradients
-// Operand fragments of the two gradient products, in the order that a wave's
-// lanes read them (16 bytes a lane, 1 KiB a fragment):
-//   dl_a [part][token / 16][expert / 32]   lane (n, g): token n, experts 8g..8g+7
+// dl is kept in two forms: dl [Tp][Ep] fp32 for dX, and for dW cut into parts
+// and laid out as operand fragments in the order that a wave's lanes read them
+// (16 bytes a lane, 1 KiB a fragment),
 //   dl_t [part][expert / 16][token / 32]   lane (n, g): expert n, tokens 8g..8g+7
-//   w_t  [part][h / 16][expert / 32]       lane (n, g): column n, experts 8g..8g+7
+// on [Tp]: whether a token takes part.
 __device__ __forceinline__ size_t frag(size_t tiles, size_t part, size_t tile) { return (part * tiles + tile) * 512; }
 
-// Workgroups 0 .. Tp/32 - 1: dl of 32 tokens, one wave per 4 of them, held in
-// LDS and written as both operands. The rest: w_t of 32 experts x 64 columns.
-__global__ __launch_bounds__(512) void k_router_dl(RouterLossParams p) {
-  extern __shared__ __align__(16) float ds[];  // [32][Ep + 4], or [32][68]
+// dl of 32 tokens per workgroup, two per wave, held in LDS and written in both
+// forms, with the tile's column sums. EJ: experts of a lane, e = lane + 64 j.
+template <int EJ>
+__global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
+  extern __shared__ __align__(16) float ds[];  // [32][Ep + 4]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
   const int E = p.E, Ep = p.Ep;
-  const int tok_wgs = p.Tp / 32;
-  if ((int)blockIdx.x >= tok_wgs) {
-    const int b = blockIdx.x - tok_wgs, e0 = 32 * (b % (Ep / 32)), h0 = 64 * (b / (Ep / 32));
-    const int r = tid >> 4, c = (tid & 15) * 4;
-    fx4 v = (fx4)(0.0f);
-    if (e0 + r < E) v = *(const fx4*)(p.W + (size_t)(e0 + r) * p.H + h0 + c);
-    *(fx4*)(ds + r * 68 + c) = v;
-    __syncthreads();
-    if (wave < 4) {
-      fx8 x;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = ds[(8 * g + i) * 68 + 16 * wave + n];
-      bx8 q[3];
-      cut<3>(x, q);
-      const size_t tiles = (size_t)(p.H / 16) * (Ep / 32), tile = (size_t)(h0 / 16 + wave) * (Ep / 32) + e0 / 32;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) *(bx8*)(p.w_t + frag(tiles, k, tile) + 8 * lane) = q[k];
-    }
-    return;
-  }
   const int t0 = blockIdx.x * 32, row = Ep + 4;
   const int N = p.counts[E];
   const float gl = p.gloss ? *p.gloss : 1.0f, inv_n = N > 0 ? 1.0f / (float)N : 0.0f;
   const float ca = gl * p.alpha * (float)E * inv_n, cb = gl * 2.0f * p.beta * inv_n, cf = inv_n / (float)p.K;
-  for (int i = 0; i < 4; ++i) {
-    const int r = wave * 4 + i, t = t0 + r;
+  float f[EJ];  // f_e
+#pragma unroll
+  for (int j = 0; j < EJ; ++j) f[j] = lane + 64 * j < E ? (float)p.counts[lane + 64 * j] * cf : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = wave * 2 + i, t = t0 + r;
     const float lse = is_live(p, t) ? p.lse[t] : -INFINITY;
     const bool on = !(lse == -INFINITY);  // nan stays on and spreads
-    float pr[kEJ], dot = 0.0f;
+    if (lane == 0) p.on[t] = on ? 1 : 0;
+    float pr[EJ], dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kEJ; ++j) {
+    for (int j = 0; j < EJ; ++j) {
       const int e = lane + 64 * j;
       pr[j] = 0.0f;
       if (e < E && on) {
         pr[j] = expf(p.logits[(size_t)t * E + e] - lse);
-        dot += (float)p.counts[e] * cf * pr[j];
+        dot += f[j] * pr[j];
       }
     }
     dot = wave_sum(dot);
@@ -323,11 +336,11 @@ __global__ __launch_bounds__(512) void k_router_dl(RouterLossParams p) {
       c = id >= 0 ? w * (gw - mean) : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < kEJ; ++j) {
+    for (int j = 0; j < EJ; ++j) {
       const int e = lane + 64 * j;
       if (e < Ep) {
         float d = 0.0f;
-        if (e < E && on) d = pr[j] * (ca * ((float)p.counts[e] * cf - dot) + cb * lse);
+        if (e < E && on) d = pr[j] * (ca * (f[j] - dot) + cb * lse);
         if (p.gw) {
           for (int k = 0; k < p.K; ++k) {  // slots in order, also where one expert is named twice
             const int ik = __shfl(id, k);
@@ -340,78 +353,117 @@ __global__ __launch_bounds__(512) void k_router_dl(RouterLossParams p) {
     }
   }
   __syncthreads();
-  const int kt = Ep / 32;
-  const size_t ta = (size_t)(p.Tp / 16) * kt, tt = (size_t)(Ep / 16) * (p.Tp / 32);
-  for (int f = wave; f < 2 * kt; f += 8) {  // dl_a: 2 token tiles x kt expert tiles
-    const int m = f & 1, k32 = f >> 1;
-    const fx8 x = load8(ds + (16 * m + n) * row + 32 * k32 + 8 * g);
-    bx8 q[3];
-    cut<3>(x, q);
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      *(bx8*)(p.dl_a + frag(ta, k, (size_t)(t0 / 16 + m) * kt + k32) + 8 * lane) = q[k];
+  for (int i = tid; i < 32 * (Ep / 4); i += 1024) {
+    const int r = i / (Ep / 4), c = i % (Ep / 4) * 4;
+    *(fx4*)(p.dl + (size_t)(t0 + r) * Ep + c) = *(const fx4*)(ds + r * row + c);
   }
-  for (int f = wave; f < Ep / 16; f += 8) {  // dl_t: Ep / 16 expert tiles
+  const size_t tt = (size_t)(Ep / 16) * (p.Tp / 32);
+  for (int et = wave; et < Ep / 16; et += 16) {  // dl_t: Ep / 16 expert tiles
     fx8 x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = ds[(8 * g + i) * row + 16 * f + n];
+    for (int i = 0; i < 8; ++i) x[i] = ds[(8 * g + i) * row + 16 * et + n];
     bx8 q[3];
     cut<3>(x, q);
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      *(bx8*)(p.dl_t + frag(tt, k, (size_t)f * (p.Tp / 32) + t0 / 32) + 8 * lane) = q[k];
+      *(bx8*)(p.dl_t + frag(tt, k, (size_t)et * (p.Tp / 32) + t0 / 32) + 8 * lane) = q[k];
   }
-  for (int e = tid; e < E; e += 512) {
+  for (int e = tid; e < E; e += 1024) {
     float s = 0.0f;
+#pragma unroll
     for (int r = 0; r < 32; ++r) s += ds[r * row + e];
     p.db_part[(size_t)blockIdx.x * E + e] = s;
   }
 }
 
-// dX = dl W: a wave holds 64 tokens x 64 columns, a workgroup 128 x 128. The
-// columns are the products' rows, so that a lane ends with four of a token's
-// consecutive columns.
-__global__ __launch_bounds__(256) void k_router_dx(RouterLossParams p) {
+// dX = dl W: a workgroup of 8 waves keeps the three parts of W of 128 columns
+// and up to 128 experts in LDS (96 KiB, cut once) and goes over its range of
+// tokens, 256 at a time; a wave holds 64 tokens x 64 columns and cuts dl as it
+// loads it. The columns are the products' rows, so that a lane ends with four
+// of a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so
+// that each L2 holds its own part of dl.
+constexpr int kDxLds = 3 * 8 * 4 * 1024;
+
+__global__ __launch_bounds__(512, 2) void k_router_dx(RouterLossParams p) {
+  extern __shared__ __align__(16) __bf16 wl[];  // [part][column / 16][expert / 32] fragments
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int kt = p.Ep / 32;
-  const int t0 = blockIdx.x * 128 + (wave & 1) * 64, h0 = blockIdx.y * 128 + (wave >> 1) * 64;
-  if (t0 >= p.Tp || h0 >= p.H) return;
-  const size_t ta = (size_t)(p.Tp / 16) * kt, tw = (size_t)(p.H / 16) * kt;
-  acc4 acc[4][4];
+  const int cols = (p.H + 127) / 128, blocks = (p.Tp + 255) / 256, kt = p.Ep / 32;
+  int cg, range;
+  xcd_pairs(blockIdx.x, cols, p.dx_ranges, cg, range);
+  const int h0 = cg * 128, half = wave & 1;
+  const int b0 = (int)((long long)blocks * range / p.dx_ranges), b1 = (int)((long long)blocks * (range + 1) / p.dx_ranges);
+  auto load_w = [&](int k0) {
+    for (int f = wave; f < 32; f += 8) {
+      const int c = f >> 2, k = f & 3, h = h0 + 16 * c + n;
+      fx8 v = (fx8)(0.0f);
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[m][c] = (acc4)(0.0f);
-  for (int k = 0; k < kt; ++k) {
-    bx8 a[4][3], b[4][3];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        a[m][q] = *(const bx8*)(p.dl_a + frag(ta, q, (size_t)(t0 / 16 + m) * kt + k) + 8 * lane);
-        b[m][q] = *(const bx8*)(p.w_t + frag(tw, q, (size_t)(h0 / 16 + m) * kt + k) + 8 * lane);
+      for (int i = 0; i < 8; ++i) {
+        const int e = 32 * (k0 + k) + 8 * g + i;
+        if (e < p.E && h < p.H) v[i] = p.W[(size_t)e * p.H + h];
       }
+      bx8 q[3];
+      cut<3>(v, q);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *(bx8*)(wl + ((i * 8 + c) * 4 + k) * 512 + 8 * lane) = q[i];
     }
+  };
+  if (kt <= 4) {
+    load_w(0);
+    __syncthreads();
+  }
+  const bool mine = h0 + 64 * half < p.H;
+  for (int b = b0; b < b1; ++b) {
+    const int t0 = b * 256 + (wave >> 1) * 64;
+    const bool work = mine && t0 < p.Tp;
+    acc4 acc[4][4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 4; ++c) acc[m][c] = (acc4)(0.0f);
+    for (int k0 = 0; k0 < kt; k0 += 4) {
+      if (kt > 4) {
+        __syncthreads();
+        load_w(k0);
+        __syncthreads();
+      }
+      if (!work) continue;
+      const int kn = kt - k0 < 4 ? kt - k0 : 4;
+      const float* src = p.dl + (size_t)(t0 + n) * p.Ep + 32 * k0 + 8 * g;
+      fx8 d[4];
 #pragma unroll
-        for (int s = 2; s >= 0; --s) {  // parts i, j with i + j = s: the smallest first
+      for (int m = 0; m < 4; ++m) d[m] = load8(src + (size_t)(16 * m) * p.Ep);
+      for (int k = 0; k < kn; ++k) {
+        bx8 a[4][3];
 #pragma unroll
-          for (int i = s; i >= 0; --i) acc[m][c] = mfma(b[c][s - i], a[m][i], acc[m][c]);
+        for (int m = 0; m < 4; ++m) cut<3>(d[m], a[m]);
+        if (k + 1 < kn) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) d[m] = load8(src + (size_t)(16 * m) * p.Ep + 32 * (k + 1));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          bx8 w[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) w[i] = *(const bx8*)(wl + ((i * 8 + 4 * half + c) * 4 + k) * 512 + 8 * lane);
+#pragma unroll
+          for (int s = 2; s >= 0; --s)  // parts i, j with i + j = s: the smallest first
+#pragma unroll
+            for (int i = s; i >= 0; --i)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) acc[m][c] = mfma(w[s - i], a[m][i], acc[m][c]);
         }
       }
     }
-  }
+    if (!work) continue;
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int t = t0 + 16 * m + n;
-    if (t < p.T) {
-      const bool on = is_on(p, t);
-      float* out = p.dX + (size_t)t * p.H + h0 + 4 * g;
+    for (int m = 0; m < 4; ++m) {
+      const int t = t0 + 16 * m + n;
+      if (t < p.T) {
+        const bool on = p.on[t];
+        float* out = p.dX + (size_t)t * p.H + h0 + 64 * half + 4 * g;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) *(acc4*)(out + 16 * c) = on ? acc[m][c] : (acc4)(0.0f);
+        for (int c = 0; c < 4; ++c) *(acc4*)(out + 16 * c) = on ? acc[m][c] : (acc4)(0.0f);
+      }
     }
   }
 }
@@ -422,49 +474,68 @@ __global__ __launch_bounds__(256) void k_router_dx(RouterLossParams p) {
 // fragments of a step (fragment j: columns 8 n + j). The waves' sums meet in
 // LDS in wave order.
 template <class D>
-__global__ __launch_bounds__(256, 2) void k_router_dw(RouterLossParams p) {
+__global__ __launch_bounds__(256, 1) void k_router_dw(RouterLossParams p) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
   constexpr int NP = Parts<D>::N;
   __shared__ __align__(16) float sum[64][128 + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int e0 = blockIdx.x * 64, h = blockIdx.y * 128 + 8 * n;
+  const int ht = (p.H + 127) / 128;
+  int ex, rest;
+  xcd_pairs(blockIdx.x, p.Ep / 64, ht * p.chunks, ex, rest);
+  const int e0 = ex * 64, h0 = rest % ht * 128, chunk = rest / ht, h = h0 + 8 * n;
   const int nt = p.Tp / 32;
-  const int b0 = (int)((long long)nt * blockIdx.z / gridDim.z), b1 = (int)((long long)nt * (blockIdx.z + 1) / gridDim.z);
+  const int b0 = (int)((long long)nt * chunk / p.chunks), b1 = (int)((long long)nt * (chunk + 1) / p.chunks);
   const size_t tt = (size_t)(p.Ep / 16) * nt;
   acc4 acc[4][8];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[a][j] = (acc4)(0.0f);
-  for (int b = b0 + wave; b < b1; b += 4) {
-    vec x[8];
+  vec x[8];
+  bx8 a[4][3];
+  unsigned long long on;  // 8 tokens' bytes
+  const elem* xcol = (const elem*)p.X + (h < p.H ? h : 0);
+  // every load goes out at once: rows past the batch read its last one, and the
+  // tokens that do not take part are cleared when their bytes have come
+  auto load = [&](int b) {
+    on = *(const unsigned long long*)(p.on + 32 * b + 8 * g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = 32 * b + 8 * g + i;
-      x[i] = (vec)(elem)0.0f;
-      if (h < p.H && is_on(p, t)) x[i] = *(const vec*)((const elem*)p.X + (size_t)t * p.H + h);
+      x[i] = *(const vec*)(xcol + (size_t)(t < p.T ? t : p.T - 1) * p.H);
     }
-    bx8 a[4][3];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int q = 0; q < 3; ++q)
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
+      for (int m = 0; m < 4; ++m)
         a[m][q] = *(const bx8*)(p.dl_t + frag(tt, q, (size_t)(e0 / 16 + m) * nt + b) + 8 * lane);
+  };
+  if (b0 + wave < b1) load(b0 + wave);
+  for (int b = b0 + wave; b < b1; b += 4) {
+    vec c[8];  // the 8 x 8 block turned round
+    bx8 d[4][3];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = on >> (8 * i) & 1 ? x[i] : (vec)(elem)0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[j][i] = x[i][j];
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) d[m][q] = a[m][q];
+    if (b + 4 < b1) load(b + 4);  // the next step's operands come in during the products
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      vec c;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = x[i][j];
       bx8 q[NP];
-      Parts<D>::of(c, q);
+      Parts<D>::of(c[j], q);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
+      for (int k = NP - 1; k >= 0; --k)
 #pragma unroll
-        for (int k = NP - 1; k >= 0; --k)
+        for (int i = 2 - k; i >= 0; --i)
 #pragma unroll
-          for (int i = 2 - k; i >= 0; --i) acc[m][j] = mfma(a[m][i], q[k], acc[m][j]);
-      }
+          for (int m = 0; m < 4; ++m) acc[m][j] = mfma(d[m][i], q[k], acc[m][j]);
     }
   }
   for (int w = 0; w < 4; ++w) {
@@ -484,34 +555,36 @@ __global__ __launch_bounds__(256, 2) void k_router_dw(RouterLossParams p) {
     }
     __syncthreads();
   }
-  float* out = p.dw_part + (size_t)blockIdx.z * p.E * p.H;
+  float* out = p.dw_part + (size_t)chunk * p.E * p.H;
   for (int i = tid; i < 64 * 16; i += 256) {
-    const int e = i >> 4, c = (i & 15) * 8, col = blockIdx.y * 128 + c;
+    const int e = i >> 4, c = (i & 15) * 8, col = h0 + c;
     if (e0 + e < p.E && col < p.H) store8(out + (size_t)(e0 + e) * p.H + col, load8(&sum[e][c]));
   }
 }
 
 // Adds the token ranges of dW (workgroups below `dw_wgs`, 4 values a thread)
 // and the token tiles of dbias (64 experts a workgroup, 16 slices).
-__global__ __launch_bounds__(1024) void k_router_add(RouterLossParams p, int dw_wgs) {
-  __shared__ double buf[1024];
+__global__ __launch_bounds__(256) void k_router_add(RouterLossParams p, int dw_wgs) {
+  __shared__ double buf[256];
   const int tid = threadIdx.x;
   if ((int)blockIdx.x < dw_wgs) {
-    const size_t n = (size_t)p.E * p.H, i = ((size_t)blockIdx.x * 1024 + tid) * 4;
+    const size_t n = (size_t)p.E * p.H, i = ((size_t)blockIdx.x * 256 + tid) * 4;
     if (i >= n) return;
     fx4 s = (fx4)(0.0f);
+#pragma unroll 8
     for (int c = 0; c < p.chunks; ++c) s += *(const fx4*)(p.dw_part + (size_t)c * n + i);
     *(fx4*)(p.dW + i) = s;
     return;
   }
-  const int e = (blockIdx.x - dw_wgs) * 64 + (tid & 63);
+  const int e = (blockIdx.x - dw_wgs) * 16 + (tid & 15);
   double s = 0.0;
   if (e < p.E)
-    for (int i = tid >> 6; i < p.Tp / 32; i += 16) s += (double)p.db_part[(size_t)i * p.E + e];
+#pragma unroll 8
+    for (int i = tid >> 4; i < p.Tp / 32; i += 16) s += (double)p.db_part[(size_t)i * p.E + e];
   buf[tid] = s;
   __syncthreads();
-  if (tid < 64 && e < p.E) {
-    for (int k = 1; k < 16; ++k) s += buf[tid + 64 * k];
+  if (tid < 16 && e < p.E) {
+    for (int k = 1; k < 16; ++k) s += buf[tid + 16 * k];
     p.dbias[e] = (float)s;
   }
 }
@@ -522,45 +595,60 @@ static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 RouterLossWs router_loss_ws(int T, int H, int E) {
   RouterLossWs w{};
-  const int tiles = ((T + kLT - 1) / kLT) * ((E + kLE - 1) / kLE);
+  // 128-token tiles where the batch fills the chip with them, else 64
+  w.mt = T >= 8192 ? 8 : 4;
+  w.et = E > 64 ? 2 : 1;
+  const int tiles = ((T + 16 * w.mt - 1) / (16 * w.mt)) * ((E + 64 * w.et - 1) / (64 * w.et));
   // ranges of H for the logits: about 512 workgroups, whole stages of 64
   w.splits = tiles > 0 ? 512 / tiles : 1;
-  if (w.splits > 32) w.splits = 32;
+  if (w.splits > 16) w.splits = 16;
   if (w.splits > H / kLK) w.splits = H / kLK;
   if (w.splits < 1) w.splits = 1;
   w.groups = (T + 15) / 16 < 256 ? (T + 15) / 16 : 256;
   if (w.groups < 1) w.groups = 1;
   size_t off = 0;
   w.part = off;   off += up256((size_t)w.splits * T * E * 4);
-  w.stat_f = off; off += up256((size_t)w.groups * (E + 1) * 4);
-  w.stat_i = off; off += up256((size_t)w.groups * (E + 1) * 4);
+  w.stat = off;   off += up256((size_t)w.groups * (E + 1) * 8);
   const size_t fwd = off;
   w.Tp = (T + 63) / 64 * 64;
   w.Ep = (E + 63) / 64 * 64;
   const int wt = (w.Ep / 64) * ((H + 127) / 128), nt = w.Tp / 32;
-  // ranges of tokens for dW: about 512 workgroups, at least 8 tiles of 32 tokens each
-  w.chunks = 512 / wt;
+  // ranges of tokens for dW: about 256 workgroups, at least 8 tiles of 32 tokens each
+  w.chunks = 256 / wt;
   if (w.chunks > nt / 8) w.chunks = nt / 8;
   if (w.chunks < 1) w.chunks = 1;
+  // ranges of tokens for dX: about 256 workgroups (one per CU), whole blocks of 256 tokens
+  const int blocks = (w.Tp + 255) / 256, cols = (H + 127) / 128;
+  w.dx_ranges = (256 + cols - 1) / cols;
+  if (w.dx_ranges > blocks) w.dx_ranges = blocks;
+  if (w.dx_ranges < 1) w.dx_ranges = 1;
   off = 0;
-  w.dl_a = off;    off += up256((size_t)3 * w.Tp * w.Ep * 2);
+  w.dl = off;      off += up256((size_t)w.Tp * w.Ep * 4);
   w.dl_t = off;    off += up256((size_t)3 * w.Tp * w.Ep * 2);
-  w.w_t = off;     off += up256((size_t)3 * H * w.Ep * 2);
+  w.on = off;      off += up256((size_t)w.Tp);
   w.db_part = off; off += up256((size_t)(w.Tp / 32) * E * 4);
   w.dw_part = off; off += up256((size_t)w.chunks * E * H * 4);
   w.total = fwd > off ? fwd : off;
   return w;
 }
 
+template <class D>
+static void logits(const RouterLossParams& p, hipStream_t s) {
+  const dim3 grid(((p.T + 16 * p.mt - 1) / (16 * p.mt)) * ((p.E + 64 * p.et - 1) / (64 * p.et)), p.splits);
+  if (p.mt == 8 && p.et == 2) k_router_logits<D, 8, 2><<<grid, 256, 0, s>>>(p);
+  else if (p.mt == 8) k_router_logits<D, 8, 1><<<grid, 256, 0, s>>>(p);
+  else if (p.et == 2) k_router_logits<D, 4, 2><<<grid, 256, 0, s>>>(p);
+  else k_router_logits<D, 4, 1><<<grid, 256, 0, s>>>(p);
+}
+
 hipError_t launch_router_loss(const RouterLossParams& p, bool bf16, hipStream_t s) {
   if (p.T > 0) {
-    const dim3 grid((p.T + kLT - 1) / kLT, (p.E + kLE - 1) / kLE, p.splits);
-    if (bf16) k_router_logits<BF16><<<grid, 256, 0, s>>>(p);
-    else k_router_logits<F16><<<grid, 256, 0, s>>>(p);
+    if (bf16) logits<BF16>(p, s);
+    else logits<F16>(p, s);
   }
-  if (p.E <= 64) k_router_stats<1><<<p.groups, 512, 0, s>>>(p);
-  else if (p.E <= 128) k_router_stats<2><<<p.groups, 512, 0, s>>>(p);
-  else k_router_stats<8><<<p.groups, 512, 0, s>>>(p);
+  if (p.E <= 64) k_router_stats<1><<<p.groups, 1024, 0, s>>>(p);
+  else if (p.E <= 128) k_router_stats<2><<<p.groups, 1024, 0, s>>>(p);
+  else k_router_stats<8><<<p.groups, 1024, 0, s>>>(p);
   k_router_finish<<<1, 1024, 0, s>>>(p);
   return hipGetLastError();
 }
@@ -569,23 +657,30 @@ hipError_t launch_router_loss_grad(const RouterLossParams& p, bool bf16, hipStre
   static unsigned long long raised = 0;
   const int lds = 32 * (p.Ep + 4) * 4;
   if (lds > 64 * 1024) {
-    const hipError_t e = raise_lds_limit((const void*)k_router_dl, 32 * (512 + 4) * 4, raised);
+    const hipError_t e = raise_lds_limit((const void*)k_router_dl<8>, 32 * (512 + 4) * 4, raised);
     if (e != hipSuccess) return e;
   }
-  const int w_wgs = p.dX ? (p.Ep / 32) * (p.H / 64) : 0;
-  const int tok_wgs = p.Tp / 32;
-  if (tok_wgs + w_wgs)
-    k_router_dl<<<tok_wgs + w_wgs, 512, lds, s>>>(p);
-  if (p.dX && p.T > 0) k_router_dx<<<dim3((p.T + 127) / 128, (p.H + 127) / 128), 256, 0, s>>>(p);
+  const int dl_wgs = p.Tp / 32;
+  if (dl_wgs) {
+    if (p.Ep == 64) k_router_dl<1><<<dl_wgs, 1024, lds, s>>>(p);
+    else if (p.Ep == 128) k_router_dl<2><<<dl_wgs, 1024, lds, s>>>(p);
+    else k_router_dl<8><<<dl_wgs, 1024, lds, s>>>(p);
+  }
+  if (p.dX) {
+    static unsigned long long dx_raised = 0;
+    const hipError_t e = raise_lds_limit((const void*)k_router_dx, kDxLds, dx_raised);
+    if (e != hipSuccess) return e;
+    k_router_dx<<<(p.H + 127) / 128 * p.dx_ranges, 512, kDxLds, s>>>(p);
+  }
   int dw_wgs = 0;
   if (p.dW) {
-    const dim3 grid(p.Ep / 64, (p.H + 127) / 128, p.chunks);
+    const int grid = (p.Ep / 64) * ((p.H + 127) / 128) * p.chunks;
     if (bf16) k_router_dw<BF16><<<grid, 256, 0, s>>>(p);
     else k_router_dw<F16><<<grid, 256, 0, s>>>(p);
-    dw_wgs = (int)(((size_t)p.E * p.H / 4 + 1023) / 1024);
+    dw_wgs = (int)(((size_t)p.E * p.H / 4 + 255) / 256);
   }
-  const int db_wgs = p.dbias ? (p.E + 63) / 64 : 0;
-  if (dw_wgs + db_wgs) k_router_add<<<dw_wgs + db_wgs, 1024, 0, s>>>(p, dw_wgs);
+  const int db_wgs = p.dbias ? (p.E + 15) / 16 : 0;
+  if (dw_wgs + db_wgs) k_router_add<<<dw_wgs + db_wgs, 256, 0, s>>>(p, dw_wgs);
   return hipGetLastError();
 }
 

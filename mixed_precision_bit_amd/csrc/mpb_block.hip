@@ -62,14 +62,15 @@ mpb::RouterLossParams router_params(const void* X, const float* W, const int32_t
   p.X = X; p.W = W; p.idx = idx; p.mask = mask;
   p.T = T; p.H = H; p.E = E; p.K = K; p.alpha = alpha; p.beta = beta;
   p.part = (float*)(ws + w.part);
-  p.stat_f = (float*)(ws + w.stat_f);
-  p.stat_i = (int32_t*)(ws + w.stat_i);
-  p.dl_a = (uint16_t*)(ws + w.dl_a);
+  p.stat = (int2*)(ws + w.stat);
+  p.dl = (float*)(ws + w.dl);
   p.dl_t = (uint16_t*)(ws + w.dl_t);
-  p.w_t = (uint16_t*)(ws + w.w_t);
+  p.on = (uint8_t*)(ws + w.on);
   p.db_part = (float*)(ws + w.db_part);
   p.dw_part = (float*)(ws + w.dw_part);
-  p.splits = w.splits; p.groups = w.groups; p.chunks = w.chunks; p.Tp = w.Tp; p.Ep = w.Ep;
+  p.splits = w.splits; p.groups = w.groups; p.chunks = w.chunks; p.dx_ranges = w.dx_ranges;
+  p.Tp = w.Tp; p.Ep = w.Ep;
+  p.mt = w.mt; p.et = w.et;
   return p;
 }
 

@@ -269,20 +269,20 @@ struct RouterLossParams {
   float* dbias;          // [E] or null
   // workspace
   float* part;           // [splits][T][E] partial logits
-  float* stat_f;         // [groups][E + 1] sums of p, sum of lse^2
-  int32_t* stat_i;       // [groups][E + 1] counts, live tokens
-  uint16_t* dl_a;        // operand fragments, see the kernels
-  uint16_t* dl_t;
-  uint16_t* w_t;
+  int2* stat;            // [groups][E + 1] sums (fp32) and counts, see the kernel
+  float* dl;             // [Tp][Ep] gradients of the logits
+  uint16_t* dl_t;        // the same as operand fragments, see the kernel
+  uint8_t* on;           // [Tp] whether a token takes part
   float* db_part;        // [Tp / 32][E]
   float* dw_part;        // [chunks][E][H]
-  int splits, groups, chunks, Tp, Ep;
+  int splits, groups, chunks, dx_ranges, Tp, Ep, mt, et;
 };
 // Regions of the workspace (the forward and the backward pass each use all of
 // it) and the launch shapes they go with, from the sizes only.
 struct RouterLossWs {
-  size_t part, stat_f, stat_i, dl_a, dl_t, w_t, db_part, dw_part, total;
-  int splits, groups, chunks, Tp, Ep;  // Tp, Ep: T and E rounded up to 64
+  size_t part, stat, dl, dl_t, on, db_part, dw_part, total;
+  int splits, groups, chunks, dx_ranges, Tp, Ep;  // Tp, Ep: T and E rounded up to 64
+  int mt, et;                          // tiles of 16 tokens, of 64 experts of a logits workgroup
 };
 RouterLossWs router_loss_ws(int T, int H, int E);
 hipError_t launch_router_loss(const RouterLossParams& p, bool bf16, hipStream_t s);
