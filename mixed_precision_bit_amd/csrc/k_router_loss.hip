@@ -14,9 +14,9 @@
 // an fp32 operand is cut into three bf16 parts (8 bits each, 24 together, by
 // truncation: exact, and no part overflows), an fp16 activation into two, a
 // bf16 one is its own part; products of parts are exact in fp32 and accumulate
-// in fp32, and only products below 2^-24 of the whole are left out. Against
-// the fp32 matrix instructions (1/16 of the bf16 rate) three to six bf16
-// products are still 2.5 to 5 times cheaper.
+// in fp32, and only products below 2^-24 of the whole are left out (dX takes
+// fp16 halves instead, see halves). Against the fp32 matrix instructions (1/16
+// of the 16-bit rate) three to five products are still 3 to 5 times cheaper.
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -164,52 +164,46 @@ __global__ __launch_bounds__(1024) void k_router_stats(RouterLossParams p) {
   float psum[EJ], z = 0.0f;
 #pragma unroll
   for (int j = 0; j < EJ; ++j) psum[j] = 0.0f;
+  float bias[EJ];
+#pragma unroll
+  for (int j = 0; j < EJ; ++j) bias[j] = p.bias && lane + 64 * j < E ? p.bias[lane + 64 * j] : 0.0f;
   for (int t = blockIdx.x * 16 + wave; t < p.T; t += gridDim.x * 16) {
-    const bool on = is_live(p, t);
+    // all of a token's loads go out together
+    const int alive = p.mask ? p.mask[t] : 1;
+    const int id = p.idx[(size_t)t * p.K + (lane < p.K ? lane : 0)];
     float l[EJ], m = -INFINITY;
+    bool nan = false;  // fmaxf drops nan
 #pragma unroll
     for (int j = 0; j < EJ; ++j) {
       const int e = lane + 64 * j;
-      l[j] = -INFINITY;
-      if (e < E) {
-        float v = 0.0f;
-        if (on) {
-          const float* src = p.part + (size_t)t * E + e;
+      const float* src = p.part + (size_t)t * E + (e < E ? e : 0);
+      float v = 0.0f;
 #pragma unroll 8
-          for (int s = 0; s < p.splits; ++s) v += src[(size_t)s * p.T * E];
-          if (p.bias) v += p.bias[e];
-        }
-        p.logits[(size_t)t * E + e] = v;
-        l[j] = v;
-        m = fmaxf(m, v);
+      for (int s = 0; s < p.splits; ++s) v += src[(size_t)s * p.T * E];
+      l[j] = alive ? v + bias[j] : 0.0f;
+      if (e < E) {
+        p.logits[(size_t)t * E + e] = l[j];
+        m = fmaxf(m, l[j]);
+        nan |= l[j] != l[j];
       }
     }
-    if (!on) {
-      if (lane == 0) p.lse[t] = 0.0f;
-      continue;
-    }
     m = wave_max(m);
-    float s = 0.0f;
+    float s = 0.0f, x[EJ];
 #pragma unroll
-    for (int j = 0; j < EJ; ++j)
-      if (lane + 64 * j < E) s += expf(l[j] - m);
-    s = wave_sum(s);
-    const float lse = m == -INFINITY && !(s == s && s > 0.0f) ? -INFINITY : m + logf(s);
-    bool nan = false;  // fmaxf drops nan: the row's own values decide
-#pragma unroll
-    for (int j = 0; j < EJ; ++j) nan |= l[j] != l[j];
-    const bool any_nan = __ballot(nan) != 0;
-    const float out = any_nan ? NAN : lse;
-    if (lane == 0) p.lse[t] = out;
-    if (out == -INFINITY) continue;  // no expert left: the token does not count
-    z += out * out;
-#pragma unroll
-    for (int j = 0; j < EJ; ++j)
-      if (lane + 64 * j < E) psum[j] += expf(l[j] - out);
-    if (lane < p.K) {
-      const int id = p.idx[(size_t)t * p.K + lane];
-      if (id >= 0 && id < E) atomicAdd(&cnt[id], 1);
+    for (int j = 0; j < EJ; ++j) {
+      x[j] = lane + 64 * j < E ? expf(l[j] - m) : 0.0f;
+      s += x[j];
     }
+    s = wave_sum(s);
+    float lse = m == -INFINITY ? -INFINITY : m + logf(s);
+    if (__ballot(nan)) lse = NAN;
+    if (lane == 0) p.lse[t] = alive ? lse : 0.0f;
+    if (!alive || lse == -INFINITY) continue;  // padding, or no expert left: the token does not count
+    z += lse * lse;
+    const float r = lse == lse ? 1.0f / s : NAN;
+#pragma unroll
+    for (int j = 0; j < EJ; ++j) psum[j] += x[j] * r;
+    if (lane < p.K && id >= 0 && id < E) atomicAdd(&cnt[id], 1);
     if (lane == 0) atomicAdd(&cnt[E], 1);
   }
 #pragma unroll
@@ -279,11 +273,33 @@ __global__ __launch_bounds__(1024) void k_router_finish(RouterLossParams p) {
 }
 
 // ---------------------------------------------------------------- gradients
-// dl is kept in two forms: dl [Tp][Ep] fp32 for dX, and for dW cut into parts
-// and laid out as operand fragments in the order that a wave's lanes read them
-// (16 bytes a lane, 1 KiB a fragment),
-//   dl_t [part][expert / 16][token / 32]   lane (n, g): expert n, tokens 8g..8g+7
+// dl is kept in two forms, both cut into parts and laid out as operand
+// fragments in the order that a wave's lanes read them (16 bytes a lane, 1 KiB a
+// fragment):
+//   dl_t [3][expert / 16][token / 32]   lane (n, g): expert n, tokens 8g..8g+7;
+//        bf16 parts, as bf16 activations need them on the other side
+//   dl_a [2][token / 16][expert / 32]   lane (n, g): token n, experts 8g..8g+7;
+//        fp16 halves (see halves) of dl scaled by its token's power of two,
+//        whose inverse is dl_s [Tp]
 // on [Tp]: whether a token takes part.
+// The power of two that brings a largest magnitude m into [2^13, 2^14) (at most
+// 2^126; 1 for zero, inf and nan).
+__device__ __forceinline__ float scale_for(float m) {
+  const int e = (int)(__float_as_uint(m) >> 23);  // biased exponent
+  const int k = e == 0 || e == 255 ? (e ? 0 : m > 0.0f ? 126 : 0) : 127 + 13 - e;
+  return ldexpf(1.0f, k > 126 ? 126 : k);
+}
+
+// x = hi + lo in fp16, both rounded to nearest: 22 bits of x, or 2^-25 where x
+// is small against its row's largest value (scale_for: 2^-38 of that). Three
+// products of halves, hi hi + hi lo + lo hi, are then within 12 x 2^-24 of the
+// exact product: half the matrix work of three bf16 parts, where a power of two
+// per row and per column can be taken out of the product.
+__device__ __forceinline__ void halves(fx8 x, hx8 (&q)[2]) {
+  q[0] = narrow<F16>(x);
+  q[1] = narrow<F16>(x - widen<F16>(q[0]));
+}
+
 __device__ __forceinline__ size_t frag(size_t tiles, size_t part, size_t tile) { return (part * tiles + tile) * 512; }
 
 // dl of 32 tokens per workgroup, two per wave, held in LDS and written in both
@@ -291,6 +307,7 @@ __device__ __forceinline__ size_t frag(size_t tiles, size_t part, size_t tile) {
 template <int EJ>
 __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
   extern __shared__ __align__(16) float ds[];  // [32][Ep + 4]
+  __shared__ float scl[32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
   const int E = p.E, Ep = p.Ep;
   const int t0 = blockIdx.x * 32, row = Ep + 4;
@@ -302,60 +319,73 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
   for (int j = 0; j < EJ; ++j) f[j] = lane + 64 * j < E ? (float)p.counts[lane + 64 * j] * cf : 0.0f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = wave * 2 + i, t = t0 + r;
-    const float lse = is_live(p, t) ? p.lse[t] : -INFINITY;
-    const bool on = !(lse == -INFINITY);  // nan stays on and spreads
+    const int r = wave * 2 + i, t = t0 + r, tc = t < p.T ? t : p.T - 1;
+    // all of a token's loads go out together
+    float lse = p.lse[tc];
+    const bool alive = is_live(p, t);
+    int id = -1;
+    float gw = 0.0f;
+    if (p.gw && lane < p.K) {
+      id = p.idx[(size_t)tc * p.K + lane];
+      gw = p.gw[(size_t)tc * p.K + lane];
+    }
+    float l[EJ], pr[EJ], dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EJ; ++j) l[j] = p.logits[(size_t)tc * E + (lane + 64 * j < E ? lane + 64 * j : 0)];
+    const bool on = alive && !(lse == -INFINITY);  // nan stays on and spreads
     if (lane == 0) p.on[t] = on ? 1 : 0;
-    float pr[EJ], dot = 0.0f;
+    if (!on) lse = 0.0f;
 #pragma unroll
     for (int j = 0; j < EJ; ++j) {
-      const int e = lane + 64 * j;
-      pr[j] = 0.0f;
-      if (e < E && on) {
-        pr[j] = expf(p.logits[(size_t)t * E + e] - lse);
-        dot += f[j] * pr[j];
-      }
+      pr[j] = on && lane + 64 * j < E ? expf(l[j] - lse) : 0.0f;
+      dot += f[j] * pr[j];
     }
     dot = wave_sum(dot);
     float c = 0.0f;
-    int id = -1;
-    if (on && p.gw) {
-      float l = -INFINITY, gw = 0.0f;
-      if (lane < p.K) {
-        id = p.idx[(size_t)t * p.K + lane];
-        if (id < 0 || id >= E) id = -1;
-        if (id >= 0) {
-          l = p.logits[(size_t)t * E + id];
-          gw = p.gw[(size_t)t * p.K + lane];
-        }
+    if (p.gw) {
+      if (!on || id < 0 || id >= E) id = -1;
+      float lk = -INFINITY;  // the slot's logit, from the lane that holds its expert
+#pragma unroll
+      for (int j = 0; j < EJ; ++j) {
+        const float v = __shfl(l[j], id & 63);
+        if (id >= 0 && id >> 6 == j) lk = v;
       }
-      const float m = wave_max(l);
-      const float x = id >= 0 && m > -INFINITY ? expf(l - m) : 0.0f;
+      const float m = wave_max(lk);
+      const float x = id >= 0 && m > -INFINITY ? expf(lk - m) : 0.0f;
       const float s = wave_sum(x), w = s > 0.0f ? x / s : x;
       const float mean = wave_sum(id >= 0 ? w * gw : 0.0f);
       c = id >= 0 ? w * (gw - mean) : 0.0f;
     }
+    float d[EJ], most = 0.0f;
 #pragma unroll
     for (int j = 0; j < EJ; ++j) {
       const int e = lane + 64 * j;
-      if (e < Ep) {
-        float d = 0.0f;
-        if (e < E && on) d = pr[j] * (ca * (f[j] - dot) + cb * lse);
-        if (p.gw) {
-          for (int k = 0; k < p.K; ++k) {  // slots in order, also where one expert is named twice
-            const int ik = __shfl(id, k);
-            const float ck = __shfl(c, k);
-            if (ik == e) d += ck;
-          }
+      d[j] = on && e < E ? pr[j] * (ca * (f[j] - dot) + cb * lse) : 0.0f;
+      if (p.gw) {
+        for (int k = 0; k < p.K; ++k) {  // slots in order, also where one expert is named twice
+          const int ik = __shfl(id, k);
+          const float ck = __shfl(c, k);
+          if (ik == e) d[j] += ck;
         }
-        ds[r * row + e] = d;
       }
+      if (e < Ep) ds[r * row + e] = d[j];
+      most = fmaxf(most, fabsf(d[j]));
+    }
+    const float up = scale_for(wave_max(most));
+    if (lane == 0) {
+      scl[r] = up;
+      p.dl_s[t] = 1.0f / up;
     }
   }
   __syncthreads();
-  for (int i = tid; i < 32 * (Ep / 4); i += 1024) {
-    const int r = i / (Ep / 4), c = i % (Ep / 4) * 4;
-    *(fx4*)(p.dl + (size_t)(t0 + r) * Ep + c) = *(const fx4*)(ds + r * row + c);
+  const int kt = Ep / 32;
+  const size_t ta = (size_t)(p.Tp / 16) * kt;
+  for (int i = wave; i < 2 * kt; i += 16) {  // dl_a: 2 token tiles x kt expert tiles
+    const int m = i & 1, k32 = i >> 1;
+    hx8 q[2];
+    halves(load8(ds + (16 * m + n) * row + 32 * k32 + 8 * g) * scl[16 * m + n], q);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) *(hx8*)(p.dl_a + frag(ta, k, (size_t)(t0 / 16 + m) * kt + k32) + 8 * lane) = q[k];
   }
   const size_t tt = (size_t)(Ep / 16) * (p.Tp / 32);
   for (int et = wave; et < Ep / 16; et += 16) {  // dl_t: Ep / 16 expert tiles
@@ -376,93 +406,112 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
   }
 }
 
-// dX = dl W: a workgroup of 8 waves keeps the three parts of W of 128 columns
-// and up to 128 experts in LDS (96 KiB, cut once) and goes over its range of
-// tokens, 256 at a time; a wave holds 64 tokens x 64 columns and cuts dl as it
-// loads it. The columns are the products' rows, so that a lane ends with four
-// of a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so
-// that each L2 holds its own part of dl.
-constexpr int kDxLds = 3 * 8 * 4 * 1024;
-
-__global__ __launch_bounds__(512, 2) void k_router_dx(RouterLossParams p) {
-  extern __shared__ __align__(16) __bf16 wl[];  // [part][column / 16][expert / 32] fragments
+// dX = dl W: a workgroup keeps W of 64 columns and up to 128 experts in LDS, as
+// two fp16 halves (32 KiB, cut once, each column scaled by a power of two), and
+// goes over its range of tokens, 256 at a time; a wave holds 64 tokens x 64
+// columns. The columns are the products' rows, so that a lane ends with four of
+// a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so that
+// each L2 holds its own part of dl.
+__global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
+  __shared__ __align__(16) _Float16 wl[2 * 4 * 4 * 512];  // [half][column / 16][expert / 32] fragments
+  __shared__ __align__(16) float down[64];                // inverse scales of the columns
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int cols = (p.H + 127) / 128, blocks = (p.Tp + 255) / 256, kt = p.Ep / 32;
+  const int cols = p.H / 64, blocks = (p.Tp + 255) / 256, kt = p.Ep / 32;
+  const size_t ta = (size_t)(p.Tp / 16) * kt;
   int cg, range;
   xcd_pairs(blockIdx.x, cols, p.dx_ranges, cg, range);
-  const int h0 = cg * 128, half = wave & 1;
+  const int h0 = cg * 64;
   const int b0 = (int)((long long)blocks * range / p.dx_ranges), b1 = (int)((long long)blocks * (range + 1) / p.dx_ranges);
-  auto load_w = [&](int k0) {
-    for (int f = wave; f < 32; f += 8) {
-      const int c = f >> 2, k = f & 3, h = h0 + 16 * c + n;
-      fx8 v = (fx8)(0.0f);
+  const auto w_at = [&](int k) {  // column 16 wave + n, experts 32 k + 8 g ..
+    fx8 v;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 32 * (k0 + k) + 8 * g + i;
-        if (e < p.E && h < p.H) v[i] = p.W[(size_t)e * p.H + h];
-      }
-      bx8 q[3];
-      cut<3>(v, q);
+    for (int i = 0; i < 8; ++i) {
+      const int e = 32 * k + 8 * g + i;
+      v[i] = p.W[(size_t)(e < p.E ? e : 0) * p.H + h0 + 16 * wave + n];
+    }
 #pragma unroll
-      for (int i = 0; i < 3; ++i) *(bx8*)(wl + ((i * 8 + c) * 4 + k) * 512 + 8 * lane) = q[i];
+    for (int i = 0; i < 8; ++i) v[i] = 32 * k + 8 * g + i < p.E ? v[i] : 0.0f;
+    return v;
+  };
+  float up = 0.0f;
+  const auto load_w = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hx8 q[2];
+      halves(w_at(k0 + k) * up, q);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *(hx8*)(wl + ((i * 4 + wave) * 4 + k) * 512 + 8 * lane) = q[i];
     }
   };
-  if (kt <= 4) {
-    load_w(0);
-    __syncthreads();
-  }
-  const bool mine = h0 + 64 * half < p.H;
-  for (int b = b0; b < b1; ++b) {
-    const int t0 = b * 256 + (wave >> 1) * 64;
-    const bool work = mine && t0 < p.Tp;
-    acc4 acc[4][4];
+  hx8 d[4][2];  // dl of the next step
+  const auto load_d = [&](int b, int k) {
+    const int t0 = b * 256 + wave * 64, tile = (t0 < p.Tp ? t0 : 0) / 16;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) d[m][q] = *(const hx8*)(p.dl_a + frag(ta, q, (size_t)(tile + m) * kt + k) + 8 * lane);
+  };
+  load_d(b0, 0);
+  float most = 0.0f;
+  for (int k = 0; k < kt; ++k) {
+    const fx8 v = w_at(k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
+  }
+  most = fmaxf(most, __shfl_xor(most, 16));
+  most = fmaxf(most, __shfl_xor(most, 32));
+  up = scale_for(most);
+  if (g == 0) down[16 * wave + n] = 1.0f / up;
+  if (kt <= 4) load_w(0);
+  __syncthreads();
+  for (int b = b0; b < b1; ++b) {
+    const int t0 = b * 256 + wave * 64;
+    acc4 acc[4][4];
+    float ts[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int t = t0 + 16 * m + n;
+      ts[m] = t < p.T && p.on[t] ? p.dl_s[t] : 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[m][c] = (acc4)(0.0f);
-    for (int k0 = 0; k0 < kt; k0 += 4) {
-      if (kt > 4) {
+    }
+    for (int k = 0; k < kt; ++k) {
+      if (kt > 4 && k % 4 == 0) {
         __syncthreads();
-        load_w(k0);
+        load_w(k);
         __syncthreads();
       }
-      if (!work) continue;
-      const int kn = kt - k0 < 4 ? kt - k0 : 4;
-      const float* src = p.dl + (size_t)(t0 + n) * p.Ep + 32 * k0 + 8 * g;
-      fx8 d[4];
+      hx8 a[4][2];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) d[m] = load8(src + (size_t)(16 * m) * p.Ep);
-      for (int k = 0; k < kn; ++k) {
-        bx8 a[4][3];
+      for (int m = 0; m < 4; ++m) {
+        a[m][0] = d[m][0];
+        a[m][1] = d[m][1];
+      }
+      // the next step's dl, also across blocks: before the stores, which a later load would wait for
+      if (k + 1 < kt) load_d(b, k + 1);
+      else if (b + 1 < b1) load_d(b + 1, 0);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) cut<3>(d[m], a[m]);
-        if (k + 1 < kn) {
+      for (int c = 0; c < 4; ++c) {
+        hx8 w[2];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) d[m] = load8(src + (size_t)(16 * m) * p.Ep + 32 * (k + 1));
-        }
+        for (int i = 0; i < 2; ++i) w[i] = *(const hx8*)(wl + ((i * 4 + c) * 4 + k % 4) * 512 + 8 * lane);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          bx8 w[3];
+        for (int s = 0; s < 3; ++s)  // lo hi, hi lo, hi hi
 #pragma unroll
-          for (int i = 0; i < 3; ++i) w[i] = *(const bx8*)(wl + ((i * 8 + 4 * half + c) * 4 + k) * 512 + 8 * lane);
-#pragma unroll
-          for (int s = 2; s >= 0; --s)  // parts i, j with i + j = s: the smallest first
-#pragma unroll
-            for (int i = s; i >= 0; --i)
-#pragma unroll
-              for (int m = 0; m < 4; ++m) acc[m][c] = mfma(w[s - i], a[m][i], acc[m][c]);
-        }
+          for (int m = 0; m < 4; ++m)
+            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[s == 0], a[m][s == 1], acc[m][c], 0, 0, 0);
       }
     }
-    if (!work) continue;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = t0 + 16 * m + n;
       if (t < p.T) {
-        const bool on = p.on[t];
-        float* out = p.dX + (size_t)t * p.H + h0 + 64 * half + 4 * g;
+        float* out = p.dX + (size_t)t * p.H + h0 + 4 * g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) *(acc4*)(out + 16 * c) = on ? acc[m][c] : (acc4)(0.0f);
+        for (int c = 0; c < 4; ++c) {
+          const acc4 v = acc[m][c] * *(const acc4*)(down + 16 * c + 4 * g) * ts[m];
+          *(acc4*)(out + 16 * c) = ts[m] > 0.0f ? v : (acc4)(0.0f);
+        }
       }
     }
   }
@@ -617,13 +666,16 @@ RouterLossWs router_loss_ws(int T, int H, int E) {
   w.chunks = 256 / wt;
   if (w.chunks > nt / 8) w.chunks = nt / 8;
   if (w.chunks < 1) w.chunks = 1;
-  // ranges of tokens for dX: about 256 workgroups (one per CU), whole blocks of 256 tokens
-  const int blocks = (w.Tp + 255) / 256, cols = (H + 127) / 128;
-  w.dx_ranges = (256 + cols - 1) / cols;
+  // ranges of tokens for dX, whole blocks of 256 tokens: one block each up to
+  // 1024 workgroups, else 512 workgroups (two per CU)
+  const int blocks = (w.Tp + 255) / 256, cols = H / 64;
+  w.dx_ranges = blocks;
+  if ((long long)blocks * cols > 1024) w.dx_ranges = (512 + cols - 1) / cols;
   if (w.dx_ranges > blocks) w.dx_ranges = blocks;
   if (w.dx_ranges < 1) w.dx_ranges = 1;
   off = 0;
-  w.dl = off;      off += up256((size_t)w.Tp * w.Ep * 4);
+  w.dl_a = off;    off += up256((size_t)2 * w.Tp * w.Ep * 2);
+  w.dl_s = off;    off += up256((size_t)w.Tp * 4);
   w.dl_t = off;    off += up256((size_t)3 * w.Tp * w.Ep * 2);
   w.on = off;      off += up256((size_t)w.Tp);
   w.db_part = off; off += up256((size_t)(w.Tp / 32) * E * 4);
@@ -667,10 +719,7 @@ hipError_t launch_router_loss_grad(const RouterLossParams& p, bool bf16, hipStre
     else k_router_dl<8><<<dl_wgs, 1024, lds, s>>>(p);
   }
   if (p.dX) {
-    static unsigned long long dx_raised = 0;
-    const hipError_t e = raise_lds_limit((const void*)k_router_dx, kDxLds, dx_raised);
-    if (e != hipSuccess) return e;
-    k_router_dx<<<(p.H + 127) / 128 * p.dx_ranges, 512, kDxLds, s>>>(p);
+    k_router_dx<<<p.H / 64 * p.dx_ranges, 256, 0, s>>>(p);
   }
   int dw_wgs = 0;
   if (p.dW) {

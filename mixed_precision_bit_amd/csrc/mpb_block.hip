@@ -63,7 +63,8 @@ mpb::RouterLossParams router_params(const void* X, const float* W, const int32_t
   p.T = T; p.H = H; p.E = E; p.K = K; p.alpha = alpha; p.beta = beta;
   p.part = (float*)(ws + w.part);
   p.stat = (int2*)(ws + w.stat);
-  p.dl = (float*)(ws + w.dl);
+  p.dl_a = (uint16_t*)(ws + w.dl_a);
+  p.dl_s = (float*)(ws + w.dl_s);
   p.dl_t = (uint16_t*)(ws + w.dl_t);
   p.on = (uint8_t*)(ws + w.on);
   p.db_part = (float*)(ws + w.db_part);

@@ -270,8 +270,9 @@ struct RouterLossParams {
   // workspace
   float* part;           // [splits][T][E] partial logits
   int2* stat;            // [groups][E + 1] sums (fp32) and counts, see the kernel
-  float* dl;             // [Tp][Ep] gradients of the logits
-  uint16_t* dl_t;        // the same as operand fragments, see the kernel
+  uint16_t* dl_a;        // gradients of the logits as operand fragments for dX
+  uint16_t* dl_t;        // and for dW, see the kernels
+  float* dl_s;           // [Tp] inverse scales of dl_a
   uint8_t* on;           // [Tp] whether a token takes part
   float* db_part;        // [Tp / 32][E]
   float* dw_part;        // [chunks][E][H]
@@ -280,7 +281,7 @@ struct RouterLossParams {
 // Regions of the workspace (the forward and the backward pass each use all of
 // it) and the launch shapes they go with, from the sizes only.
 struct RouterLossWs {
-  size_t part, stat, dl, dl_t, on, db_part, dw_part, total;
+  size_t part, stat, dl_a, dl_t, dl_s, on, db_part, dw_part, total;
   int splits, groups, chunks, dx_ranges, Tp, Ep;  // Tp, Ep: T and E rounded up to 64
   int mt, et;                          // tiles of 16 tokens, of 64 experts of a logits workgroup
 };
