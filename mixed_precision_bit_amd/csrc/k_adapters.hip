@@ -41,24 +41,29 @@ __device__ __forceinline__ int rank_of(const AdapterParams& p, int a) {
   return r < 0 ? 0 : r < p.R ? r : p.R;
 }
 
-// The tile of a workgroup: its adapter and tokens (toks[i] = -1 past its end).
-// Returns the adapter (n: none), or -1 if there is no such tile.
-struct TileLds {
+// The tile of a workgroup: its adapter (n: none), the adapter's rank and its
+// tokens (toks[i] = -1 past its end).
+struct __align__(16) TileLds {
   int ids[kAdapterScanT];
   int toks[64];
   int waves[kAdapterScanT / 64];
-  int adapter;
+  int adapter, rank;
 };
 
+// Finds it; false if there is no such tile.
 template <int ROWS>
-__device__ __forceinline__ int find_tile(const AdapterParams& p, int tile, TileLds& s) {
+__device__ __forceinline__ bool find_tile(const AdapterParams& p, int tile, TileLds& s, int& adapter, int& rank) {
   const int tid = threadIdx.x;
   if (p.perm) {
-    if (tile >= p.tiles[0]) return -1;
-    const int* d = p.tiles + 4 + 4 * (size_t)tile;  // adapter, first, count
-    if (tid < ROWS) s.toks[tid] = tid < d[2] ? p.perm[d[1] + tid] : -1;
+    const int count = p.tiles[0];
+    const int* d = p.tiles + 4 + 4 * (size_t)tile;  // adapter, first, tokens, rank (within the list's room for any tile)
+    const int a = d[0], first = d[1], toks = d[2], r = d[3];
+    if (tile >= count) return false;
+    if (tid < ROWS) s.toks[tid] = tid < toks ? p.perm[first + tid] : -1;
+    adapter = a;
+    rank = r;
     __syncthreads();
-    return d[0];
+    return true;
   }
   // one thread per token: pos = earlier tokens of the same group; every ROWS-th
   // token of a group starts a tile, tiles numbered by their first token
@@ -66,23 +71,34 @@ __device__ __forceinline__ int find_tile(const AdapterParams& p, int tile, TileL
   s.ids[tid] = id;
   if (tid < 64) s.toks[tid] = -1;
   if (tid == 0) s.adapter = -1;
+  const int r = id >= 0 ? rank_of(p, id) : 0;  // on its way during the scan
   __syncthreads();
   int pos = 0;
-  for (int i = 0; i < p.T; ++i) pos += i < tid && s.ids[i] == id ? 1 : 0;
+  typedef int ix4 __attribute__((ext_vector_type(4)));
+#pragma unroll 4
+  for (int i = 0; i < p.T; i += 4) {
+    const ix4 v = *(const ix4*)&s.ids[i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pos += i + k < tid && v[k] == id ? 1 : 0;
+  }
   const bool first = id >= 0 && pos % ROWS == 0;
   const unsigned long long m = __ballot(first);
   if ((tid & 63) == 0) s.waves[tid >> 6] = __popcll(m);
   __syncthreads();
   int before = __popcll(m & ((1ull << (tid & 63)) - 1));
   for (int w = 0; w < (tid >> 6); ++w) before += s.waves[w];
-  if (first && before == tile) s.adapter = id | (pos / ROWS) << 16;
+  if (first && before == tile) {
+    s.adapter = id | (pos / ROWS) << 16;
+    s.rank = r;
+  }
   __syncthreads();
   const int found = s.adapter;
-  if (found < 0) return -1;
-  const int a = found & 0xffff, part = found >> 16;
-  if (id == a && pos / ROWS == part) s.toks[pos % ROWS] = tid;
+  if (found < 0) return false;
+  adapter = found & 0xffff;
+  rank = s.rank;
+  if (id == adapter && pos / ROWS == found >> 16) s.toks[pos % ROWS] = tid;
   __syncthreads();
-  return a;
+  return true;
 }
 
 // Counting sort of the tokens by group and the tile list, one workgroup. Lanes
@@ -138,12 +154,13 @@ __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
   }
   int first = ci - c, tile = ni - n;
   for (int g = g0; g < g1; ++g) {
-    const int k = cnt[g];
+    const int k = cnt[g], r = k ? rank_of(p, g) : 0;
     for (int i = 0; i < k; i += rows, ++tile) {
       int* d = p.tiles + 4 + 4 * (size_t)tile;
       d[0] = g;
       d[1] = first + i;
       d[2] = k - i < rows ? k - i : rows;
+      d[3] = r;
     }
     cnt[g] = first;
     first += k;
@@ -157,53 +174,61 @@ __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
   }
 }
 
-// z of one tile over one range of Kd. The four waves take steps of 32 in turn;
-// their sums meet in LDS in wave order. RT: rank tiles of 16.
+// z of one tile over one range of Kd. The waves take steps of 32 (wide tiles:
+// pairs of them, whole cache lines of x) in turn; their sums meet in LDS in wave
+// order. Wide tiles split Kd over 8 waves rather than over more ranges, whose
+// partial sums k_expand would have to read again for every 256 columns. RT: rank
+// tiles of 16.
+constexpr int shrink_waves(int MT) { return MT == 1 ? 4 : 8; }
+
 template <class D, int MT, int RT>
-__global__ __launch_bounds__(256) void k_shrink(AdapterParams p) {
+__global__ __launch_bounds__(64 * shrink_waves(MT)) void k_shrink(AdapterParams p) {
+  constexpr int NW = shrink_waves(MT), U = MT == 1 ? 1 : 2;
   typedef typename D::vec vec;
   typedef typename D::elem elem;
   __shared__ TileLds tl;
   __shared__ float sum[16 * MT][16 * RT + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int a = find_tile<16 * MT>(p, blockIdx.x, tl);
-  if (a < 0) return;
-  const int rank = rank_of(p, a);
-  if (rank == 0) return;
-  const int steps = p.Kd / 32, s0 = (int)((long long)steps * blockIdx.y / gridDim.y),
+  int a, rank;
+  if (!find_tile<16 * MT>(p, blockIdx.x, tl, a, rank) || rank == 0) return;
+  const int steps = p.Kd / (32 * U), s0 = (int)((long long)steps * blockIdx.y / gridDim.y),
             s1 = (int)((long long)steps * (blockIdx.y + 1) / gridDim.y);
-  int tok[MT];
+  // Loads are unconditional, so that those of several steps go out together:
+  // rows past the tile's end repeat its first token and rows past the rank the
+  // adapter's first row, and what they give is not used.
   const elem* x[MT];
+  const elem* w[RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    tok[m] = tl.toks[16 * m + n];
-    x[m] = (const elem*)p.X + (size_t)(tok[m] < 0 ? 0 : tok[m]) * p.Kd + 8 * g;
+    const int t = tl.toks[16 * m + n];
+    x[m] = (const elem*)p.X + (size_t)(t < 0 ? tl.toks[0] : t) * p.Kd + 8 * g;
   }
-  const elem* w = (const elem*)p.A + ((size_t)a * p.R + n) * p.Kd + 8 * g;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    w[r] = (const elem*)p.A + ((size_t)a * p.R + (16 * r + n < rank ? 16 * r + n : 0)) * p.Kd + 8 * g;
   acc4 acc[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[m][r] = (acc4)(0.0f);
-#pragma unroll 2
-  for (int s = s0 + wave; s < s1; s += 4) {
-    vec xv[MT], av[RT];
+#pragma unroll(MT == 1 ? 4 : 1)
+  for (int s = s0 + wave; s < s1; s += NW) {
+    vec xv[U][MT], av[U][RT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      xv[m] = (vec)(elem)0.0f;
-      if (tok[m] >= 0) xv[m] = *(const vec*)(x[m] + 32 * s);
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xv[u][m] = *(const vec*)(x[m] + 32 * (U * s + u));
+#pragma unroll
+      for (int r = 0; r < RT; ++r) av[u][r] = *(const vec*)(w[r] + 32 * (U * s + u));
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      av[r] = (vec)(elem)0.0f;
-      if (16 * r + n < rank) av[r] = *(const vec*)(w + (size_t)(16 * r) * p.Kd + 32 * s);
-    }
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[m][r] = mfma16(xv[m], av[r], acc[m][r]);
+        for (int r = 0; r < RT; ++r) acc[m][r] = mfma16(xv[u][m], av[u][r], acc[m][r]);
   }
-  for (int v = 0; v < 4; ++v) {
+  for (int v = 0; v < NW; ++v) {
     if (wave == v) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -218,7 +243,7 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterParams p) {
     __syncthreads();
   }
   float* z = p.z + (size_t)blockIdx.y * p.T * p.R;
-  for (int i = tid; i < 16 * MT * 16 * RT; i += 256) {
+  for (int i = tid; i < 16 * MT * 16 * RT; i += 64 * NW) {
     const int row = i / (16 * RT), r = i % (16 * RT), t = tl.toks[row];
     if (t >= 0 && r < p.R) z[(size_t)t * p.R + r] = sum[row][r];
   }
@@ -227,90 +252,121 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterParams p) {
 // out of one tile: a wave holds 16 tokens and 64 columns at a time. With MT = 4
 // the waves take the tile's four rows of 16 tokens, with MT = 1 the columns in
 // turn. RK: rank tiles of 32. The columns are the products' rows, so that a
-// lane ends with four consecutive columns of one token.
-constexpr int kExpandCols = 256;
+// lane ends with four consecutive columns of one token. The next 64 columns'
+// base and B are always on their way, in the other of two register sets: the
+// loop holds no condition and no copy, at which the compiler would wait for the
+// stores too (4093 x 2816, rank 64: 43 us with one).
+constexpr int kExpandCols = 512;
 
-template <class D, int MT, int RK>
+template <class D, int MT, int RK, bool BASE>
 __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
-  constexpr int NP = Parts<D>::N;
+  constexpr int NP = Parts<D>::N, kStep = MT == 4 ? 64 : 256;
   __shared__ TileLds tl;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int a = find_tile<16 * MT>(p, blockIdx.x, tl);
-  if (a < 0) return;
-  const int rank = rank_of(p, a);
+  int a, rank;
+  if (!find_tile<16 * MT>(p, blockIdx.x, tl, a, rank)) return;
   if (rank == 0 && p.base == p.out) return;
-  if (MT == 4 && tl.toks[16 * wave] < 0) return;  // this wave's rows are past the tile's end
-  const int t = tl.toks[(MT == 4 ? 16 * wave : 0) + n];
-  bx8 z[RK][3];
-  if (rank > 0) {
-    const float scale = p.scales ? p.scales[a] : 1.0f;
+  const int first = tl.toks[MT == 4 ? 16 * wave : 0], mine = tl.toks[(MT == 4 ? 16 * wave : 0) + n];
+  // Loads and stores are unconditional: rows past the tile's end repeat the
+  // wave's first token (and store its values again), ranks past the adapter's
+  // its first 8.
+  const int t = mine < 0 ? first : mine;
+  const int c0 = blockIdx.y * kExpandCols + (MT == 4 ? 0 : 64 * wave);
+  const int c1 = (int)(blockIdx.y + 1) * kExpandCols < p.N ? (int)(blockIdx.y + 1) * kExpandCols : p.N;
+  if (first < 0 || c0 >= c1) return;  // this wave's rows or columns are past the end
+  const size_t row = (size_t)t * p.N + 4 * g;
+  if (rank == 0) {  // no adapter
+    for (int c = c0; c < c1; c += kStep)
 #pragma unroll
-    for (int k = 0; k < RK; ++k) {
-      fx8 v = (fx8)(0.0f);
-      const int r = 32 * k + 8 * g;
-      if (t >= 0 && r < rank) {
-        const float* src = p.z + (size_t)t * p.R + r;
-        for (int s = 0; s < p.ranges; ++s) v += load8(src + (size_t)s * p.T * p.R);
+      for (int j = 0; j < 4; ++j)
+        *(acc4*)(p.out + row + (c + 16 * j)) = BASE ? *(const acc4*)(p.base + row + c + 16 * j) : (acc4)(0.0f);
+    return;
+  }
+  struct Cols {
+    acc4 base[4];
+    vec b[4][RK];
+  };
+  int kof[RK];
+  ux4 mask[RK];  // clears B's columns past the rank, which hold anything
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = r + i < rank ? v[i] * scale : 0.0f;
-      }
-      cut<3>(v, z[k]);
+  for (int k = 0; k < RK; ++k) {
+    kof[k] = 32 * k + 8 * g < rank ? 32 * k + 8 * g : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 32 * k + 8 * g + 2 * i;
+      mask[k][i] = (r < rank ? 0xffffu : 0u) | (r + 1 < rank ? 0xffff0000u : 0u);
     }
   }
-  const int c1 = (int)(blockIdx.y + 1) * kExpandCols < p.N ? (int)(blockIdx.y + 1) * kExpandCols : p.N;
-  for (int c = blockIdx.y * kExpandCols + (MT == 4 ? 0 : 64 * wave); c < c1; c += MT == 4 ? 64 : 256) {
-    acc4 acc[4];
-    const size_t at = (size_t)(t < 0 ? 0 : t) * p.N + c + 4 * g;
+  const elem* brow = (const elem*)p.B + ((size_t)a * p.N + n) * p.R;
+  const auto load = [&](int c, Cols& v) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      acc[j] = (acc4)(0.0f);
-      if (p.base && t >= 0) acc[j] = *(const acc4*)(p.base + at + 16 * j);
+      v.base[j] = BASE ? *(const acc4*)(p.base + row + c + 16 * j) : (acc4)(0.0f);
+#pragma unroll
+      for (int k = 0; k < RK; ++k) v.b[j][k] = *(const vec*)(brow + (size_t)(c + 16 * j) * p.R + kof[k]);
     }
-    if (rank > 0) {
+  };
+  Cols v0, v1;
+  load(c0, v0);
+  bx8 z[RK][3];
+  const float scale = p.scales ? p.scales[a] : 1.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc4 d = (acc4)(0.0f);
-        const elem* b = (const elem*)p.B + ((size_t)a * p.N + c + 16 * j + n) * p.R + 8 * g;
+  for (int k = 0; k < RK; ++k) {
+    fx8 v = (fx8)(0.0f);
+    const float* src = p.z + (size_t)t * p.R + kof[k];
+#pragma unroll 8
+    for (int s = 0; s < p.ranges; ++s) v += load8(src + (size_t)s * p.T * p.R);
 #pragma unroll
-        for (int k = 0; k < RK; ++k) {
-          vec v = (vec)(elem)0.0f;
-          const int r = 32 * k + 8 * g;
-          if (r < rank) {
-            v = *(const vec*)(b + 32 * k);
-            if (r + 8 > rank) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = r + i < rank ? v[i] : (elem)0.0f;
-            }
-          }
-          bx8 q[NP];
-          Parts<D>::of(v, q);
-#pragma unroll
-          for (int u = NP - 1; u >= 0; --u)
-#pragma unroll
-            for (int i = 2 - u; i >= 0; --i) d = mfma(q[u], z[k][i], d);
-        }
-        acc[j] += d;
-      }
-    }
-    if (t >= 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *(acc4*)(p.out + at + 16 * j) = acc[j];
-    }
+    for (int i = 0; i < 8; ++i) v[i] = 32 * k + 8 * g + i < rank ? v[i] * scale : 0.0f;
+    cut<3>(v, z[k]);
   }
+  const auto work = [&](int c, const Cols& v) {
+    acc4 d[4];
+#pragma unroll
+    for (int k = 0; k < RK; ++k) {
+      bx8 q[4][NP];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        Parts<D>::of(__builtin_bit_cast(vec, __builtin_bit_cast(ux4, v.b[j][k]) & mask[k]), q[j]);
+#pragma unroll
+      for (int u = NP - 1; u >= 0; --u)
+#pragma unroll
+        for (int i = 2 - u; i >= 0; --i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = mfma(q[j][u], z[k][i], k == 0 && u == NP - 1 && i == 2 - u ? (acc4)(0.0f) : d[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *(acc4*)(p.out + row + (c + 16 * j)) = v.base[j] + d[j];
+  };
+  const int last = c0 + (c1 - 1 - c0) / kStep * kStep;
+  for (int c = c0;; c += 2 * kStep) {
+    load(c + kStep < last ? c + kStep : last, v1);
+    work(c, v0);
+    if (c + kStep > last) break;
+    load(c + 2 * kStep < last ? c + 2 * kStep : last, v0);
+    work(c + kStep, v1);
+    if (c + 2 * kStep > last) break;
+  }
+}
+
+template <class D, int MT, bool BASE>
+void expand(const AdapterParams& p, dim3 grid, hipStream_t s) {
+  if (p.R <= 32) k_expand<D, MT, 1, BASE><<<grid, 256, 0, s>>>(p);
+  else if (p.R <= 64) k_expand<D, MT, 2, BASE><<<grid, 256, 0, s>>>(p);
+  else k_expand<D, MT, 4, BASE><<<grid, 256, 0, s>>>(p);
 }
 
 template <class D, int MT>
 void shrink_expand(const AdapterParams& p, int tiles, hipStream_t s) {
   const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + kExpandCols - 1) / kExpandCols);
-  if (p.R <= 16) k_shrink<D, MT, 1><<<gs, 256, 0, s>>>(p);
-  else if (p.R <= 32) k_shrink<D, MT, 2><<<gs, 256, 0, s>>>(p);
-  else if (p.R <= 64) k_shrink<D, MT, 4><<<gs, 256, 0, s>>>(p);
-  else k_shrink<D, MT, 8><<<gs, 256, 0, s>>>(p);
-  if (p.R <= 32) k_expand<D, MT, 1><<<ge, 256, 0, s>>>(p);
-  else if (p.R <= 64) k_expand<D, MT, 2><<<ge, 256, 0, s>>>(p);
-  else k_expand<D, MT, 4><<<ge, 256, 0, s>>>(p);
+  if (p.R <= 16) k_shrink<D, MT, 1><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
+  else if (p.R <= 32) k_shrink<D, MT, 2><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
+  else if (p.R <= 64) k_shrink<D, MT, 4><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
+  else k_shrink<D, MT, 8><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
+  if (p.base) expand<D, MT, true>(p, ge, s);
+  else expand<D, MT, false>(p, ge, s);
 }
 
 }  // namespace
@@ -322,8 +378,9 @@ AdapterWs adapter_ws(int T, int Kd, int n, int R) {
   w.mt = !w.scan && T / (n + 1) >= 32 ? 4 : 1;
   const int rows = 16 * w.mt;
   w.max_tiles = (n + 1 < T ? n + 1 : T) + T / rows;
-  // ranges of Kd: about 512 workgroups, at least 4 steps of 32 (one per wave) each
-  w.ranges = w.max_tiles > 0 ? 512 / w.max_tiles : 1;
+  // ranges of Kd: about 512 workgroups of 4 waves, or 192 of 8 for wide tiles, at
+  // least a step of 32 for each wave
+  w.ranges = w.max_tiles > 0 ? (w.mt == 4 ? 192 : 512) / w.max_tiles : 1;
   if (w.ranges > Kd / 128) w.ranges = Kd / 128;
   if (w.ranges > 16) w.ranges = 16;
   if (w.ranges < 1) w.ranges = 1;

@@ -646,7 +646,7 @@ RouterLossWs router_loss_ws(int T, int H, int E) {
   RouterLossWs w{};
   // 128-token tiles where the batch fills the chip with them, else 64
   w.mt = T >= 8192 ? 8 : 4;
-  w.et = E > 64 ? 2 : 1;
+  w.et = E > 64 && T >= 8192 ? 2 : 1;
   const int tiles = ((T + 16 * w.mt - 1) / (16 * w.mt)) * ((E + 64 * w.et - 1) / (64 * w.et));
   // ranges of H for the logits: about 512 workgroups, whole stages of 64
   w.splits = tiles > 0 ? 512 / tiles : 1;
