@@ -175,8 +175,8 @@ __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
 }
 
 // z of one tile over one range of Kd. The waves take steps of 32 (wide tiles:
-// pairs of them, whole cache lines of x) in turn; their sums meet in LDS in wave
-// order. Wide tiles split Kd over 8 waves rather than over more ranges, whose
+// pairs of them, whole cache lines of x) in turn; their sums meet in LDS in a
+// fixed order. Wide tiles split Kd over 8 waves rather than over more ranges, whose
 // partial sums k_expand would have to read again for every 256 columns. RT: rank
 // tiles of 16.
 constexpr int shrink_waves(int MT) { return MT == 1 ? 4 : 8; }
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(64 * shrink_waves(MT)) void k_shrink(AdapterParams 
   typedef typename D::vec vec;
   typedef typename D::elem elem;
   __shared__ TileLds tl;
-  __shared__ float sum[16 * MT][16 * RT + 1];
+  __shared__ float sum[4][16 * MT][16 * RT + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
   int a, rank;
   if (!find_tile<16 * MT>(p, blockIdx.x, tl, a, rank) || rank == 0) return;
@@ -228,15 +228,15 @@ __global__ __launch_bounds__(64 * shrink_waves(MT)) void k_shrink(AdapterParams 
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[m][r] = mfma16(xv[u][m], av[u][r], acc[m][r]);
   }
-  for (int v = 0; v < NW; ++v) {
-    if (wave == v) {
+  for (int v = 0; v < NW; v += 4) {  // wave w adds to sum w % 4
+    if (wave / 4 == v / 4) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float* at = &sum[16 * m + 4 * g + i][16 * r + n];
+            float* at = &sum[wave & 3][16 * m + 4 * g + i][16 * r + n];
             *at = v ? *at + acc[m][r][i] : acc[m][r][i];
           }
     }
@@ -245,18 +245,19 @@ __global__ __launch_bounds__(64 * shrink_waves(MT)) void k_shrink(AdapterParams 
   float* z = p.z + (size_t)blockIdx.y * p.T * p.R;
   for (int i = tid; i < 16 * MT * 16 * RT; i += 64 * NW) {
     const int row = i / (16 * RT), r = i % (16 * RT), t = tl.toks[row];
-    if (t >= 0 && r < p.R) z[(size_t)t * p.R + r] = sum[row][r];
+    if (t >= 0 && r < p.R) z[(size_t)t * p.R + r] = (sum[0][row][r] + sum[1][row][r]) + (sum[2][row][r] + sum[3][row][r]);
   }
 }
 
 // out of one tile: a wave holds 16 tokens and 64 columns at a time. With MT = 4
 // the waves take the tile's four rows of 16 tokens, with MT = 1 the columns in
 // turn. RK: rank tiles of 32. The columns are the products' rows, so that a
-// lane ends with four consecutive columns of one token. The next 64 columns'
-// base and B are always on their way, in the other of two register sets: the
-// loop holds no condition and no copy, at which the compiler would wait for the
-// stores too (4093 x 2816, rank 64: 43 us with one).
-constexpr int kExpandCols = 512;
+// lane has four consecutive columns of one token; the wave's sums then pass
+// through LDS, so that base and out are read and written 256 bytes of a row at a
+// time. The next 64 columns' base and B are always on their way, in the other of
+// two register sets: the loop holds no condition and no copy, at which the
+// compiler would wait for the stores too.
+constexpr int expand_cols(int MT) { return MT == 4 ? 512 : 1024; }
 
 template <class D, int MT, int RK, bool BASE>
 __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
@@ -264,24 +265,33 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   typedef typename D::elem elem;
   constexpr int NP = Parts<D>::N, kStep = MT == 4 ? 64 : 256;
   __shared__ TileLds tl;
+  __shared__ __align__(16) float turn[4][16][64 + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
   int a, rank;
   if (!find_tile<16 * MT>(p, blockIdx.x, tl, a, rank)) return;
   if (rank == 0 && p.base == p.out) return;
   const int first = tl.toks[MT == 4 ? 16 * wave : 0], mine = tl.toks[(MT == 4 ? 16 * wave : 0) + n];
-  // Loads and stores are unconditional: rows past the tile's end repeat the
-  // wave's first token (and store its values again), ranks past the adapter's
-  // its first 8.
+  // Loads are unconditional, and a wide tile's stores: rows past the tile's end
+  // repeat the wave's first token (and store its values again), ranks past the
+  // adapter's its first 8.
   const int t = mine < 0 ? first : mine;
-  const int c0 = blockIdx.y * kExpandCols + (MT == 4 ? 0 : 64 * wave);
-  const int c1 = (int)(blockIdx.y + 1) * kExpandCols < p.N ? (int)(blockIdx.y + 1) * kExpandCols : p.N;
+  const int c0 = blockIdx.y * expand_cols(MT) + (MT == 4 ? 0 : 64 * wave);
+  const int ce = (int)(blockIdx.y + 1) * expand_cols(MT), c1 = ce < p.N ? ce : p.N;
   if (first < 0 || c0 >= c1) return;  // this wave's rows or columns are past the end
-  const size_t row = (size_t)t * p.N + 4 * g;
+  // rows of memory accesses: token 4 i + g, columns 4 n ..
+  size_t row[4];
+  unsigned live = 0;  // narrow tiles, mostly of a few tokens, store no row twice
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int u = tl.toks[(MT == 4 ? 16 * wave : 0) + 4 * i + g];
+    row[i] = (size_t)(u < 0 ? first : u) * p.N + 4 * n;
+    live |= (u < 0 ? 0u : 1u) << (4 * i);
+  }
   if (rank == 0) {  // no adapter
     for (int c = c0; c < c1; c += kStep)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *(acc4*)(p.out + row + (c + 16 * j)) = BASE ? *(const acc4*)(p.base + row + c + 16 * j) : (acc4)(0.0f);
+      for (int i = 0; i < 4; ++i)
+        *(acc4*)(p.out + row[i] + c) = BASE ? *(const acc4*)(p.base + row[i] + c) : (acc4)(0.0f);
     return;
   }
   struct Cols {
@@ -303,7 +313,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   const auto load = [&](int c, Cols& v) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v.base[j] = BASE ? *(const acc4*)(p.base + row + c + 16 * j) : (acc4)(0.0f);
+      v.base[j] = BASE ? *(const acc4*)(p.base + row[j] + c) : (acc4)(0.0f);
 #pragma unroll
       for (int k = 0; k < RK; ++k) v.b[j][k] = *(const vec*)(brow + (size_t)(c + 16 * j) * p.R + kof[k]);
     }
@@ -337,8 +347,16 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) d[j] = mfma(q[j][u], z[k][i], k == 0 && u == NP - 1 && i == 2 - u ? (acc4)(0.0f) : d[j]);
     }
+    // one wave's LDS accesses run in order
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *(acc4*)(p.out + row + (c + 16 * j)) = v.base[j] + d[j];
+    for (int j = 0; j < 4; ++j) *(acc4*)&turn[wave][n][16 * j + 4 * g] = d[j];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const acc4 sum = v.base[i] + *(const acc4*)&turn[wave][4 * i + g][4 * n];
+      if (MT == 4 || live >> (4 * i) & 1) *(acc4*)(p.out + row[i] + c) = sum;
+    }
+    __builtin_amdgcn_wave_barrier();
   };
   const int last = c0 + (c1 - 1 - c0) / kStep * kStep;
   for (int c = c0;; c += 2 * kStep) {
@@ -360,7 +378,7 @@ void expand(const AdapterParams& p, dim3 grid, hipStream_t s) {
 
 template <class D, int MT>
 void shrink_expand(const AdapterParams& p, int tiles, hipStream_t s) {
-  const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + kExpandCols - 1) / kExpandCols);
+  const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + expand_cols(MT) - 1) / expand_cols(MT));
   if (p.R <= 16) k_shrink<D, MT, 1><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else if (p.R <= 32) k_shrink<D, MT, 2><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else if (p.R <= 64) k_shrink<D, MT, 4><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
@@ -378,9 +396,9 @@ AdapterWs adapter_ws(int T, int Kd, int n, int R) {
   w.mt = !w.scan && T / (n + 1) >= 32 ? 4 : 1;
   const int rows = 16 * w.mt;
   w.max_tiles = (n + 1 < T ? n + 1 : T) + T / rows;
-  // ranges of Kd: about 512 workgroups of 4 waves, or 192 of 8 for wide tiles, at
+  // ranges of Kd: about 512 workgroups of 4 waves, or 320 of 8 for wide tiles, at
   // least a step of 32 for each wave
-  w.ranges = w.max_tiles > 0 ? (w.mt == 4 ? 192 : 512) / w.max_tiles : 1;
+  w.ranges = w.max_tiles > 0 ? (w.mt == 4 ? 320 : 512) / w.max_tiles : 1;
   if (w.ranges > Kd / 128) w.ranges = Kd / 128;
   if (w.ranges > 16) w.ranges = 16;
   if (w.ranges < 1) w.ranges = 1;

@@ -140,16 +140,7 @@ __global__ __launch_bounds__(THREADS) void k_block_norm_grad(BlockNormGradParams
   fx8 gp[NV], gn[NV];  // column sums of dg_post, dg_next
 #pragma unroll
   for (int j = 0; j < NV; ++j) gp[j] = gn[j] = (fx8)(0.0f);
-  GradRow<D, NV> ahead;
-  if (AHEAD) ahead.load(p, blockIdx.x);
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-    GradRow<D, NV> in;
-    if (AHEAD) {
-      in = ahead;
-      if (t + (int)gridDim.x < p.T) ahead.load(p, t + gridDim.x);
-    } else {
-      in.load(p, t);
-    }
+  const auto work = [&](int t, const GradRow<D, NV>& in) {
     const size_t row = (size_t)t * p.H;
     float s1[3] = {0.0f, 0.0f, 0.0f};  // sums of y^2, d y, o^2
 #pragma unroll
@@ -221,6 +212,27 @@ __global__ __launch_bounds__(THREADS) void k_block_norm_grad(BlockNormGradParams
         const int v = tid + j * nt;
         if (v < nvec) store8(p.d_o + row + 8 * v, post ? (dw[j] - in.o[j] * mo) * ro : dw[j]);
       }
+    }
+  };
+  GradRow<D, NV> in;
+  if (AHEAD) {
+    // two register sets in turn (a copy from one to the other would wait for the
+    // row's stores as well); past the last row the last one is loaded again
+    GradRow<D, NV> in2;
+    const int step = gridDim.x, last = blockIdx.x + (p.T - 1 - blockIdx.x) / step * step;
+    in.load(p, blockIdx.x);
+    for (int t = blockIdx.x;; t += 2 * step) {
+      in2.load(p, t + step < last ? t + step : last);
+      work(t, in);
+      if (t + step > last) break;
+      in.load(p, t + 2 * step < last ? t + 2 * step : last);
+      work(t + step, in2);
+      if (t + 2 * step > last) break;
+    }
+  } else {
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+      in.load(p, t);
+      work(t, in);
     }
   }
 #pragma unroll

@@ -17,6 +17,8 @@
 // in fp32, and only products below 2^-24 of the whole are left out (dX takes
 // fp16 halves instead, see halves). Against the fp32 matrix instructions (1/16
 // of the 16-bit rate) three to five products are still 3 to 5 times cheaper.
+#include <type_traits>
+
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -464,14 +466,17 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
   if (g == 0) down[16 * wave + n] = 1.0f / up;
   if (kt <= 4) load_w(0);
   __syncthreads();
-  for (int b = b0; b < b1; ++b) {
+  // FULL: every token of the block is below T, so that nothing stands between the
+  // stores and the next block's products but a wait for its dl, loaded before them
+  const auto block = [&](int b, auto FULL) {
     const int t0 = b * 256 + wave * 64;
     acc4 acc[4][4];
     float ts[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = t0 + 16 * m + n;
-      ts[m] = t < p.T && p.on[t] ? p.dl_s[t] : 0.0f;
+      ts[m] = 0.0f;
+      if (FULL.value || t < p.Tp) ts[m] = p.on[t] ? p.dl_s[t] : 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[m][c] = (acc4)(0.0f);
     }
@@ -487,9 +492,8 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
         a[m][0] = d[m][0];
         a[m][1] = d[m][1];
       }
-      // the next step's dl, also across blocks: before the stores, which a later load would wait for
-      if (k + 1 < kt) load_d(b, k + 1);
-      else if (b + 1 < b1) load_d(b + 1, 0);
+      const bool same = k + 1 < kt;
+      load_d(same || b + 1 >= b1 ? b : b + 1, same ? k + 1 : 0);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         hx8 w[2];
@@ -505,7 +509,7 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = t0 + 16 * m + n;
-      if (t < p.T) {
+      if (FULL.value || t < p.T) {
         float* out = p.dX + (size_t)t * p.H + h0 + 4 * g;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -514,7 +518,10 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
         }
       }
     }
-  }
+  };
+  int b = b0;
+  for (; b < b1 && (b + 1) * 256 <= p.T; ++b) block(b, std::true_type{});
+  if (b < b1) block(b, std::false_type{});
 }
 
 // dW = dl^T X: a workgroup holds 64 experts x 128 columns over one range of
