@@ -3,7 +3,7 @@
 //
 // Tokens are gathered by adapter into tiles of up to 16 MT tokens of one
 // adapter, so that an adapter's weights are read once per tile:
-//   k_plan     (batches above kScanT) counting sort of the tokens by adapter,
+//   k_plan     (batches above kAdapterScanT) counting sort of the tokens by adapter,
 //              and the tile list; smaller batches are gathered by every
 //              workgroup for itself, which costs less than a launch
 //   k_shrink   z = A_a x for a tile over one range of Kd; the partial sums go
@@ -54,12 +54,12 @@ struct __align__(16) TileLds {
 template <int ROWS>
 __device__ __forceinline__ bool find_tile(const AdapterParams& p, int tile, TileLds& s, int& adapter, int& rank) {
   const int tid = threadIdx.x;
-  if (p.perm) {
+  if (p.perm) {  // within the lists' room for any tile
     const int count = p.tiles[0];
-    const int* d = p.tiles + 4 + 4 * (size_t)tile;  // adapter, first, tokens, rank (within the list's room for any tile)
-    const int a = d[0], first = d[1], toks = d[2], r = d[3];
+    const int* d = p.tiles + 4 + 2 * (size_t)tile;  // adapter, rank
+    const int a = d[0], r = d[1], t = tid < ROWS ? p.perm[(size_t)tile * ROWS + tid] : -1;
     if (tile >= count) return false;
-    if (tid < ROWS) s.toks[tid] = tid < toks ? p.perm[first + tid] : -1;
+    if (tid < ROWS) s.toks[tid] = t;
     adapter = a;
     rank = r;
     __syncthreads();
@@ -106,7 +106,7 @@ __device__ __forceinline__ bool find_tile(const AdapterParams& p, int tile, Tile
 // request's tokens would otherwise meet at one counter).
 __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
   __shared__ int cnt[kAdapterMaxN + 1];
-  __shared__ int wsum[2][16];
+  __shared__ int wsum[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = p.n + 1;
   for (int i = tid; i < G; i += 1024) cnt[i] = 0;
   __syncthreads();
@@ -127,43 +127,28 @@ __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
   };
   for (int t = tid; t < T64; t += 1024) take(t < p.T ? group_of(p, t) : -1);
   __syncthreads();
-  // first token and first tile of each group: a thread scans a run of groups
+  // first tile of each group: a thread scans a run of groups
   const int per = (G + 1023) / 1024, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
-  int c = 0, n = 0;
-  for (int g = g0; g < g1; ++g) {
-    c += cnt[g];
-    n += (cnt[g] + rows - 1) / rows;
-  }
-  int ci = c, ni = n;  // inclusive over the wave
+  int n = 0;
+  for (int g = g0; g < g1; ++g) n += (cnt[g] + rows - 1) / rows;
+  int ni = n;  // inclusive over the wave
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int a = __shfl_up(ci, d), b = __shfl_up(ni, d);
-    if (lane >= d) {
-      ci += a;
-      ni += b;
-    }
+    const int b = __shfl_up(ni, d);
+    if (lane >= d) ni += b;
   }
-  if (lane == 63) {
-    wsum[0][wave] = ci;
-    wsum[1][wave] = ni;
-  }
+  if (lane == 63) wsum[wave] = ni;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    ci += wsum[0][w];
-    ni += wsum[1][w];
-  }
-  int first = ci - c, tile = ni - n;
+  for (int w = 0; w < wave; ++w) ni += wsum[w];
+  int tile = ni - n;
   for (int g = g0; g < g1; ++g) {
     const int k = cnt[g], r = k ? rank_of(p, g) : 0;
+    cnt[g] = tile * rows;  // the group's first place
     for (int i = 0; i < k; i += rows, ++tile) {
-      int* d = p.tiles + 4 + 4 * (size_t)tile;
-      d[0] = g;
-      d[1] = first + i;
-      d[2] = k - i < rows ? k - i : rows;
-      d[3] = r;
+      p.tiles[4 + 2 * tile] = g;
+      p.tiles[5 + 2 * tile] = r;
     }
-    cnt[g] = first;
-    first += k;
+    for (int i = cnt[g] + k; i < tile * rows; ++i) p.perm[i] = -1;  // places past the last tile's end
   }
   if (tid == 1023) p.tiles[0] = ni;
   __syncthreads();
@@ -409,8 +394,8 @@ AdapterWs adapter_ws(int T, int Kd, int n, int R) {
     return at;
   };
   w.z = take((size_t)w.ranges * T * R * 4);
-  w.perm = take(w.scan ? 0 : (size_t)T * 4);
-  w.tiles = take(w.scan ? 0 : ((size_t)w.max_tiles + 1) * 16);
+  w.perm = take(w.scan ? 0 : (size_t)w.max_tiles * rows * 4);
+  w.tiles = take(w.scan ? 0 : ((size_t)w.max_tiles * 2 + 4) * 4);
   w.total = off < 256 ? 256 : off;
   return w;
 }

@@ -42,10 +42,29 @@ __device__ __forceinline__ void store8(float* p, fx8 v) {
   *(fx4*)(p + 4) = fx4{v[4], v[5], v[6], v[7]};
 }
 
+// v of another lane: DPP patterns within rows of 16 lanes (a register move,
+// where a shuffle goes through the LDS unit).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// op over the wave, the same bits in every lane: pairs, quads, 8, 16 lanes by
+// DPP (quad permutes, then mirrors), 32 and 64 by shuffles.
+template <class Op>
+__device__ __forceinline__ float wave_all(float v, Op op) {
+  v = op(v, dpp<0xb1>(v));   // quad_perm 1 0 3 2
+  v = op(v, dpp<0x4e>(v));   // quad_perm 2 3 0 1
+  v = op(v, dpp<0x141>(v));  // row_half_mirror
+  v = op(v, dpp<0x140>(v));  // row_mirror
+  v = op(v, __shfl_xor(v, 16));
+  return op(v, __shfl_xor(v, 32));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+  return wave_all(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Sums of N values over the workgroup, the same bits in every thread (each

@@ -146,12 +146,6 @@ __global__ __launch_bounds__(256, 2) void k_router_logits(RouterLossParams p) {
 }
 
 // ---------------------------------------------------------------- softmax, counts
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
-}
-
 // One wave per token: adds the ranges of H, writes logits and lse, and keeps
 // its share of P_e, z and N in registers; a workgroup (16 waves) writes one row
 // of them to stat [groups][E + 1] (sum and count of each expert, then z and N).
@@ -365,8 +359,8 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
       d[j] = on && e < E ? pr[j] * (ca * (f[j] - dot) + cb * lse) : 0.0f;
       if (p.gw) {
         for (int k = 0; k < p.K; ++k) {  // slots in order, also where one expert is named twice
-          const int ik = __shfl(id, k);
-          const float ck = __shfl(c, k);
+          const int ik = __builtin_amdgcn_readlane(id, k);
+          const float ck = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(c), k));
           if (ik == e) d[j] += ck;
         }
       }
@@ -417,6 +411,7 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
 __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
   __shared__ __align__(16) _Float16 wl[2 * 4 * 4 * 512];  // [half][column / 16][expert / 32] fragments
   __shared__ __align__(16) float down[64];                // inverse scales of the columns
+  __shared__ __align__(16) float turn[4][16][64 + 4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   const int cols = p.H / 64, blocks = (p.Tp + 255) / 256, kt = p.Ep / 32;
   const size_t ta = (size_t)(p.Tp / 16) * kt;
@@ -506,17 +501,21 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
             acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[s == 0], a[m][s == 1], acc[m][c], 0, 0, 0);
       }
     }
+    // through LDS (one wave's accesses run in order), to store whole lines
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int t = t0 + 16 * m + n;
-      if (FULL.value || t < p.T) {
-        float* out = p.dX + (size_t)t * p.H + h0 + 4 * g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const acc4 v = acc[m][c] * *(const acc4*)(down + 16 * c + 4 * g) * ts[m];
-          *(acc4*)(out + 16 * c) = ts[m] > 0.0f ? v : (acc4)(0.0f);
-        }
+      for (int c = 0; c < 4; ++c) {
+        const acc4 v = acc[m][c] * *(const acc4*)(down + 16 * c + 4 * g) * ts[m];
+        *(acc4*)&turn[wave][n][16 * c + 4 * g] = ts[m] > 0.0f ? v : (acc4)(0.0f);
       }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 16 * m + 4 * i + g;
+        if (FULL.value || t < p.T) *(acc4*)(p.dX + (size_t)t * p.H + h0 + 4 * n) = *(const acc4*)&turn[wave][4 * i + g][4 * n];
+      }
+      __builtin_amdgcn_wave_barrier();
     }
   };
   int b = b0;

@@ -303,8 +303,8 @@ struct AdapterParams {
   float* out;              // [T][N]
   int T, Kd, N, n, R;
   float* z;                // [ranges][T][R]
-  int32_t* perm;           // [T] tokens by adapter, or null (no plan)
-  int32_t* tiles;          // count, then 4 words per tile: adapter, first, tokens
+  int32_t* perm;           // [tiles][16 mt] tokens of each tile (-1 past its end), or null (no plan)
+  int32_t* tiles;          // count, 3 unused words, then each tile's adapter and rank
   int ranges;
 };
 struct AdapterWs {
