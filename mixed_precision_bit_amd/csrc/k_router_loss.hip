@@ -214,54 +214,72 @@ __global__ __launch_bounds__(1024) void k_router_stats(RouterLossParams p) {
   }
 }
 
-// Adds the groups' rows (fp64, group order per slice, slices in order) and
-// forms the losses. One workgroup.
+// Adds the groups' rows (fp64; 16 slices in group order, then the slices in
+// order) and forms the losses. One workgroup; every load of a thread is
+// independent of the others. EJ: columns of 64.
+template <int EJ>
 __global__ __launch_bounds__(1024) void k_router_finish(RouterLossParams p) {
-  __shared__ double fs[1024];
-  __shared__ int is[1024];
-  __shared__ double zsum;
-  __shared__ int nlive;
-  const int tid = threadIdx.x, E = p.E, W = E + 1;
-  double part = 0.0;
-  // columns of 64, 16 slices of the groups each
-  for (int c0 = 0; c0 < W; c0 += 64) {
-    const int c = c0 + (tid & 63), sl = tid >> 6;
-    double f = 0.0;
-    int n = 0;
-    if (c < W) {
-#pragma unroll 8
-      for (int i = sl; i < p.groups; i += 16) {
-        const int2 v = p.stat[(size_t)i * W + c];
-        f += (double)__int_as_float(v.x);
-        n += v.y;
-      }
-    }
-    fs[tid] = f;
-    is[tid] = n;
-    __syncthreads();
-    if (tid < 64 && c < W) {
-      for (int k = 1; k < 16; ++k) {
-        f += fs[tid + 64 * k];
-        n += is[tid + 64 * k];
-      }
-      p.counts[c] = n;
-      if (c < E) {
-        p.prob[c] = (float)f;
-        part += f * (double)n;
-      } else {
-        zsum = f;
-        nlive = n;
-      }
-    }
-    __syncthreads();
-  }
-  if (tid < 64) {
+  __shared__ double fs[16][64];
+  __shared__ int is[16][64];
+  const int tid = threadIdx.x, lane = tid & 63, sl = tid >> 6, E = p.E, W = E + 1;
+  // z and N: the last column, one group a thread (at most 256 groups)
+  const int2 last = tid < p.groups ? p.stat[(size_t)tid * W + E] : make_int2(0, 0);
+  double f[EJ];
+  int n[EJ];
 #pragma unroll
-    for (int m = 32; m; m >>= 1) part += __shfl_xor(part, m);
+  for (int j = 0; j < EJ; ++j) {
+    f[j] = 0.0;
+    n[j] = 0;
   }
+#pragma unroll 4
+  for (int i = sl; i < p.groups; i += 16) {
+#pragma unroll
+    for (int j = 0; j < EJ; ++j) {
+      const int2 v = p.stat[(size_t)i * W + (lane + 64 * j < E ? lane + 64 * j : 0)];
+      f[j] += (double)__int_as_float(v.x);
+      n[j] += v.y;
+    }
+  }
+  double part = 0.0;
+#pragma unroll
+  for (int j = 0; j < EJ; ++j) {
+    fs[sl][lane] = f[j];
+    is[sl][lane] = n[j];
+    __syncthreads();
+    if (sl == 0 && lane + 64 * j < E) {
+      for (int k = 1; k < 16; ++k) {
+        f[j] += fs[k][lane];
+        n[j] += is[k][lane];
+      }
+      p.counts[lane + 64 * j] = n[j];
+      p.prob[lane + 64 * j] = (float)f[j];
+      part += f[j] * (double)n[j];
+    }
+    __syncthreads();
+  }
+  // wave 0: sum over the experts; waves 0..3: z and N over the groups
+  double z = (double)__int_as_float(last.x);
+  int live = last.y;
+#pragma unroll
+  for (int m = 32; m; m >>= 1) {
+    part += __shfl_xor(part, m);
+    z += __shfl_xor(z, m);
+    live += __shfl_xor(live, m);
+  }
+  if (lane == 0) {
+    fs[sl][0] = z;
+    is[sl][0] = live;
+  }
+  __syncthreads();
   if (tid == 0) {
-    const double N = nlive > 0 ? (double)nlive : 1.0;
-    const double bal = (double)E * part / ((double)p.K * N * N), z = zsum / N;
+    for (int k = 1; k < 4; ++k) {
+      z += fs[k][0];
+      live += is[k][0];
+    }
+    p.counts[E] = live;
+    const double N = live > 0 ? (double)live : 1.0;
+    const double bal = (double)E * part / ((double)p.K * N * N);
+    z /= N;
     p.loss[0] = (float)((double)p.alpha * bal + (double)p.beta * z);
     p.loss[1] = (float)bal;
     p.loss[2] = (float)z;
@@ -704,10 +722,16 @@ hipError_t launch_router_loss(const RouterLossParams& p, bool bf16, hipStream_t 
     if (bf16) logits<BF16>(p, s);
     else logits<F16>(p, s);
   }
-  if (p.E <= 64) k_router_stats<1><<<p.groups, 1024, 0, s>>>(p);
-  else if (p.E <= 128) k_router_stats<2><<<p.groups, 1024, 0, s>>>(p);
-  else k_router_stats<8><<<p.groups, 1024, 0, s>>>(p);
-  k_router_finish<<<1, 1024, 0, s>>>(p);
+  if (p.E <= 64) {
+    k_router_stats<1><<<p.groups, 1024, 0, s>>>(p);
+    k_router_finish<1><<<1, 1024, 0, s>>>(p);
+  } else if (p.E <= 128) {
+    k_router_stats<2><<<p.groups, 1024, 0, s>>>(p);
+    k_router_finish<2><<<1, 1024, 0, s>>>(p);
+  } else {
+    k_router_stats<8><<<p.groups, 1024, 0, s>>>(p);
+    k_router_finish<8><<<1, 1024, 0, s>>>(p);
+  }
   return hipGetLastError();
 }
 
