@@ -210,6 +210,11 @@ _XT = {MPB_F16: torch.float16, MPB_BF16: torch.bfloat16}
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 
+# the current stream's handle without a Stream object around it, where this torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Args:
     """Checks the tensors of one call against the shapes and types the C entry
     takes them for (a C caller answers for these itself) and hands out their
@@ -225,6 +230,8 @@ class _Args:
     def __call__(self, what, t, dtype, *shape):
         if t is None:
             return None
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr()
         if t.dtype is not dtype and not (dtype.itemsize == 2 and t.dtype is torch.int16):
             self.fail(f"{what} is {t.dtype}, not {dtype}")
         if t.shape != shape:
@@ -252,7 +259,7 @@ class _Args:
         return self.call(fn, stream, args)
 
     def call(self, fn, stream, args):
-        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        rc = fn(*args, _raw_stream(self.index) if stream is None else stream.cuda_stream)
         return rc if rc >= 0 else _check(self.name, rc)
 
 
