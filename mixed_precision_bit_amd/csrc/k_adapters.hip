@@ -3,9 +3,11 @@
 //
 // Tokens are gathered by adapter into tiles of up to 16 MT tokens of one
 // adapter, so that an adapter's weights are read once per tile:
-//   k_plan     (batches above kAdapterScanT) counting sort of the tokens by adapter,
-//              and the tile list; smaller batches are gathered by every
-//              workgroup for itself, which costs less than a launch
+//   k_plan     (batches above kAdapterScanT = 64) counting sort of the tokens by
+//              adapter, and the tile list; smaller batches are gathered by every
+//              workgroup for itself: 16.6 us against 17.3 and a launch for 64
+//              tokens of 64 adapters, 9.7 against 11.9 for one; from 128 the
+//              scan costs more (21.4 against 18.9)
 //   k_shrink   z = A_a x for a tile over one range of Kd; the partial sums go
 //              to z [range][T][R] in fp32
 //   k_expand   z's ranges added in order, scaled, and multiplied by B_a; base
@@ -16,6 +18,12 @@
 // rounded below fp32. A token's arithmetic does not depend on the tile it is
 // in: its results are the same in any batch of the same launch shape.
 // Rows past an adapter's rank are never read, columns past it never used.
+//
+// 128 tokens of 64 adapters, 4096 x 4096, ranks up to 32: plan 4.0, shrink 6.3,
+// expand 8.6 us, bound by chains of latencies (the tile's tokens, its operands,
+// the sums). 4093 tokens of 16 adapters, 2816 x 2816, ranks up to 64: plan 6.4,
+// shrink 19.7, expand 33.7 us; the last moves 92 MB of base and out and reads B
+// through the cache, 16 bytes a cycle (a fragment's lanes lie in 16 rows).
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -46,9 +54,9 @@ __device__ __forceinline__ int rank_of(const AdapterParams& p, int a) {
 struct __align__(16) TileLds {
   int ids[kAdapterScanT];
   int toks[64];
-  int waves[kAdapterScanT / 64];
   int adapter, rank;
 };
+static_assert(kAdapterScanT == 64, "one wave scans the batch");
 
 // Finds it; false if there is no such tile.
 template <int ROWS>
@@ -65,67 +73,81 @@ __device__ __forceinline__ bool find_tile(const AdapterParams& p, int tile, Tile
     __syncthreads();
     return true;
   }
-  // one thread per token: pos = earlier tokens of the same group; every ROWS-th
-  // token of a group starts a tile, tiles numbered by their first token
-  const int id = tid < p.T ? group_of(p, tid) : -1;
-  s.ids[tid] = id;
-  if (tid < 64) s.toks[tid] = -1;
-  if (tid == 0) s.adapter = -1;
-  const int r = id >= 0 ? rank_of(p, id) : 0;  // on its way during the scan
-  __syncthreads();
-  int pos = 0;
-  typedef int ix4 __attribute__((ext_vector_type(4)));
+  // the first wave, a lane per token: pos = earlier tokens of the same group;
+  // every ROWS-th token of a group starts a tile, tiles numbered by their first token
+  if (tid < 64) {
+    const int id = tid < p.T ? group_of(p, tid) : -1;
+    const int r = id >= 0 ? rank_of(p, id) : 0;  // on its way during the scan
+    s.ids[tid] = id;
+    s.toks[tid] = -1;
+    if (tid == 0) s.adapter = -1;
+    __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses run in order
+    int pos = 0;
+    typedef int ix4 __attribute__((ext_vector_type(4)));
 #pragma unroll 4
-  for (int i = 0; i < p.T; i += 4) {
-    const ix4 v = *(const ix4*)&s.ids[i];
+    for (int i = 0; i < p.T; i += 4) {
+      const ix4 v = *(const ix4*)&s.ids[i];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) pos += i + k < tid && v[k] == id ? 1 : 0;
+      for (int k = 0; k < 4; ++k) pos += i + k < tid && v[k] == id ? 1 : 0;
+    }
+    const bool first = id >= 0 && pos % ROWS == 0;
+    const unsigned long long m = __ballot(first);
+    const bool lead = first && __popcll(m & ((1ull << tid) - 1)) == tile;
+    const unsigned long long at = __ballot(lead);
+    if (at) {
+      const int l = __ffsll(at) - 1, a = __shfl(id, l), part = __shfl(pos, l) / ROWS;
+      if (id == a && pos / ROWS == part) s.toks[pos % ROWS] = tid;
+      if (lead) {
+        s.adapter = id;
+        s.rank = r;
+      }
+    }
   }
-  const bool first = id >= 0 && pos % ROWS == 0;
-  const unsigned long long m = __ballot(first);
-  if ((tid & 63) == 0) s.waves[tid >> 6] = __popcll(m);
   __syncthreads();
-  int before = __popcll(m & ((1ull << (tid & 63)) - 1));
-  for (int w = 0; w < (tid >> 6); ++w) before += s.waves[w];
-  if (first && before == tile) {
-    s.adapter = id | (pos / ROWS) << 16;
-    s.rank = r;
-  }
-  __syncthreads();
-  const int found = s.adapter;
-  if (found < 0) return false;
-  adapter = found & 0xffff;
+  adapter = s.adapter;
   rank = s.rank;
-  if (id == adapter && pos / ROWS == found >> 16) s.toks[pos % ROWS] = tid;
-  __syncthreads();
-  return true;
+  return adapter >= 0;
 }
 
-// Counting sort of the tokens by group and the tile list, one workgroup. Lanes
-// of one wave with the same group take their places together (runs of one
-// request's tokens would otherwise meet at one counter).
+// Counting sort of the tokens by group and the tile list, one workgroup: two
+// passes over the ids, eight of a thread's loads at once. A wave whose lanes all
+// hold one group (a run of one request's tokens) takes its places together; the
+// lanes of others meet at the LDS counters. The order of tokens within a tile is
+// whatever the counters give and changes no result.
+constexpr int kPlanIds = 8;
+
 __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
   __shared__ int cnt[kAdapterMaxN + 1];
   __shared__ int wsum[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = p.n + 1;
   for (int i = tid; i < G; i += 1024) cnt[i] = 0;
   __syncthreads();
-  const int T64 = (p.T + 63) / 64 * 64;
-  auto take = [&](int id) {  // this lane's place among the tokens of its group
-    int at = 0;
-    unsigned long long todo = __ballot(id >= 0);
-    while (todo) {
-      const int lead = __ffsll(todo) - 1, g = __shfl(id, lead);
-      const unsigned long long same = __ballot(id == g);
-      int base = 0;
-      if (lane == lead) base = atomicAdd(&cnt[g], __popcll(same));
-      base = __shfl(base, lead);
-      if (id == g) at = base + __popcll(same & ((1ull << lane) - 1));
-      todo &= ~same;
+  const auto load = [&](int t0, int (&id)[kPlanIds]) {
+#pragma unroll
+    for (int i = 0; i < kPlanIds; ++i) {
+      const int t = t0 + 1024 * i + tid;
+      id[i] = group_of(p, t < p.T ? t : p.T - 1);
     }
-    return at;
+#pragma unroll
+    for (int i = 0; i < kPlanIds; ++i)
+      if (t0 + 1024 * i + tid >= p.T) id[i] = -1;
   };
-  for (int t = tid; t < T64; t += 1024) take(t < p.T ? group_of(p, t) : -1);
+  const auto take = [&](int id) {  // this lane's place among the tokens of its group
+    const int g = __builtin_amdgcn_readfirstlane(id);
+    if (__ballot(id == g) == ~0ull) {
+      int base = 0;
+      if (g >= 0 && lane == 0) base = atomicAdd(&cnt[g], 64);
+      return __builtin_amdgcn_readfirstlane(base) + lane;
+    }
+    return id >= 0 ? atomicAdd(&cnt[id], 1) : 0;
+  };
+  int id[kPlanIds];
+  for (int t0 = 0; t0 < p.T; t0 += 1024 * kPlanIds) {
+    load(t0, id);
+#pragma unroll
+    for (int i = 0; i < kPlanIds; ++i)
+      if (t0 + 1024 * i < p.T) take(id[i]);
+  }
   __syncthreads();
   // first tile of each group: a thread scans a run of groups
   const int per = (G + 1023) / 1024, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
@@ -152,10 +174,15 @@ __global__ __launch_bounds__(1024) void k_plan(AdapterParams p, int rows) {
   }
   if (tid == 1023) p.tiles[0] = ni;
   __syncthreads();
-  for (int t = tid; t < T64; t += 1024) {
-    const int id = t < p.T ? group_of(p, t) : -1;
-    const int at = take(id);
-    if (id >= 0) p.perm[at] = t;
+  for (int t0 = 0; t0 < p.T; t0 += 1024 * kPlanIds) {
+    if (p.T > 1024 * kPlanIds) load(t0, id);  // else they are still there
+#pragma unroll
+    for (int i = 0; i < kPlanIds; ++i) {
+      if (t0 + 1024 * i < p.T) {
+        const int at = take(id[i]);
+        if (id[i] >= 0) p.perm[at] = t0 + 1024 * i + tid;
+      }
+    }
   }
 }
 
@@ -377,8 +404,12 @@ void shrink_expand(const AdapterParams& p, int tiles, hipStream_t s) {
 AdapterWs adapter_ws(int T, int Kd, int n, int R) {
   AdapterWs w{};
   w.scan = T <= kAdapterScanT;
-  // 64-token tiles where adapters hold that many tokens on average, else 16
-  w.mt = !w.scan && T / (n + 1) >= 32 ? 4 : 1;
+  // 64-token tiles, which read an adapter's weights a quarter as often, for ranks
+  // above 16 where adapters hold 256 tokens or more on average (rank 64, 2816 x
+  // 2816: 1176 tokens each 203 us against 234 with 16-token tiles, 240 each 64
+  // against 61; rank 32, 4096 x 4096, 32 each 28 against 22; rank 16, 2048 x 2048,
+  // 6600 each 354 against 331)
+  w.mt = R > 16 && T / (n + 1) >= 256 ? 4 : 1;
   const int rows = 16 * w.mt;
   w.max_tiles = (n + 1 < T ? n + 1 : T) + T / rows;
   // ranges of Kd: about 512 workgroups of 4 waves, or 320 of 8 for wide tiles, at

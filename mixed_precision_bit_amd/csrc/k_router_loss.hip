@@ -53,6 +53,13 @@ __device__ __forceinline__ void xcd_pairs(int b, int n, int count, int& tile, in
 // is shared by MT products); the tokens' activations are staged in LDS for all
 // four waves, 64 elements of H at a time, the next stage's loads in flight
 // during the products. Partial sums go to part[range][T][E].
+// 128 tokens x 128 experts from 8192 tokens (16381 x 4096 x 128: 66 us against 75
+// with 64 experts and 95 with 64 tokens), 64 x 64 below (4096 x 2816 x 128: 18.7
+// against 22 with 128 experts, which leave too few workgroups). The matrix cores
+// are busy a third of the time: the cutting (as many VALU cycles) and the reads of
+// W, 16 bytes a cycle as a fragment's lanes lie in 16 rows, do not overlap enough
+// with them. Staging W in LDS as well (18.3 and 73 us) and loading two stages
+// ahead (19.2 and 75) did not help.
 constexpr int kLK = 64, kLRow = kLK + 8;  // 16 bytes of padding per LDS row
 
 template <class D, int MT, int ET>
@@ -149,7 +156,9 @@ __global__ __launch_bounds__(256, 2) void k_router_logits(RouterLossParams p) {
 // One wave per token: adds the ranges of H, writes logits and lse, and keeps
 // its share of P_e, z and N in registers; a workgroup (16 waves) writes one row
 // of them to stat [groups][E + 1] (sum and count of each expert, then z and N).
-// EJ: experts of a lane, e = lane + 64 j.
+// EJ: experts of a lane, e = lane + 64 j. Bound by the chain of a token's loads,
+// reductions and exponentials, a few tokens a wave: 6.7 us for 4096 tokens, 20 for
+// 16381 (42 MB).
 template <int EJ>
 __global__ __launch_bounds__(1024) void k_router_stats(RouterLossParams p) {
   __shared__ int cnt[513];
@@ -317,7 +326,8 @@ __device__ __forceinline__ void halves(fx8 x, hx8 (&q)[2]) {
 __device__ __forceinline__ size_t frag(size_t tiles, size_t part, size_t tile) { return (part * tiles + tile) * 512; }
 
 // dl of 32 tokens per workgroup, two per wave, held in LDS and written in both
-// forms, with the tile's column sums. EJ: experts of a lane, e = lane + 64 j.
+// forms, with the tile's column sums. EJ: experts of a lane, e = lane + 64 j. The
+// logits, not the activations, are read: 7.7 us for 4096 tokens, 18.8 for 16381.
 template <int EJ>
 __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
   extern __shared__ __align__(16) float ds[];  // [32][Ep + 4]
@@ -425,7 +435,9 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
 // goes over its range of tokens, 256 at a time; a wave holds 64 tokens x 64
 // columns. The columns are the products' rows, so that a lane ends with four of
 // a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so that
-// each L2 holds its own part of dl.
+// each L2 holds its own part of dl. 16381 x 4096 x 128: 74 us for 268 MB written
+// (3.6 TB/s) and 52 GFLOP of products; with three bf16 parts 115, with both
+// operands read from L2 as bf16 fragments 135, with stores of 64 bytes a row 82.
 __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
   __shared__ __align__(16) _Float16 wl[2 * 4 * 4 * 512];  // [half][column / 16][expert / 32] fragments
   __shared__ __align__(16) float down[64];                // inverse scales of the columns
@@ -545,7 +557,10 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
 // tokens, its four waves taking 32 tokens in turn. A lane loads 8 tokens x 8
 // columns of X and turns them round in registers, which gives the 8 column
 // fragments of a step (fragment j: columns 8 n + j). The waves' sums meet in
-// LDS in wave order.
+// LDS in wave order. One wave a SIMD with the next step's operands in flight
+// (338 registers): 16381 x 4096 x 128 takes 65 us, 0.8 PFLOP/s of the 1.18 that a
+// large bf16 product reaches; two waves without that 152, and 212 with loads that
+// wait for their token's mask.
 template <class D>
 __global__ __launch_bounds__(256, 1) void k_router_dw(RouterLossParams p) {
   typedef typename D::vec vec;

@@ -109,7 +109,7 @@ int moe_block_norm(const float* o_dev, const void* r_dev, int x_dtype, int T, in
 
 size_t moe_block_norm_grad_workspace_bytes(int T, int H) {
   if (T < 0 || T > (1 << 20) || H <= 0 || H % 64 || H > 65536) return 0;
-  const size_t b = (size_t)2 * mpb::block_norm_grad_groups(T, H) * H * sizeof(float);
+  const size_t b = (size_t)2 * mpb::block_norm_grad_groups(T) * H * sizeof(float);
   return b < 256 ? 256 : b;
 }
 

@@ -244,7 +244,7 @@ struct BlockNormGradParams {
 };
 hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s);
 // workgroups of the backward kernel (decided from the shapes only: the workspace depends on it)
-int block_norm_grad_groups(int T, int H);
+int block_norm_grad_groups(int T);
 hipError_t launch_block_norm_grad(const BlockNormGradParams& p, bool bf16, hipStream_t s);
 
 // Router losses and their gradients (k_router_loss.hip).
@@ -290,7 +290,7 @@ hipError_t launch_router_loss(const RouterLossParams& p, bool bf16, hipStream_t 
 hipError_t launch_router_loss_grad(const RouterLossParams& p, bool bf16, hipStream_t s);
 
 // Low-rank adapters (k_adapters.hip).
-constexpr int kAdapterScanT = 256;   // batches up to this are gathered without a plan launch
+constexpr int kAdapterScanT = 64;    // batches up to this are gathered without a plan launch
 constexpr int kAdapterMaxN = 4096;   // most adapters of a call (the plan's counters in LDS)
 struct AdapterParams {
   const void* X;           // [T][Kd]

@@ -75,6 +75,7 @@ def check(d, got):
 SHAPES = [  # T, Kd, N, n, R, runs
     (1, 2048, 2048, 4, 16, False), (1, 64, 64, 1, 8, False), (2, 128, 192, 3, 24, False), (16, 256, 64, 1, 32, True),
     (17, 64, 320, 1, 128, True), (72, 2048, 1408, 60, 16, False), (128, 4096, 256, 64, 32, False), (255, 192, 128, 300, 72, False),
+    (64, 320, 704, 2, 64, True), (65, 320, 704, 2, 64, True), (2100, 128, 192, 3, 24, True), (1100, 320, 1408, 2, 64, False),
     (256, 320, 704, 2, 64, True), (257, 320, 704, 2, 64, True), (257, 128, 128, 400, 40, False), (600, 2816, 448, 5, 64, True),
     (4099, 256, 320, 7, 16, False), (4099, 64, 64, 1, 128, True), (1500, 128, 64, 4096, 8, False), (33, 65536, 64, 2, 16, False)]
 
@@ -89,7 +90,7 @@ def test_adapters(T, Kd, N, n, R, runs, mixed, dt):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [40, 700])
+@pytest.mark.parametrize("T", [40, 700, 1700])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_unused_ranks_ids_and_defaults(T, dt):
     """Nan past an adapter's rank, ranks and ids out of range, no base, no scales."""
@@ -107,7 +108,7 @@ def test_unused_ranks_ids_and_defaults(T, dt):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [40, 700])
+@pytest.mark.parametrize("T", [40, 700, 1700])
 def test_in_place_and_rows_not_taken(T):
     d = inputs(T, 128, 256, 3, 16, "bf16", seed=10, mixed=False)
     want = run(d, "bf16")
@@ -122,7 +123,7 @@ def test_in_place_and_rows_not_taken(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [100, 700])
+@pytest.mark.parametrize("T", [60, 700, 1700])
 def test_a_tokens_result_does_not_depend_on_the_others(T):
     """The same tokens in another order, and with other tokens' inputs infinite: the same bits."""
     d = inputs(T, 256, 128, 5, 32, "f16", seed=11)
@@ -138,7 +139,7 @@ def test_a_tokens_result_does_not_depend_on_the_others(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [90, 500])
+@pytest.mark.parametrize("T", [50, 500, 2000])
 def test_stream_and_graph_replays_with_other_ids(T):
     d, e = (inputs(T, 192, 320, 6, 24, "bf16", seed=s) for s in (12, 13))
     want = [run(v, "bf16") for v in (d, e)]
