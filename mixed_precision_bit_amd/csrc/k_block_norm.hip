@@ -6,13 +6,13 @@
 //   y = r + s sigmoid(gate) u       the residual stream after the block
 //   x = y rms(y) g_next             the next block's normed input
 //
-// One pass over the rows: a workgroup holds a row in registers (2 vectors of 8
-// elements per thread), so every input is read once and every output written
+// One pass over the rows: a workgroup holds a row in registers (vectors of 8
+// elements, one or two per thread), so every input is read once and every output written
 // once; the two means are two workgroup sums. All arithmetic and both sums are
 // fp32; y is rounded once for r_out, and x is formed from the unrounded y.
 // Bound by HBM: 4096 x 2816 bf16 with a full gate takes 31.7 us, 4.36 TB/s of the
 // 4.9 TB/s that a large copy reaches; up to some hundred rows the launch itself
-// (3.4 us for one row of 2048).
+// (3.2 us for one row of 2048).
 //
 // Backward, from y (the stored stream), with d = dx g_next:
 //   dy = dr_out + rms(y) (d - yh mean(d yh)),  yh = y rms(y);  dg_next = sum_t dx yh
@@ -22,7 +22,7 @@
 // one partial row; k_col_sum adds the partials in workgroup order, so results
 // do not depend on timing. 4093 x 2816 takes 51 + 4.7 us (3.4 TB/s: eight rows a
 // workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 150 + 4.8
-// (4.35 TB/s).
+// (4.3 TB/s).
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -281,32 +281,32 @@ inline int norm_threads(int H, int nv) { return ((H / 8 + nv - 1) / nv + 63) / 6
 
 }  // namespace
 
-hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s) {
+// One vector a thread up to H = 4096 (one row of 2048: 3.2 us against 3.6 with
+// two; 4096 x 2816: 32.4 against 32.8), then two; past 16384 the eight vectors a
+// thread spill, which only such rows pay.
+template <class D>
+static void norm_rows(const BlockNormParams& p, hipStream_t s) {
   const int grid = p.T < 4096 ? p.T : 4096;
-  if (p.H <= 16384) {
-    const int nt = norm_threads(p.H, 2);
-    if (bf16) k_block_norm<BF16, 2><<<grid, nt, 0, s>>>(p);
-    else k_block_norm<F16, 2><<<grid, nt, 0, s>>>(p);
-  } else {
-    const int nt = norm_threads(p.H, 8);
-    if (bf16) k_block_norm<BF16, 8><<<grid, nt, 0, s>>>(p);
-    else k_block_norm<F16, 8><<<grid, nt, 0, s>>>(p);
-  }
+  if (p.H <= 4096) k_block_norm<D, 1><<<grid, norm_threads(p.H, 1), 0, s>>>(p);
+  else if (p.H <= 16384) k_block_norm<D, 2><<<grid, norm_threads(p.H, 2), 0, s>>>(p);
+  else k_block_norm<D, 8><<<grid, norm_threads(p.H, 8), 0, s>>>(p);
+}
+
+hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s) {
+  if (bf16) norm_rows<BF16>(p, s);
+  else norm_rows<F16>(p, s);
   return hipGetLastError();
 }
 
-// Two workgroups a CU: more would add partial rows of 8 H bytes each to write and read.
+// Two workgroups a CU (512): more would add partial rows of 8 H bytes each, and
+// take turns on the CUs (4093 x 2816: 56 us in all against 66 with 768, 71 with 1024).
 int block_norm_grad_groups(int T) { return T < 512 ? T : 512; }
 
-// One vector a thread below H = 4096 (4093 x 2816: 51.6 us against 54.1 with two),
-// two from there (8192 x 4096: 145 against 153): the shorter row leaves a wave of
-// two-vector threads a quarter empty, the longer one fills it, and half the waves
-// meet at each barrier. Rows past 8192 elements leave no registers for a second
-// row; past 16384 the eight vectors a thread spill, which only such rows pay.
+// Two vectors a thread; rows past 8192 elements leave no registers for a second
+// row, and past 16384 the eight vectors a thread spill, which only such rows pay.
 template <class D>
 static void grad_rows(const BlockNormGradParams& p, int grid, hipStream_t s) {
-  if (p.H < 4096) k_block_norm_grad<D, 1, 512, true><<<grid, norm_threads(p.H, 1), 0, s>>>(p);
-  else if (p.H <= 8192) k_block_norm_grad<D, 2, 512, true><<<grid, norm_threads(p.H, 2), 0, s>>>(p);
+  if (p.H <= 8192) k_block_norm_grad<D, 2, 512, true><<<grid, norm_threads(p.H, 2), 0, s>>>(p);
   else if (p.H <= 16384) k_block_norm_grad<D, 2, 1024, false><<<grid, norm_threads(p.H, 2), 0, s>>>(p);
   else k_block_norm_grad<D, 8, 1024, false><<<grid, norm_threads(p.H, 8), 0, s>>>(p);
 }
