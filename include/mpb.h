@@ -297,7 +297,8 @@ int moe_block_norm(const float* o_dev, const void* r_dev, int x_dtype, int T, in
  * dr may be dr_out or dx itself, and do may be o. Every sum is in fp32 and in
  * a fixed order (deterministic). ws_dev (16-byte aligned): at least
  * moe_block_norm_grad_workspace_bytes(T, H) bytes, needed only for the gamma
- * gradients; contents not preserved. T == 0 zeroes the gamma gradients.
+ * gradients; contents not preserved, one per call that may overlap another.
+ * T == 0 zeroes the gamma gradients.
  * Limits and errors as above, plus MPB_E_WS.
  */
 size_t moe_block_norm_grad_workspace_bytes(int T, int H);
@@ -329,8 +330,9 @@ int moe_block_norm_grad(const float* o_dev, const void* y_dev, int x_dtype, int 
  * The logits are exact products accumulated in fp32, in an order other than
  * moe_route's fp64 one; every sum has a fixed order (deterministic). No live
  * token: losses 0. ws_dev (16-byte aligned): at least
- * moe_router_loss_workspace_bytes(T, H, E) bytes, contents not preserved.
- * Limits as for moe_route. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS,
+ * moe_router_loss_workspace_bytes(T, H, E) bytes, contents not preserved, one
+ * per call that may overlap another. Infinite inputs of a live token give its
+ * logits, and with them the losses, infinite or NaN values. Limits as for moe_route. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS,
  * MPB_E_HIP. Does not need mpb_init.
  */
 size_t moe_router_loss_workspace_bytes(int T, int H, int E);

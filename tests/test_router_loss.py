@@ -5,7 +5,9 @@ matrix instructions for 32 of them, each instruction's result rounded to fp32
 after up to 32 additions of its own, over ranges that are added once more: within
 n(H) u of the sum of the products' absolute values, n(L) = 6 L / 32 + 96; what the
 cut parts leave out is below 4 u of it. The gradients' products have the same form
-with L = E rounded up to 64 or the number of tokens. Sums of p over tokens pass at
+with L = E rounded up to 64 or the number of tokens; dX takes three instructions
+instead of up to six and its halves leave out 12 u: 3 L / 32 + 96 + 12 is below
+n(L) + 8 from L = 64. Sums of p over tokens pass at
 most T / 2048 + 32 additions, exponentials and logarithms are within 4 u of their
 value and carry their argument's error."""
 import ctypes
