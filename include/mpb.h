@@ -386,7 +386,8 @@ int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_d
  *               then not touched)
  * Tokens are gathered by adapter on the device, so ids may change from call to
  * call (also under graph replay). Products are exact, sums fp32 in a fixed
- * order (deterministic), and A_a x_t is not rounded below fp32. Needs Kd and N
+ * order (deterministic), and A_a x_t is not rounded below fp32; a token whose x,
+ * A_a or B_a holds infinite values gets infinite or NaN ones. Needs Kd and N
  * multiples of 64 (Kd <= 65536, N <= 131072), R a multiple of 8 in 8..128, n in
  * 1..4096, T <= 2^20, 16-byte aligned rows; T == 0 is a no-op. ws_dev (16-byte
  * aligned): at least moe_adapters_workspace_bytes(T, Kd, n, R) bytes, contents

@@ -253,6 +253,8 @@ class _Args:
     def run(self, fn, stream, *args):
         if self.index < 0:
             self.fail("tensors are on the CPU")
+        if stream is not None and stream.device.index != self.index:
+            self.fail(f"the stream is on {stream.device}, the tensors on device {self.index}")
         if self.index != torch.cuda.current_device():
             with torch.cuda.device(self.index):
                 return self.call(fn, stream, args)

@@ -5,6 +5,8 @@ the expert FFN all run in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -122,13 +124,21 @@ class DeviceLayer:
         return idx, w, out
 
     # ---------------------------------------------------------------- the block around the layer
+    # Where a call takes a stream, its results and workspaces are allocated for
+    # that stream: a workspace freed on return is not handed out on another one
+    # while the call's kernels may still run.
+    @staticmethod
+    def _on(stream):
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
     def alloc_rows(self, T, xdtype):
         """[T][H] activations."""
         return torch.empty((T, self.H), dtype=XTORCH[xdtype], device=self.device)
 
     def norm_in(self, r, xdtype, gamma, eps=1e-6, stream=None):
         """The first block's normed input of a residual stream r [T][H]."""
-        x = self.alloc_rows(r.shape[0], xdtype)
+        with self._on(stream):
+            x = self.alloc_rows(r.shape[0], xdtype)
         M.moe_block_norm(None, r, XDTYPE[xdtype], None, None, gamma, 1.0, eps, None, x, stream)
         return x
 
@@ -136,8 +146,9 @@ class DeviceLayer:
         """Adds every token's adapter to out [T][H] in place. adapters: a dict with A [n][R][H], B [n][H][R],
         adapter [T], and ranks [n] and scales [n] if they differ from R and 1."""
         A = adapters["A"]
-        ws = torch.empty(M.moe_adapters_workspace_bytes(X.shape[0], self.H, A.shape[0], A.shape[1]), dtype=torch.uint8,
-                         device=self.device)
+        with self._on(stream):
+            ws = torch.empty(M.moe_adapters_workspace_bytes(X.shape[0], self.H, A.shape[0], A.shape[1]),
+                             dtype=torch.uint8, device=self.device)
         M.moe_adapters(X, XDTYPE[xdtype], A, adapters["B"], adapters.get("ranks"), adapters.get("scales"),
                        adapters["adapter"], out, out, ws, stream)
 
@@ -146,11 +157,12 @@ class DeviceLayer:
         """One residual block: the layer on X [T][H] (the normed stream), its tokens' adapters, and the layer's output
         normed, gated and scaled onto the stream r [T][H]. Returns idx, w, the layer's output with the adapters', the
         stream after the block and (with gamma_next) the next block's normed input."""
-        idx, w, out = self.forward(X, xdtype, stream)
+        with self._on(stream):
+            idx, w, out = self.forward(X, xdtype, stream)
+            r_out = self.alloc_rows(r.shape[0], xdtype)
+            x_next = None if gamma_next is None else self.alloc_rows(r.shape[0], xdtype)
         if adapters is not None:
             self.adapt(X, xdtype, adapters, out, stream)
-        r_out = self.alloc_rows(r.shape[0], xdtype)
-        x_next = None if gamma_next is None else self.alloc_rows(r.shape[0], xdtype)
         M.moe_block_norm(out, r, XDTYPE[xdtype], gate, gamma_post, gamma_next, scale, eps, r_out, x_next, stream)
         return idx, w, out, r_out, x_next
 
@@ -160,11 +172,12 @@ class DeviceLayer:
         two norms' weights (None where there is none)."""
         T = r_out.shape[0]
         f32 = dict(dtype=torch.float32, device=self.device)
-        g = {"r": self.alloc_rows(T, xdtype), "out": torch.empty((T, self.H), **f32),
-             "gate": None if gate is None else torch.empty_like(gate),
-             "gamma_post": None if gamma_post is None else torch.empty(self.H, **f32),
-             "gamma_next": None if gamma_next is None else torch.empty(self.H, **f32)}
-        ws = torch.empty(M.moe_block_norm_grad_workspace_bytes(T, self.H), dtype=torch.uint8, device=self.device)
+        with self._on(stream):
+            g = {"r": self.alloc_rows(T, xdtype), "out": torch.empty((T, self.H), **f32),
+                 "gate": None if gate is None else torch.empty_like(gate),
+                 "gamma_post": None if gamma_post is None else torch.empty(self.H, **f32),
+                 "gamma_next": None if gamma_next is None else torch.empty(self.H, **f32)}
+            ws = torch.empty(M.moe_block_norm_grad_workspace_bytes(T, self.H), dtype=torch.uint8, device=self.device)
         M.moe_block_norm_grad(out, r_out, XDTYPE[xdtype], gate, gamma_post, gamma_next, scale, eps, dr_out, dx_next,
                               g["r"], g["out"], g["gate"], g["gamma_post"], g["gamma_next"], ws, stream)
         return g
@@ -173,11 +186,13 @@ class DeviceLayer:
         """Balance and z loss of the routed batch: a dict of loss [3], counts [E + 1], prob [E] and what the gradient
         needs (logits, lse, and the call's arguments)."""
         T, f32 = X.shape[0], dict(dtype=torch.float32, device=self.device)
-        s = {"logits": torch.empty((T, self.E), **f32), "lse": torch.empty(T, **f32),
-             "counts": torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
-             "prob": torch.empty(self.E, **f32), "loss": torch.empty(3, **f32),
-             "args": (X, xdtype, idx, mask, alpha, beta)}
-        ws = torch.empty(M.moe_router_loss_workspace_bytes(T, self.H, self.E), dtype=torch.uint8, device=self.device)
+        with self._on(stream):
+            s = {"logits": torch.empty((T, self.E), **f32), "lse": torch.empty(T, **f32),
+                 "counts": torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
+                 "prob": torch.empty(self.E, **f32), "loss": torch.empty(3, **f32),
+                 "args": (X, xdtype, idx, mask, alpha, beta)}
+            ws = torch.empty(M.moe_router_loss_workspace_bytes(T, self.H, self.E), dtype=torch.uint8,
+                             device=self.device)
         M.moe_router_loss(X, XDTYPE[xdtype], self.W_r, self.bias, idx, mask, alpha, beta, s["logits"], s["lse"],
                           s["counts"], s["prob"], s["loss"], ws, stream)
         return s
@@ -186,9 +201,10 @@ class DeviceLayer:
         """Gradients (X, W_r, bias) of router_loss's loss[0] times gloss, and of the routing weights (gw [T][K])."""
         X, xdtype, idx, mask, alpha, beta = s["args"]
         f32 = dict(dtype=torch.float32, device=self.device)
-        dX, dW, db = torch.empty(X.shape, **f32), torch.empty((self.E, self.H), **f32), torch.empty(self.E, **f32)
-        ws = torch.empty(M.moe_router_loss_workspace_bytes(X.shape[0], self.H, self.E), dtype=torch.uint8,
-                         device=self.device)
+        with self._on(stream):
+            dX, dW, db = torch.empty(X.shape, **f32), torch.empty((self.E, self.H), **f32), torch.empty(self.E, **f32)
+            ws = torch.empty(M.moe_router_loss_workspace_bytes(X.shape[0], self.H, self.E), dtype=torch.uint8,
+                             device=self.device)
         M.moe_router_loss_grad(X, XDTYPE[xdtype], self.W_r, idx, mask, s["logits"], s["lse"], s["counts"], alpha, beta,
                                gw, gloss, dX, dW, db, ws, stream)
         return dX, dW, db

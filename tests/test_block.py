@@ -92,3 +92,35 @@ def test_block_under_graph_replay(layer_cache):
         for a, c in zip(got, want[k]):
             assert torch.equal(a, c)
         D.forward(x, "f16")
+
+
+def test_block_on_its_own_stream(layer_cache):
+    """Everything on a stream other than the current one, the current one writing into fresh memory meanwhile."""
+    from mixed_precision_bit_amd import _lib as M
+    from mixed_precision_bit_amd.layer import DeviceLayer
+    L = layer_cache(0)
+    D = DeviceLayer.from_synth(L)
+    d, ad = TN.inputs(16, D.H, "f16", "token", True, True, seed=3), TA.inputs(16, D.H, D.H, 3, 8, "f16", seed=3)
+    mask = torch.arange(16, device="cuda") % 5 != 0  # a bool mask
+
+    def all_of(stream):
+        x = D.norm_in(d["r"], "f16", d["gn"], stream=stream)
+        b = D.block(x, d["r"], "f16", d["gp"], d["gn"], d["gate"], 0.7, adapters=ad, stream=stream)
+        g = D.block_norm_grad(b[2], b[3], "f16", d["dr_out"], d["dx"], d["gp"], d["gn"], d["gate"], 0.7, stream=stream)
+        s = D.router_loss(x, "f16", b[0], mask, stream=stream)
+        return [*b, *g.values(), s["loss"], s["counts"], *D.router_loss_grad(s, stream=stream)]
+
+    M.mpb_init(D.H, D.I, D.E, D.S, D.K, D.q_dev, L.q)
+    want = all_of(None)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    M.mpb_init(D.H, D.I, D.E, D.S, D.K, D.q_dev, L.q, stream=st)
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = all_of(st)
+        junk = [torch.full((1 << 18,), float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
+    M.mpb_init(D.H, D.I, D.E, D.S, D.K, D.q_dev, L.q)

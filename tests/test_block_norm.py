@@ -244,6 +244,23 @@ def test_grad_in_place_and_frozen_weights():
     M.moe_block_norm_grad(do, d["r"], M.MPB_BF16, d["gate"], d["gp"], d["gn"], 0.7, EPS, dr, d["dx"], dr, do, None,
                           None, None, None)
     assert torch.equal(dr, want["dr"]) and torch.equal(do, want["do"])
+    dr = d["dx"].clone()
+    M.moe_block_norm_grad(d["o"], d["r"], M.MPB_BF16, d["gate"], d["gp"], d["gn"], 0.7, EPS, d["dr_out"], dr, dr, None,
+                          None, None, None, None)
+    assert torch.equal(dr, want["dr"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [320, 16384, 20480])
+def test_grad_in_place_over_many_rows(H):
+    """In place with several rows a workgroup, whose loads run ahead."""
+    M = lib_m()
+    d = inputs(1400, H, "f16", "full", True, True, seed=5)
+    want = run_grad(d, "f16", 0.7)
+    dr, do = d["dr_out"].clone(), d["o"].clone()
+    M.moe_block_norm_grad(do, d["r"], M.MPB_F16, d["gate"], d["gp"], d["gn"], 0.7, EPS, dr, d["dx"], dr, do, None,
+                          None, None, None)
+    assert torch.equal(dr, want["dr"]) and torch.equal(do, want["do"])
 
 
 @pytest.mark.gpu
