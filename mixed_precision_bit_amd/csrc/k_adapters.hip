@@ -19,8 +19,8 @@
 // in: its results are the same in any batch of the same launch shape.
 // Rows past an adapter's rank are never read, columns past it never used.
 //
-// 128 tokens of 64 adapters, 4096 x 4096, ranks up to 32: plan 4.0, shrink 6.3,
-// expand 8.6 us, bound by chains of latencies (the tile's tokens, its operands,
+// 128 tokens of 64 adapters, 4096 x 4096, ranks up to 32: plan 3.8, shrink 5.9,
+// expand 7.3 us, bound by chains of latencies (the tile's tokens, its operands,
 // the sums). 4093 tokens of 16 adapters, 2816 x 2816, ranks up to 64: plan 6.4,
 // shrink 19.7, expand 33.7 us; the last moves 92 MB of base and out and reads B
 // through the cache, 16 bytes a cycle (a fragment's lanes lie in 16 rows).
@@ -269,8 +269,8 @@ __global__ __launch_bounds__(64 * shrink_waves(MT)) void k_shrink(AdapterParams 
 // time. The next 64 columns' base and B are always on their way, in the other of
 // two register sets: the loop holds no condition and no copy, at which the
 // compiler would wait for the stores too.
-constexpr int expand_cols(int MT) { return MT == 4 ? 512 : 1024; }
-
+// The four waves of a narrow tile share its z: each adds every fourth range, and
+// the four sums meet in LDS.
 template <class D, int MT, int RK, bool BASE>
 __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   typedef typename D::vec vec;
@@ -278,6 +278,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   constexpr int NP = Parts<D>::N, kStep = MT == 4 ? 64 : 256;
   __shared__ TileLds tl;
   __shared__ __align__(16) float turn[4][16][64 + 4];
+  __shared__ fx8 zs[MT == 1 ? 4 : 1][RK][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
   int a, rank;
   if (!find_tile<16 * MT>(p, blockIdx.x, tl, a, rank)) return;
@@ -287,9 +288,9 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   // repeat the wave's first token (and store its values again), ranks past the
   // adapter's its first 8.
   const int t = mine < 0 ? first : mine;
-  const int c0 = blockIdx.y * expand_cols(MT) + (MT == 4 ? 0 : 64 * wave);
-  const int ce = (int)(blockIdx.y + 1) * expand_cols(MT), c1 = ce < p.N ? ce : p.N;
-  if (first < 0 || c0 >= c1) return;  // this wave's rows or columns are past the end
+  const int c0 = blockIdx.y * p.cols + (MT == 4 ? 0 : 64 * wave);
+  const int ce = (int)(blockIdx.y + 1) * p.cols, c1 = ce < p.N ? ce : p.N;
+  if (MT == 4 && first < 0) return;  // this wave's rows are past the tile's end
   // rows of memory accesses: token 4 i + g, columns 4 n ..
   size_t row[4];
   unsigned live = 0;  // narrow tiles, mostly of a few tokens, store no row twice
@@ -331,18 +332,31 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
     }
   };
   Cols v0, v1;
-  load(c0, v0);
-  bx8 z[RK][3];
+  if (c0 < c1) load(c0, v0);
   const float scale = p.scales ? p.scales[a] : 1.0f;
+  constexpr int kShare = MT == 1 ? 4 : 1;
+  fx8 zv[RK];
 #pragma unroll
   for (int k = 0; k < RK; ++k) {
-    fx8 v = (fx8)(0.0f);
+    zv[k] = (fx8)(0.0f);
     const float* src = p.z + (size_t)t * p.R + kof[k];
-#pragma unroll 8
-    for (int s = 0; s < p.ranges; ++s) v += load8(src + (size_t)s * p.T * p.R);
+#pragma unroll 4
+    for (int s = MT == 1 ? wave : 0; s < p.ranges; s += kShare) zv[k] += load8(src + (size_t)s * p.T * p.R);
+  }
+  if (MT == 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 32 * k + 8 * g + i < rank ? v[i] * scale : 0.0f;
-    cut<3>(v, z[k]);
+    for (int k = 0; k < RK; ++k) zs[wave][k][lane] = zv[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < RK; ++k) zv[k] = (zs[0][k][lane] + zs[1][k][lane]) + (zs[2][k][lane] + zs[3][k][lane]);
+  }
+  if (c0 >= c1) return;  // this wave's columns are past the end
+  bx8 z[RK][3];
+#pragma unroll
+  for (int k = 0; k < RK; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) zv[k][i] = 32 * k + 8 * g + i < rank ? zv[k][i] * scale : 0.0f;
+    cut<3>(zv[k], z[k]);
   }
   const auto work = [&](int c, const Cols& v) {
     acc4 d[4];
@@ -390,7 +404,7 @@ void expand(const AdapterParams& p, dim3 grid, hipStream_t s) {
 
 template <class D, int MT>
 void shrink_expand(const AdapterParams& p, int tiles, hipStream_t s) {
-  const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + expand_cols(MT) - 1) / expand_cols(MT));
+  const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + p.cols - 1) / p.cols);
   if (p.R <= 16) k_shrink<D, MT, 1><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else if (p.R <= 32) k_shrink<D, MT, 2><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else if (p.R <= 64) k_shrink<D, MT, 4><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
@@ -431,7 +445,13 @@ AdapterWs adapter_ws(int T, int Kd, int n, int R) {
   return w;
 }
 
-hipError_t launch_adapters(const AdapterParams& p, const AdapterWs& w, bool bf16, hipStream_t s) {
+hipError_t launch_adapters(const AdapterParams& q, const AdapterWs& w, bool bf16, hipStream_t s) {
+  AdapterParams p = q;
+  // columns of an expand workgroup: 512 of a wide tile; of a narrow one up to 1024
+  // (4093 x 2816: 33.8 us against 36.2 with 512), fewer where that makes less than
+  // 512 workgroups (128 tokens of 64 adapters: 7.3 against 8.8)
+  p.cols = w.mt == 4 ? 512 : 1024;
+  while (w.mt == 1 && p.cols > 256 && (long long)w.max_tiles * ((p.N + p.cols - 1) / p.cols) < 512) p.cols /= 2;
   if (!w.scan) k_plan<<<1, 1024, 0, s>>>(p, 16 * w.mt);
   if (bf16) {
     if (w.mt == 4) shrink_expand<BF16, 4>(p, w.max_tiles, s);

@@ -306,6 +306,7 @@ struct AdapterParams {
   int32_t* perm;           // [tiles][16 mt] tokens of each tile (-1 past its end), or null (no plan)
   int32_t* tiles;          // count, 3 unused words, then each tile's adapter and rank
   int ranges;
+  int cols;                // columns of an expand workgroup (set by launch_adapters)
 };
 struct AdapterWs {
   size_t z, perm, tiles, total;
