@@ -21,8 +21,9 @@
 //
 // 128 tokens of 64 adapters, 4096 x 4096, ranks up to 32: plan 3.8, shrink 5.9,
 // expand 7.3 us, bound by chains of latencies (the tile's tokens, its operands,
-// the sums). 4093 tokens of 16 adapters, 2816 x 2816, ranks up to 64: plan 6.4,
-// shrink 19.7, expand 33.7 us; the last moves 92 MB of base and out and reads B
+// the sums). 4093 tokens of 16 adapters, 2816 x 2816, ranks up to 64: plan 6.2,
+// shrink 16.6, expand 32.4 us (19.4 and 33.7 where base and out pass through the
+// caches as other data does); the last moves 92 MB of base and out and reads B
 // through the cache, 16 bytes a cycle (a fragment's lanes lie in 16 rows).
 #include "k_block_common.h"
 #include "mpb.h"
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
   const auto load = [&](int c, Cols& v) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v.base[j] = BASE ? *(const acc4*)(p.base + row[j] + c) : (acc4)(0.0f);
+      v.base[j] = BASE ? stream_load((const acc4*)(p.base + row[j] + c)) : (acc4)(0.0f);
 #pragma unroll
       for (int k = 0; k < RK; ++k) v.b[j][k] = *(const vec*)(brow + (size_t)(c + 16 * j) * p.R + kof[k]);
     }
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(256) void k_expand(AdapterParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const acc4 sum = v.base[i] + *(const acc4*)&turn[wave][4 * i + g][4 * n];
-      if (MT == 4 || live >> (4 * i) & 1) *(acc4*)(p.out + row[i] + c) = sum;
+      if (MT == 4 || live >> (4 * i) & 1) stream_store((acc4*)(p.out + row[i] + c), sum);
     }
     __builtin_amdgcn_wave_barrier();
   };

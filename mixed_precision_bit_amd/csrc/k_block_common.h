@@ -37,6 +37,21 @@ __device__ __forceinline__ fx8 load8(const float* p) {
   const fx4 a = *(const fx4*)p, b = *(const fx4*)(p + 4);
   return fx8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
+// Results of a whole pass, which the caches could not keep anyway, are stored
+// (and inputs read once loaded) as streams, so that they do not push out what the
+// other workgroups read again.
+template <class V>
+__device__ __forceinline__ void stream_store(V* p, V v) {
+  __builtin_nontemporal_store(v, p);
+}
+template <class V>
+__device__ __forceinline__ V stream_load(const V* p) {
+  return __builtin_nontemporal_load(p);
+}
+__device__ __forceinline__ void stream_store8(float* p, fx8 v) {
+  stream_store((fx4*)p, fx4{v[0], v[1], v[2], v[3]});
+  stream_store((fx4*)(p + 4), fx4{v[4], v[5], v[6], v[7]});
+}
 __device__ __forceinline__ void store8(float* p, fx8 v) {
   *(fx4*)p = fx4{v[0], v[1], v[2], v[3]};
   *(fx4*)(p + 4) = fx4{v[4], v[5], v[6], v[7]};

@@ -20,9 +20,9 @@
 //   do = rms(o) (du g_post - oh mean(du g_post oh));  dg_post = sum_t du oh
 // The column sums stay in registers over the rows of a workgroup, which writes
 // one partial row; k_col_sum adds the partials in workgroup order, so results
-// do not depend on timing. 4093 x 2816 takes 51 + 4.7 us (3.4 TB/s: eight rows a
-// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 150 + 4.8
-// (4.3 TB/s).
+// do not depend on timing. 4093 x 2816 takes 48 + 4.6 us (3.5 TB/s: eight rows a
+// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 148 + 4.7
+// (4.4 TB/s).
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(THREADS) void k_block_norm_grad(BlockNormGradParams
           gn[j] += d * yh;
           dy += (d * load8(p.g_next + 8 * v) - yh * my) * ry;
         }
-        *(vec*)((elem*)p.dr + row + 8 * v) = narrow<D>(dy);
+        stream_store((vec*)((elem*)p.dr + row + 8 * v), narrow<D>(dy));
         fx8 w = (fx8)(1.0f);
         if (post) w = load8(p.g_post + 8 * v);
         fx8 du = dy * k;  // with a token gate's sigmoid
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(THREADS) void k_block_norm_grad(BlockNormGradParams
             du[i] *= sigmoid(g[i]);
             dg[i] = du[i] * in.o[j][i] * ro * w[i] * sigmoid(-g[i]);
           }
-          if (p.dgate) *(vec*)((elem*)p.dgate + row + 8 * v) = narrow<D>(dg);
+          if (p.dgate) stream_store((vec*)((elem*)p.dgate + row + 8 * v), narrow<D>(dg));
         }
         if (post) gp[j] += du * in.o[j] * ro;
         dw[j] = du * w;
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(THREADS) void k_block_norm_grad(BlockNormGradParams
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int v = tid + j * nt;
-        if (v < nvec) store8(p.d_o + row + 8 * v, post ? (dw[j] - in.o[j] * mo) * ro : dw[j]);
+        if (v < nvec) stream_store8(p.d_o + row + 8 * v, post ? (dw[j] - in.o[j] * mo) * ro : dw[j]);
       }
     }
   };

@@ -435,9 +435,10 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
 // goes over its range of tokens, 256 at a time; a wave holds 64 tokens x 64
 // columns. The columns are the products' rows, so that a lane ends with four of
 // a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so that
-// each L2 holds its own part of dl. 16381 x 4096 x 128: 74 us for 268 MB written
-// (3.6 TB/s) and 52 GFLOP of products; with three bf16 parts 115, with both
-// operands read from L2 as bf16 fragments 135, with stores of 64 bytes a row 82.
+// each L2 holds its own part of dl. 16381 x 4096 x 128: 58 us for 268 MB written
+// (4.6 TB/s) and 52 GFLOP of products; with plain stores 75, with stores of 64
+// bytes a row 82, with three bf16 parts 115, with both operands read from L2 as
+// bf16 fragments 135.
 __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
   __shared__ __align__(16) _Float16 wl[2 * 4 * 4 * 512];  // [half][column / 16][expert / 32] fragments
   __shared__ __align__(16) float down[64];                // inverse scales of the columns
@@ -543,7 +544,8 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = t0 + 16 * m + 4 * i + g;
-        if (FULL.value || t < p.T) *(acc4*)(p.dX + (size_t)t * p.H + h0 + 4 * n) = *(const acc4*)&turn[wave][4 * i + g][4 * n];
+        if (FULL.value || t < p.T)
+          stream_store((acc4*)(p.dX + (size_t)t * p.H + h0 + 4 * n), *(const acc4*)&turn[wave][4 * i + g][4 * n]);
       }
       __builtin_amdgcn_wave_barrier();
     }
