@@ -20,8 +20,8 @@
 //   do = rms(o) (du g_post - oh mean(du g_post oh));  dg_post = sum_t du oh
 // The column sums stay in registers over the rows of a workgroup, which writes
 // one partial row; k_col_sum adds the partials in workgroup order, so results
-// do not depend on timing. 4093 x 2816 takes 48 + 4.6 us (3.5 TB/s: eight rows a
-// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 148 + 4.7
+// do not depend on timing. 4093 x 2816 takes 50 + 4.7 us (3.6 TB/s: eight rows a
+// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 151 + 4.8
 // (4.4 TB/s).
 #include "k_block_common.h"
 #include "mpb.h"

@@ -53,7 +53,7 @@ __device__ __forceinline__ void xcd_pairs(int b, int n, int count, int& tile, in
 // is shared by MT products); the tokens' activations are staged in LDS for all
 // four waves, 64 elements of H at a time, the next stage's loads in flight
 // during the products. Partial sums go to part[range][T][E].
-// 128 tokens x 128 experts from 8192 tokens (16381 x 4096 x 128: 66 us against 75
+// 128 tokens x 128 experts from 8192 tokens (16381 x 4096 x 128: 63 to 66 us against 75
 // with 64 experts and 95 with 64 tokens), 64 x 64 below (4096 x 2816 x 128: 18.7
 // against 22 with 128 experts, which leave too few workgroups). The matrix cores
 // are busy a third of the time: the cutting (as many VALU cycles) and the reads of
@@ -435,9 +435,9 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
 // goes over its range of tokens, 256 at a time; a wave holds 64 tokens x 64
 // columns. The columns are the products' rows, so that a lane ends with four of
 // a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so that
-// each L2 holds its own part of dl. 16381 x 4096 x 128: 58 us for 268 MB written
-// (4.6 TB/s) and 52 GFLOP of products; with plain stores 75, with stores of 64
-// bytes a row 82, with three bf16 parts 115, with both operands read from L2 as
+// each L2 holds its own part of dl. 16381 x 4096 x 128: 73 us for 268 MB written
+// (3.7 TB/s) and 52 GFLOP of products; with plain stores 75 (and 65 instead of 57
+// for dW behind it, whose operands they push out), with stores of 64 bytes a row 82, with three bf16 parts 115, with both operands read from L2 as
 // bf16 fragments 135.
 __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
   __shared__ __align__(16) _Float16 wl[2 * 4 * 4 * 512];  // [half][column / 16][expert / 32] fragments
@@ -560,7 +560,7 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
 // columns of X and turns them round in registers, which gives the 8 column
 // fragments of a step (fragment j: columns 8 n + j). The waves' sums meet in
 // LDS in wave order. One wave a SIMD with the next step's operands in flight
-// (338 registers): 16381 x 4096 x 128 takes 65 us, 0.8 PFLOP/s of the 1.18 that a
+// (338 registers): 16381 x 4096 x 128 takes 57 us, 0.9 PFLOP/s of the 1.18 that a
 // large bf16 product reaches; two waves without that 152, and 212 with loads that
 // wait for their token's mask.
 template <class D>
