@@ -71,7 +71,6 @@ class DeviceLayer:
             if bind:
                 M.mpb_init(H, I, E, S, K, q_dev, np.asarray(q, np.int32))
         self.q_dev = q_dev
-        self.route_ws = None  # router logits scratch, sized by alloc_route
         torch.cuda.synchronize()
 
     @classmethod
@@ -84,13 +83,19 @@ class DeviceLayer:
             sum(t.numel() * 2 for lt in self.luts for t in lt)
 
     # ---------------------------------------------------------------- calls
+    # Where a call takes a stream, its results and workspaces are allocated for
+    # that stream: a workspace freed on return is not handed out on another one
+    # while the call's kernels may still run. The layer keeps none of them: calls
+    # on several streams and captured graphs share no memory, and a captured call's
+    # workspaces stay in its graph's pool whatever is called later.
+    @staticmethod
+    def _on(stream):
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
     def alloc_route(self, T):
-        """Router outputs for T tokens; also sizes the router workspace for T."""
+        """Router outputs for T tokens."""
         idx = torch.empty((T, self.K), dtype=torch.int32, device=self.device)
         w = torch.empty((T, self.K), dtype=torch.float32, device=self.device)
-        need = max(1, M.moe_route_workspace_bytes(T, self.E))
-        if self.route_ws is None or self.route_ws.numel() < need:
-            self.route_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         return idx, w
 
     def alloc_ffn(self, T):
@@ -109,28 +114,27 @@ class DeviceLayer:
         M.moe_fused(X, XDTYPE[xdtype], self.W_r, self.bias, idx, w, self.planes_table, self.luts_table, self.q_dev,
                     out, ws, stream)
 
-    def route(self, X, xdtype, idx, w, stream=None):
-        M.moe_route(X, XDTYPE[xdtype], self.W_r, self.bias, self.K, idx, w, self.route_ws, stream)
+    def route(self, X, xdtype, idx, w, stream=None, ws=None):
+        """moe_route; ws: a workspace of the caller's, or None for one of this call's own."""
+        if ws is None:
+            with self._on(stream):
+                ws = torch.empty(max(1, M.moe_route_workspace_bytes(X.shape[0], self.E)), dtype=torch.uint8,
+                                 device=self.device)
+        M.moe_route(X, XDTYPE[xdtype], self.W_r, self.bias, self.K, idx, w, ws, stream)
 
     def ffn(self, X, xdtype, idx, w, out, ws, stream=None):
         M.moe_ffn(X, XDTYPE[xdtype], idx, w, self.planes_table, self.luts_table, self.q_dev, out, ws, stream)
 
     def forward(self, X, xdtype, stream=None):
         T = X.shape[0]
-        idx, w = self.alloc_route(T)
-        out, ws = self.alloc_ffn(T)
+        with self._on(stream):
+            idx, w = self.alloc_route(T)
+            out, ws = self.alloc_ffn(T)
         self.route(X, xdtype, idx, w, stream)
         self.ffn(X, xdtype, idx, w, out, ws, stream)
         return idx, w, out
 
     # ---------------------------------------------------------------- the block around the layer
-    # Where a call takes a stream, its results and workspaces are allocated for
-    # that stream: a workspace freed on return is not handed out on another one
-    # while the call's kernels may still run.
-    @staticmethod
-    def _on(stream):
-        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
     def alloc_rows(self, T, xdtype):
         """[T][H] activations."""
         return torch.empty((T, self.H), dtype=XTORCH[xdtype], device=self.device)
@@ -157,8 +161,8 @@ class DeviceLayer:
         """One residual block: the layer on X [T][H] (the normed stream), its tokens' adapters, and the layer's output
         normed, gated and scaled onto the stream r [T][H]. Returns idx, w, the layer's output with the adapters', the
         stream after the block and (with gamma_next) the next block's normed input."""
+        idx, w, out = self.forward(X, xdtype, stream)
         with self._on(stream):
-            idx, w, out = self.forward(X, xdtype, stream)
             r_out = self.alloc_rows(r.shape[0], xdtype)
             x_next = None if gamma_next is None else self.alloc_rows(r.shape[0], xdtype)
         if adapters is not None:
