@@ -221,8 +221,13 @@ class _Args:
     device pointers. Raw 16-bit tensors (int16) stand for either activation
     type. The call runs with the tensors' device current."""
 
-    def __init__(self, name, t):
-        self.name, self.index = name, t.get_device()  # -1: not on a GPU
+    def __init__(self, name, *sized):
+        """sized: the tensors that the sizes are read from, none of which may be missing."""
+        self.name = name
+        for t in sized:
+            if t is None:
+                self.fail("null pointer")
+        self.index = sized[0].get_device()  # -1: not on a GPU
 
     def fail(self, msg, code=-1):
         raise MpbError(self.name, code, msg)
@@ -318,7 +323,7 @@ def moe_block_norm_grad(o, y, x_dtype, gate, gamma_post, gamma_next, scale, eps,
 
 
 def _router_args(name, X, x_dtype, W_router, topk_idx, mask):
-    a = _Args(name, X)
+    a = _Args(name, X, W_router, topk_idx)
     xt = _xtype(name, x_dtype)
     if X.dim() != 2 or W_router.dim() != 2 or topk_idx.dim() != 2:
         a.fail("X is [T][H], W_router [E][H], topk_idx [T][K]", -2)
@@ -360,7 +365,7 @@ def moe_adapters_workspace_bytes(T, Kd, n, R) -> int:
 
 def moe_adapters(X, x_dtype, A, B, ranks, scales, adapter, base, out, ws, stream=None):
     """out = base + scales[a] * B[a] (A[a] x) with a = adapter[t] per token; A [n][R][Kd], B [n][N][R]."""
-    a = _Args("moe_adapters", X)
+    a = _Args("moe_adapters", X, A, B)
     xt = _xtype(a.name, x_dtype)
     if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         a.fail("X is [T][Kd], A [n][R][Kd], B [n][N][R]", -2)
