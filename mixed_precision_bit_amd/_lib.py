@@ -352,6 +352,8 @@ def moe_router_loss_grad(X, x_dtype, W_router, topk_idx, mask, logits, lse, coun
     """Gradients of the loss (times the scalar tensor gloss, if given) and of the routing weights (gw)."""
     a, T, H, E, K, head, ids = _router_args("moe_router_loss_grad", X, x_dtype, W_router, topk_idx, mask)
     if gloss is not None and gloss.dim():
+        if gloss.numel() != 1:
+            a.fail(f"gloss has shape {tuple(gloss.shape)}, not one value", -2)
         gloss = gloss.reshape(())
     return a.run(lib().moe_router_loss_grad, stream, *head, *ids, a("logits", logits, _F32, T, E),
                  a("lse", lse, _F32, T), a("counts", counts, _I32, E + 1), T, H, E, K, alpha, beta,

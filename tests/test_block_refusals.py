@@ -30,3 +30,13 @@ def test_missing_tensors():
     ad = torch.zeros(4, dtype=torch.int32)
     for X, a, b in ((None, A, B), (h, None, B), (h, A, None)):
         refused(-1, M.moe_adapters, X, M.MPB_BF16, a, b, None, None, ad, None, torch.zeros(4, 64), ws)
+
+
+def test_a_loss_gradient_of_several_values():
+    M = lib_m()
+    X, W, idx = torch.zeros(4, 128).bfloat16(), torch.zeros(8, 128), torch.zeros(4, 2, dtype=torch.int32)
+    o = [torch.zeros(4, 8), torch.zeros(4), torch.zeros(9, dtype=torch.int32)]
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    for gloss in (torch.ones(3), torch.ones(0), torch.ones(2, 1)):
+        refused(-2, M.moe_router_loss_grad, X, M.MPB_BF16, W, idx, None, *o, 0.1, 0.1, None, gloss, None, W, None, ws)
+    refused(-1, M.moe_router_loss_grad, X, M.MPB_BF16, W, idx, None, *o, 0.1, 0.1, None, torch.ones(1, 1), None, W, None, ws)
