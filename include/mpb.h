@@ -358,8 +358,10 @@ int moe_router_loss(const void* X_dev, int x_dtype, const float* W_router_dev, c
  *   gloss_dev   device fp32 scalar, the gradient of loss[0], or NULL (1)
  *   dX_dev [T][H], dW_dev [E][H], dbias_dev [E]   fp32 (the gradients of a
  *               mean over a batch fall below fp16's range), each may be NULL
- * Products of exact fp32 parts accumulated in fp32, every sum in a fixed
- * order. Workspace (the forward call's may be reused), limits and errors as
+ * Accumulated in fp32, every sum in a fixed order: dW from dl and X exactly,
+ * dX from dl and W_router to 22 bits each, where a value is not below 2^-28 of
+ * its token's largest dl or its column's largest W_router (below that to 2^-49
+ * of the largest). Workspace (the forward call's may be reused), limits and errors as
  * above.
  */
 int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_dev, const int32_t* topk_idx_dev,

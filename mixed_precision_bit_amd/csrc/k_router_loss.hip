@@ -313,14 +313,18 @@ __device__ __forceinline__ float scale_for(float m) {
   return ldexpf(1.0f, k > 126 ? 126 : k);
 }
 
-// x = hi + lo in fp16, both rounded to nearest: 22 bits of x, or 2^-25 where x
-// is small against its row's largest value (scale_for: 2^-38 of that). Three
-// products of halves, hi hi + hi lo + lo hi, are then within 12 x 2^-24 of the
-// exact product: half the matrix work of three bf16 parts, where a power of two
-// per row and per column can be taken out of the product.
+// x = hi + lo / kLo in fp16, both rounded to nearest: 22 bits of x. Without kLo,
+// lo would fall below fp16's smallest step (2^-24) where x is under 2^-17 of its
+// row's largest value (scale_for), and leave errors of 2^-38 of that; with it they
+// stay below 2^-49 of it. Three products of halves, hi hi + (hi lo + lo hi) / kLo,
+// are then within 12 x 2^-24 of the exact product (and of 2^-49 of the row's or
+// column's largest value): half the matrix work of three bf16 parts, where a power
+// of two per row and per column can be taken out of the product.
+constexpr float kLo = 2048.0f;
+
 __device__ __forceinline__ void halves(fx8 x, hx8 (&q)[2]) {
   q[0] = narrow<F16>(x);
-  q[1] = narrow<F16>(x - widen<F16>(q[0]));
+  q[1] = narrow<F16>((x - widen<F16>(q[0])) * kLo);
 }
 
 __device__ __forceinline__ size_t frag(size_t tiles, size_t part, size_t tile) { return (part * tiles + tile) * 512; }
@@ -435,10 +439,12 @@ __global__ __launch_bounds__(1024) void k_router_dl(RouterLossParams p) {
 // goes over its range of tokens, 256 at a time; a wave holds 64 tokens x 64
 // columns. The columns are the products' rows, so that a lane ends with four of
 // a token's consecutive columns. Ranges of tokens are dealt to the XCDs, so that
-// each L2 holds its own part of dl. 16381 x 4096 x 128: 73 us for 268 MB written
-// (3.7 TB/s) and 52 GFLOP of products; with plain stores 75 (and 65 instead of 57
-// for dW behind it, whose operands they push out), with stores of 64 bytes a row 82, with three bf16 parts 115, with both operands read from L2 as
-// bf16 fragments 135.
+// each L2 holds its own part of dl. 16381 x 4096 x 128: 77 us for 268 MB written
+// (3.5 TB/s) and 52 GFLOP of products; without kLo, which takes the products with
+// a second half apart, 73. Measured without it: with plain stores 75 (and 65 instead
+// of 57 for dW behind it, whose operands they push out), with stores of 64 bytes a
+// row 82, with three bf16 parts 115, with both operands read from L2 as bf16
+// fragments 135.
 __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
   __shared__ __align__(16) _Float16 wl[2 * 4 * 4 * 512];  // [half][column / 16][expert / 32] fragments
   __shared__ __align__(16) float down[64];                // inverse scales of the columns
@@ -525,11 +531,16 @@ __global__ __launch_bounds__(256, 2) void k_router_dx(RouterLossParams p) {
         hx8 w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) w[i] = *(const hx8*)(wl + ((i * 4 + c) * 4 + k % 4) * 512 + 8 * lane);
+        acc4 lo[4];  // the products with a second half, times kLo
 #pragma unroll
         for (int s = 0; s < 3; ++s)  // lo hi, hi lo, hi hi
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[s == 0], a[m][s == 1], acc[m][c], 0, 0, 0);
+          for (int m = 0; m < 4; ++m) {
+            acc4& to = s < 2 ? lo[m] : acc[m][c];
+            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[s == 0], a[m][s == 1], s ? to : (acc4)(0.0f), 0, 0, 0);
+          }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[m][c] += lo[m] * (1.0f / kLo);
       }
     }
     // through LDS (one wave's accesses run in order), to store whole lines
