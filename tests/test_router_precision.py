@@ -22,7 +22,7 @@ import math
 
 import pytest
 
-from test_router_loss import DT, U, check, clean, dbl, inputs, run_fwd, run_grad
+from test_router_loss import DT, U, check, check_fwd, clean, dbl, inputs, run_fwd, run_grad
 
 torch = pytest.importorskip("torch")
 
@@ -115,3 +115,94 @@ def test_dx_of_spread_rows(T, H, E, K, gw, dt):
     dl, made, tol = gradient(o, d, gw=gw)
     W = d["W"].double()
     check(run_grad(d, dt, o, gw=gw, want=("dX",))["dX"], dl @ W, dx_tol(dl, tol, W), "dX")
+
+
+# ---------------------------------------------------------------- products to fp32 accuracy, by the norm of their errors
+def far(n):
+    """Tolerance of an error's norm, in units of u and of the norm of what the sums are made of (the root of the sum of
+    their terms' squares, or the sum where that is larger). Roundings of u / sqrt(3) each, independent, at partial sums
+    that grow to the whole: sqrt(n / 6) of them over n; three times that, and 8 for what each term carries by itself."""
+    return (8 + 3 * (n / 6) ** 0.5) * U
+
+
+def norms(got, terms_sq, ref, n, what):
+    """The error's norm over the whole result against far(n)."""
+    size = torch.maximum(terms_sq.sqrt(), ref.abs())
+    err = float((got.double() - ref).norm() / size.norm())
+    assert err <= far(n), f"{what}: error {err / U:.1f} u, tolerance {far(n) / U:.1f} u"
+
+
+def check_products(d, dt, o, g, gw):
+    """Logits from X and W, then dX, dW and dbias from dl of the stored logits: element by element, and in norm."""
+    D = clean(dbl(d))
+    (T, H), E = D["X"].shape, D["W"].shape[0]
+    X, W = D["X"], D["W"]
+    ref = X @ W.t()
+    b = 0.0 if D["b"] is None else D["b"]
+    live = torch.ones(T, dtype=torch.bool, device=X.device) if D["mask"] is None else D["mask"].bool()
+    norms(o["logits"][live], ((X * X) @ (W * W).t() + b * b)[live], (ref + b)[live], 6 * H / 32 + 32, "logits")
+    dl, made, tol = gradient(o, d, gw=gw)
+    made_sq = made * made
+    # of what an element is made of, dl keeps (|l - lse| + 40) u at most and a tenth of that as a rule
+    n_dx, n_dw = 4 * E / 32 + 40, 6 * T / 32 + 260
+    check(g["dX"], dl @ W, dx_tol(dl, tol, W), "dX")
+    norms(g["dX"], made_sq @ (W * W), dl @ W, n_dx, "dX")
+    ax = X.abs()
+    check(g["dW"], dl.t() @ X, tol.t() @ ax + (n_dw + 4) * U * (dl.abs().t() @ ax) + 1e-37, "dW")
+    norms(g["dW"], made_sq.t() @ (X * X), dl.t() @ X, n_dw, "dW")
+    check(g["db"], dl.sum(0), tol.sum(0) + 34 * U * dl.abs().sum(0) + 1e-37, "dbias")
+    norms(g["db"], made_sq.sum(0), dl.sum(0), 64, "dbias")
+
+
+PRODUCTS = [(1, 2048, 60, 4), (72, 2048, 60, 4), (33, 128, 512, 16), (700, 320, 129, 8), (65, 65536, 4, 2),
+            (1000, 2816, 128, 8), (4099, 256, 60, 4)]
+# 128-token tiles of the logits (from 8192 tokens) with 64 and 128 experts, whole and ragged, dX over several blocks of
+# 256 tokens a workgroup with and without W taken in again between them
+LARGE = [(8192, 512, 60, 4), (8209, 512, 128, 8), (8209, 2816, 60, 4), (8209, 2816, 300, 8), (16381, 2048, 128, 8)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,H,E,K", PRODUCTS + LARGE)
+def test_products(T, H, E, K, masked, dt):
+    d = inputs(T, H, E, K, dt, masked, seed=T + E)
+    o = run_fwd(d, dt)
+    if T >= 8192:
+        check_fwd(d, dt, o)
+    for gw in (True, False):
+        check_products(d, dt, o, run_grad(d, dt, o, gw=gw), gw)
+
+
+def parts(x, n):
+    """The first n bf16 parts of x, cut off by truncation."""
+    x, out = x.float(), 0.0
+    for _ in range(n):
+        p = (x.view(torch.int32) & -65536).view(torch.float32)
+        out, x = out + p.double(), x - p
+    return out
+
+
+@pytest.mark.parametrize("T,H,E,K", [(72, 2048, 60, 4), (700, 320, 129, 8), (300, 2816, 128, 8)])
+def test_fewer_parts_are_noticed(T, H, E, K):
+    """Planted in the reference's own values, on the CPU: W in two parts for the logits, dl in two parts or rounded to
+    bf16 for the gradients, each outside; the whole values are inside."""
+    g = torch.Generator().manual_seed(T)
+    X = torch.randn(T, H, generator=g).bfloat16()
+    W = torch.randn(E, H, generator=g) * H ** -0.5
+    d = {"X": X, "W": W, "b": -0.5 * torch.log1p(torch.arange(E).float()), "mask": None, "gw": torch.randn(T, K, generator=g) / T}
+    l = X.double() @ W.double().t() + d["b"]
+    d["idx"] = torch.topk(l, K, dim=1).indices.int()
+    counts = torch.cat([torch.bincount(d["idx"].flatten().long(), minlength=E), torch.tensor([T])])
+    o = {"logits": l, "lse": torch.logsumexp(l, 1), "counts": counts}
+    for gw in (True, False):
+        dl = gradient(o, d, gw=gw)[0]
+        grads = lambda q: {"dX": q @ W.double(), "dW": q.t() @ X.double(), "db": q.sum(0)}  # noqa: E731
+        check_products(d, "bf16", o, grads(dl.float().double()), gw)
+        for q in (dl.bfloat16().double(), parts(dl, 2)):
+            for k in ("dX", "dW"):
+                with pytest.raises(AssertionError, match=k):
+                    check_products(d, "bf16", o, {**grads(dl), k: grads(q)[k]}, gw)
+        short = {**o, "logits": X.double() @ parts(W, 2).t() + d["b"]}
+        with pytest.raises(AssertionError, match="logits"):
+            check_products(d, "bf16", short, grads(dl), gw)
