@@ -698,7 +698,7 @@ RouterLossWs router_loss_ws(int T, int H, int E) {
   RouterLossWs w{};
   // 128-token tiles where the batch fills the chip with them, else 64
   w.mt = T >= 8192 ? 8 : 4;
-  w.et = E > 64 && T >= 8192 ? 2 : 1;
+  w.et = w.mt == 8 && E > 64 ? 2 : 1;
   const int tiles = ((T + 16 * w.mt - 1) / (16 * w.mt)) * ((E + 64 * w.et - 1) / (64 * w.et));
   // ranges of H for the logits: about 512 workgroups, whole stages of 64
   w.splits = tiles > 0 ? 512 / tiles : 1;
@@ -739,9 +739,9 @@ RouterLossWs router_loss_ws(int T, int H, int E) {
 template <class D>
 static void logits(const RouterLossParams& p, hipStream_t s) {
   const dim3 grid(((p.T + 16 * p.mt - 1) / (16 * p.mt)) * ((p.E + 64 * p.et - 1) / (64 * p.et)), p.splits);
-  if (p.mt == 8 && p.et == 2) k_router_logits<D, 8, 2><<<grid, 256, 0, s>>>(p);
+  // 128 experts only beside 128 tokens
+  if (p.et == 2) k_router_logits<D, 8, 2><<<grid, 256, 0, s>>>(p);
   else if (p.mt == 8) k_router_logits<D, 8, 1><<<grid, 256, 0, s>>>(p);
-  else if (p.et == 2) k_router_logits<D, 4, 2><<<grid, 256, 0, s>>>(p);
   else k_router_logits<D, 4, 1><<<grid, 256, 0, s>>>(p);
 }
 
