@@ -406,7 +406,8 @@ void expand(const AdapterParams& p, dim3 grid, hipStream_t s) {
 template <class D, int MT>
 void shrink_expand(const AdapterParams& p, int tiles, hipStream_t s) {
   const dim3 gs(tiles, p.ranges), ge(tiles, (p.N + p.cols - 1) / p.cols);
-  if (p.R <= 16) k_shrink<D, MT, 1><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
+  constexpr int kLeast = MT == 1 ? 1 : 2;  // wide tiles have ranks above 16
+  if (p.R <= 16 * kLeast) k_shrink<D, MT, kLeast><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else if (p.R <= 32) k_shrink<D, MT, 2><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else if (p.R <= 64) k_shrink<D, MT, 4><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
   else k_shrink<D, MT, 8><<<gs, 64 * shrink_waves(MT), 0, s>>>(p);
