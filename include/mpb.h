@@ -330,10 +330,11 @@ int moe_block_norm_grad(const float* o_dev, const void* y_dev, int x_dtype, int 
  * The logits are exact products accumulated in fp32, in an order other than
  * moe_route's fp64 one; every sum has a fixed order (deterministic). No live
  * token: losses 0. ws_dev (16-byte aligned): at least
- * moe_router_loss_workspace_bytes(T, H, E) bytes, contents not preserved, one
- * per call that may overlap another. Infinite inputs of a live token give its
- * logits, and with them the losses, infinite or NaN values. Limits as for moe_route. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS,
- * MPB_E_HIP. Does not need mpb_init.
+ * moe_router_loss_workspace_bytes(T, H, E) bytes (for this T: a smaller batch
+ * may need more), contents not preserved, one per call that may overlap
+ * another. Infinite inputs of a live token give its logits, and with them the
+ * losses, infinite or NaN values. Limits as for moe_route. Errors: MPB_E_ARG,
+ * MPB_E_SHAPE, MPB_E_WS, MPB_E_HIP. Does not need mpb_init.
  */
 size_t moe_router_loss_workspace_bytes(int T, int H, int E);
 int moe_router_loss(const void* X_dev, int x_dtype, const float* W_router_dev, const float* bias_dev,
@@ -392,8 +393,9 @@ int moe_router_loss_grad(const void* X_dev, int x_dtype, const float* W_router_d
  * A_a or B_a holds infinite values gets infinite or NaN ones. Needs Kd and N
  * multiples of 64 (Kd <= 65536, N <= 131072), R a multiple of 8 in 8..128, n in
  * 1..4096, T <= 2^20, 16-byte aligned rows; T == 0 is a no-op. ws_dev (16-byte
- * aligned): at least moe_adapters_workspace_bytes(T, Kd, n, R) bytes, contents
- * not preserved; calls that may overlap need a workspace each. Errors:
+ * aligned): at least moe_adapters_workspace_bytes(T, Kd, n, R) bytes (for this
+ * T: a smaller batch may need more), contents not preserved; calls that may
+ * overlap need a workspace each. Errors:
  * MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS, MPB_E_HIP. Does not need mpb_init.
  */
 size_t moe_adapters_workspace_bytes(int T, int Kd, int n, int R);

@@ -421,10 +421,17 @@ AdapterWs adapter_ws(int T, int Kd, int n, int R) {
   AdapterWs w{};
   w.scan = T <= kAdapterScanT;
   // 64-token tiles, which read an adapter's weights a quarter as often, for ranks
-  // above 16 where adapters hold 256 tokens or more on average (rank 64, 2816 x
-  // 2816: 1176 tokens each 203 us against 234 with 16-token tiles, 240 each 64
-  // against 61; rank 32, 4096 x 4096, 32 each 28 against 22; rank 16, 2048 x 2048,
-  // 6600 each 354 against 331)
+  // above 16 where adapters hold 256 tokens or more on average. The whole call, us
+  // with 16- and with 64-token tiles, ranks up to R, by tokens a group (of n + 1):
+  //                            192       256       384       512       1024
+  //   R 32, 4096^2,  4 groups  21/27     23/30     28/31     35/39     55/52
+  //                 16         47/46     56/59     76/74     95/106    186/189
+  //   R 64, 2816^2,  4         25/36     30/41     30/41     38/40     53/52
+  //                 16         51/55     55/59     80/71     92/94     184/147
+  //   R 128, 2816^2, 4         39/58     47/66     54/55     58/53     84/78
+  //                 16         81/90     89/93     136/101   162/118   317/205
+  // Below 256 16-token tiles win; from there to 512 it goes by the groups, and above
+  // by the rank. Rank 16, 2048^2, 6600 tokens each: 331 against 354.
   w.mt = R > 16 && T / (n + 1) >= 256 ? 4 : 1;
   const int rows = 16 * w.mt;
   w.max_tiles = (n + 1 < T ? n + 1 : T) + T / rows;

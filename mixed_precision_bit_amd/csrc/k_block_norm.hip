@@ -10,9 +10,10 @@
 // elements, one or two per thread), so every input is read once and every output written
 // once; the two means are two workgroup sums. All arithmetic and both sums are
 // fp32; y is rounded once for r_out, and x is formed from the unrounded y.
-// Bound by HBM: 4096 x 2816 bf16 with a full gate takes 31.7 us, 4.36 TB/s of the
-// 4.9 TB/s that a large copy reaches; up to some hundred rows the launch itself
-// (3.2 us for one row of 2048).
+// Bound by HBM: 4096 x 2816 bf16 with a full gate takes 31.7 us a call among others
+// (33 by itself under a trace), 4.37 TB/s of the 4.9 TB/s that a large copy reaches; up
+// to some hundred rows the launch itself (3.1 us for one row of 2048). Times below
+// are traced ones.
 //
 // Backward, from y (the stored stream), with d = dx g_next:
 //   dy = dr_out + rms(y) (d - yh mean(d yh)),  yh = y rms(y);  dg_next = sum_t dx yh
@@ -20,9 +21,9 @@
 //   do = rms(o) (du g_post - oh mean(du g_post oh));  dg_post = sum_t du oh
 // The column sums stay in registers over the rows of a workgroup, which writes
 // one partial row; k_col_sum adds the partials in workgroup order, so results
-// do not depend on timing. 4093 x 2816 takes 50 + 4.7 us (3.6 TB/s: eight rows a
-// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 151 + 4.8
-// (4.4 TB/s).
+// do not depend on timing. 4093 x 2816 takes 50 + 4.7 us (3.7 TB/s: eight rows a
+// workgroup leave a ramp at both ends), 8192 x 4096 with a full gate 144 + 4.8
+// (4.7 TB/s).
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -281,9 +282,9 @@ inline int norm_threads(int H, int nv) { return ((H / 8 + nv - 1) / nv + 63) / 6
 
 }  // namespace
 
-// One vector a thread up to H = 4096 (one row of 2048: 3.2 us against 3.6 with
-// two; 4096 x 2816: 32.4 against 32.8), then two; past 16384 the eight vectors a
-// thread spill, which only such rows pay.
+// One vector a thread up to H = 4096 (one row of 2048: 3.1 us against 3.5 with
+// two; 4096 x 2816: 33.0 against 33.2), then two; past 16384 the eight vectors a
+// thread spill 75 registers, which only such rows pay.
 template <class D>
 static void norm_rows(const BlockNormParams& p, hipStream_t s) {
   const int grid = p.T < 4096 ? p.T : 4096;
@@ -299,11 +300,13 @@ hipError_t launch_block_norm(const BlockNormParams& p, bool bf16, hipStream_t s)
 }
 
 // Two workgroups a CU (512): more would add partial rows of 8 H bytes each, and
-// take turns on the CUs (4093 x 2816: 56 us in all against 66 with 768, 71 with 1024).
+// take turns on the CUs (4093 x 2816: 55 us in all against 63 with 768, 58 with 1024;
+// 8192 x 4096 with a full gate 148 against 158, 154).
 int block_norm_grad_groups(int T) { return T < 512 ? T : 512; }
 
 // Two vectors a thread; rows past 8192 elements leave no registers for a second
-// row, and past 16384 the eight vectors a thread spill, which only such rows pay.
+// row and spill 10 to 13 of them, and past 16384 the eight vectors a thread spill
+// some 590, which only such rows pay.
 template <class D>
 static void grad_rows(const BlockNormGradParams& p, int grid, hipStream_t s) {
   if (p.H <= 8192) k_block_norm_grad<D, 2, 512, true><<<grid, norm_threads(p.H, 2), 0, s>>>(p);

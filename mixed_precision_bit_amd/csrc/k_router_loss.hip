@@ -53,9 +53,15 @@ __device__ __forceinline__ void xcd_pairs(int b, int n, int count, int& tile, in
 // is shared by MT products); the tokens' activations are staged in LDS for all
 // four waves, 64 elements of H at a time, the next stage's loads in flight
 // during the products. Partial sums go to part[range][T][E].
-// 128 tokens x 128 experts from 8192 tokens (16381 x 4096 x 128: 63 to 66 us against 75
-// with 64 experts and 95 with 64 tokens), 64 x 64 below (4096 x 2816 x 128: 18.7
-// against 22 with 128 experts, which leave too few workgroups). The matrix cores
+// 128 tokens x 128 experts (64 where there are no more) from 8192 tokens, 64 x 64
+// below. The whole forward call, us with 64- and with 128-token tiles:
+//   tokens             4096        6000        8192        10000       16381
+//   2048 x 60, bf16    21.3/24.5   25.3/26.0   25.6/25.8   29.3/31.9   34.9/35.1
+//   2816 x 128, bf16   30.1/34.1   41.0/40.9   42.5/42.4   63.2/52.0   72.0/71.8
+//   2816 x 128, fp16   34.8/36.8   48.7/46.5   50.9/48.6   77.5/62.8   88.1/85.0
+//   2816 x 300, bf16   89.9/79.9   94.1/95.5   118/109     145/118     185/172
+// (16381 x 4096 x 128: the kernel 63 us against 95; with 128 tokens x 64 experts 75;
+// 4096 x 2816 x 128: 18.6 against 22). The matrix cores
 // are busy a third of the time: the cutting (as many VALU cycles) and the reads of
 // W, 16 bytes a cycle as a fragment's lanes lie in 16 rows, do not overlap enough
 // with them. Staging W in LDS as well (18.3 and 73 us) and loading two stages
@@ -664,7 +670,7 @@ __global__ __launch_bounds__(256, 1) void k_router_dw(RouterLossParams p) {
 }
 
 // Adds the token ranges of dW (workgroups below `dw_wgs`, 4 values a thread)
-// and the token tiles of dbias (64 experts a workgroup, 16 slices).
+// and the token tiles of dbias (16 experts a workgroup, 16 slices).
 __global__ __launch_bounds__(256) void k_router_add(RouterLossParams p, int dw_wgs) {
   __shared__ double buf[256];
   const int tid = threadIdx.x;
