@@ -131,7 +131,7 @@ def prepare(case, seed):
         s["t_lse"] = torch.logsumexp(s["teacher"] / tau, 1) - torch.log(0.5 + 0.48 * rand(T)) if case["rest"] else None
         w = torch.ones(T, device="cuda") if not case["masked"] else (rand(T) < 0.9).float()
         s["w"] = w / w.sum().clamp(min=1)                     # 0: padding
-        s |= {"stats": empty(T, 2), "kl": empty(T), "loss": empty(1)}
+        s |= {"stats": empty(T, 4), "kl": empty(T), "loss": empty(1)}
         s["dS"] = None if case["way"] == "fwd" else torch.empty_like(s["S"])
         # fp16 gradients come with a loss scale, as always: those of a mean over a batch are below its range
         s["gloss"] = torch.full((1,), 32768.0, device="cuda") if case["dtype"] == "f16" and case["way"] != "fwd" else None
@@ -260,10 +260,9 @@ def _heads(s, c):
 def _distill_own(s, c):
     import mixed_precision_bit_amd as M
     sd = {"f16": M.MPB_F16, "bf16": M.MPB_BF16, "f32": M.MPB_F32}[c["dtype"]]
-    ws = _ws(M.moe_distill_loss_workspace_bytes(c["T"]))
     dS = s["dS"] if c["way"] == "step" else None
     M.moe_distill_loss(s["S"], sd, s["ids"], s["teacher"], s["t_lse"], s["w"], c["tau"], s["stats"], s["kl"], s["loss"], dS,
-                       s["gloss"], ws)
+                       s["gloss"])
     if c["way"] == "two":
         M.moe_distill_loss_grad(s["S"], sd, s["ids"], s["teacher"], s["t_lse"], s["w"], c["tau"], s["stats"], s["dS"],
                                 s["gloss"])
