@@ -60,7 +60,7 @@ enum {
 
 enum { MPB_PAGE_GPU = 0, MPB_PAGE_CPU = 1, MPB_PAGE_IN_TRANSFER = 2 }; /* page states */
 
-enum { MPB_F16 = 0, MPB_BF16 = 1 }; /* activation dtypes */
+enum { MPB_F16 = 0, MPB_BF16 = 1, MPB_F32 = 2 }; /* activation dtypes; MPB_F32 only where a call takes it */
 
 typedef struct {
     int32_t H; /* hidden size, multiple of 64 */
@@ -402,6 +402,151 @@ size_t moe_adapters_workspace_bytes(int T, int Kd, int n, int R);
 int moe_adapters(const void* X_dev, int x_dtype, int T, int Kd, const void* A_dev, const void* B_dev,
                  const int32_t* ranks_dev, const float* scales_dev, int n, int R, int N, const int32_t* adapter_dev,
                  const float* base_dev, float* out_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/*
+ * Dense projection with bias, activation and residual in its epilogue: the
+ * projection that all requests share (moe_adapters' base), the products of a dense
+ * layer, a model's output head.
+ *   z = X W^T + bias,  y = res + act(z)
+ *   X_dev       [T][Kd] x_dtype;  W_dev [N][Kd] x_dtype;  bias_dev [N] fp32 or NULL
+ *   act         MPB_ACT_*: none, relu, silu z / (1 + e^-z), gelu z Phi(z), or its
+ *               form z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
+ *   res_dev     [T][N] of y's type, or NULL; may be y_dev
+ *   z_dev       [T][N] x_dtype, what the gradient needs of an activation, or NULL
+ *   y_dev       [T][N] of y_dtype: x_dtype or MPB_F32
+ * Products are exact, sums fp32 in a fixed order (deterministic), and act is taken
+ * of the unrounded z; each output is rounded once. Needs Kd a multiple of 64 up to
+ * 65536, N a multiple of 8 up to 524288, T <= 2^20, 16-byte aligned rows; T == 0 is
+ * a no-op. ws_dev (16-byte aligned): at least moe_linear_workspace_bytes(T, Kd, N)
+ * bytes (for this T: a smaller batch may need more), contents not preserved; calls
+ * that may overlap need a workspace each. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS,
+ * MPB_E_HIP. Does not need mpb_init.
+ */
+enum { MPB_ACT_NONE = 0, MPB_ACT_RELU = 1, MPB_ACT_SILU = 2, MPB_ACT_GELU = 3, MPB_ACT_GELU_TANH = 4 };
+size_t moe_linear_workspace_bytes(int T, int Kd, int N);
+int moe_linear(const void* X_dev, int x_dtype, const void* W_dev, const float* bias_dev, int act, const void* res_dev,
+               int T, int Kd, int N, void* z_dev, void* y_dev, int y_dtype, void* ws_dev, size_t ws_bytes,
+               void* stream);
+
+/*
+ * Gradients of moe_linear (that of res is dy itself). From z as the forward call
+ * wrote it (NULL for MPB_ACT_NONE) and the gradient of y,
+ *   dz = dy act'(z);  dX = dz W,  dW = dz^T X,  dbias = sum_t dz
+ *   dy_dev      [T][N] of dy_dtype: x_dtype or MPB_F32
+ *   dX_dev      [T][Kd] x_dtype;  dW_dev [N][Kd] fp32;  dbias_dev [N] fp32; each
+ *               may be NULL (W_dev is read for dX, X_dev for dW)
+ * relu' is 0 at 0. Sums are fp32 in a fixed order (deterministic). Where dz is not
+ * dy itself (an activation, or fp32 dy) the products take it in 16-bit parts: dX,
+ * which is rounded to that type, from dz rounded to x_dtype, dW from dz to 16 bits
+ * (bf16) or 22 (fp16; those of a value not below 2^-16 of the largest |dz|, to
+ * 2^-38 of that below), dbias from dz itself. fp16 parts carry a power of two, so that small
+ * gradients keep their bits whatever their range; an infinite or NaN dz gives
+ * infinite or NaN sums. T == 0 zeroes dW and dbias. ws_dev: at least
+ * moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype) bytes. Limits and errors
+ * as above.
+ */
+size_t moe_linear_grad_workspace_bytes(int T, int Kd, int N, int act, int dy_dtype);
+int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, const void* z_dev, const void* dy_dev,
+                    int dy_dtype, int T, int Kd, int N, void* dX_dev, float* dW_dev, float* dbias_dev, void* ws_dev,
+                    size_t ws_bytes, void* stream);
+
+/*
+ * Norms of query and key heads and the rotation by their positions, in one pass:
+ * what follows the projection of queries, keys and values. For every head
+ *   n = x rms(x) gamma, rms(x) = 1 / sqrt(mean(x^2) + eps)   (n = x without gamma)
+ *   out = n with the pairs of its first Dr elements turned: pair i, (a, b), to
+ *   (a cos f - b sin f, a sin f + b cos f), f = pos[axis_i][t] freq_i
+ *   q_dev, k_dev   [T][Hq][D] and [T][Hk][D] x_dtype, q_stride and k_stride
+ *               elements from token to token (slices of one packed projection);
+ *               k_dev may be NULL with Hk 0
+ *   gamma_q_dev, gamma_k_dev   [D] fp32, or NULL: that side has no norm
+ *   pos_dev     [A][T] int32 positions, one row for each of A axes (time, height
+ *               and width of image and video tokens; A = 1 for text)
+ *   axis_dev    [Dr / 2] int32, the axis of every pair, or NULL (axis 0); a pair
+ *               whose axis is outside [0, A) is not turned
+ *   freq_dev    [Dr / 2] fp32, radians a position
+ *   pairs       MPB_PAIRS_HALVES: pair i is elements i and i + Dr / 2;
+ *               MPB_PAIRS_NEIGHBOURS: elements 2 i and 2 i + 1
+ *   q_out_dev, k_out_dev   x_dtype, their own strides; may be q_dev and k_dev with
+ *               the same strides
+ * Dr == 0: no rotation (pos, axis and freq are not used). Angles are formed in fp64
+ * and kept as a fraction of a turn: positions of 2^31 keep 2^-24 of a turn. The
+ * rest is fp32, each output rounded once. Needs D and Dr multiples of 16, 16 <= D
+ * <= 512, Dr <= D, Hq in 1..1024, Hk in 0..1024, A in 1..8, T <= 2^20, strides
+ * multiples of 8 that hold the token's heads, 16-byte aligned pointers; T == 0 is a
+ * no-op. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_HIP. Does not need mpb_init.
+ */
+enum { MPB_PAIRS_HALVES = 0, MPB_PAIRS_NEIGHBOURS = 1 };
+int moe_head_norm(const void* q_dev, int64_t q_stride, const void* k_dev, int64_t k_stride, int x_dtype, int T, int Hq,
+                  int Hk, int D, const float* gamma_q_dev, const float* gamma_k_dev, float eps, const int32_t* pos_dev,
+                  int A, const int32_t* axis_dev, const float* freq_dev, int Dr, int pairs, void* q_out_dev,
+                  int64_t q_out_stride, void* k_out_dev, int64_t k_out_stride, void* stream);
+
+/*
+ * Gradients of moe_head_norm: of q and k from those of q_out and k_out (x_dtype,
+ * strides of their own), and of the two gammas, summed over tokens and heads.
+ *   q_dev, k_dev   as in the forward call; a side without gamma is not read and may
+ *               be NULL
+ *   dq_dev, dk_dev   x_dtype; may be dq_out_dev and dk_out_dev, or q_dev and k_dev,
+ *               with the same strides
+ *   dgamma_q_dev, dgamma_k_dev   [D] fp32, or NULL
+ * Sums are fp32 in a fixed order (deterministic). ws_dev (16-byte aligned): at least
+ * moe_head_norm_grad_workspace_bytes(T, Hq, Hk, D) bytes, needed only for the gammas'
+ * gradients; contents not preserved, one per call that may overlap another. T == 0
+ * zeroes them. Limits and errors as above, plus MPB_E_WS.
+ */
+size_t moe_head_norm_grad_workspace_bytes(int T, int Hq, int Hk, int D);
+int moe_head_norm_grad(const void* q_dev, int64_t q_stride, const void* k_dev, int64_t k_stride, int x_dtype, int T,
+                       int Hq, int Hk, int D, const float* gamma_q_dev, const float* gamma_k_dev, float eps,
+                       const int32_t* pos_dev, int A, const int32_t* axis_dev, const float* freq_dev, int Dr, int pairs,
+                       const void* dq_out_dev, int64_t dq_out_stride, const void* dk_out_dev, int64_t dk_out_stride,
+                       void* dq_dev, int64_t dq_stride, void* dk_dev, int64_t dk_stride, float* dgamma_q_dev,
+                       float* dgamma_k_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/*
+ * Distillation of a teacher's stored top logits: what a model whose experts run at
+ * lower bitwidths loses against the full one, and the gradient that wins it back.
+ * For every row, with p = softmax(s / tau) over the V student logits and k stored
+ * teacher logits y_j at ids_j,
+ *   q_j = exp(y_j / tau - L)
+ *   kl  = sum_j q_j (log q_j - log p_j) + q_r (log q_r - log p_r)
+ *   loss = tau^2 sum_t weight_t kl_t
+ * Where teacher_lse_dev is given, L is the teacher's own logsumexp of y / tau over
+ * its whole vocabulary, and what the k entries leave of both distributions is one
+ * more outcome: q_r = 1 - sum_j q_j (not below 0), p_r = the student's probability
+ * of all other ids. Where it is NULL, L is taken over the k entries and q_r = 0.
+ *   S_dev       [T][V] s_dtype (MPB_F16, MPB_BF16 or MPB_F32), s_stride elements from row to
+ *               row; rows may begin at any element
+ *   ids_dev, teacher_dev   [T][k] int32 and fp32, in any order; an entry whose id is
+ *               outside [0, V) does not count, entries of one id add up their q
+ *   teacher_lse_dev   [T] fp32 or NULL
+ *   weight_dev  [T] fp32, or NULL (1 / T); a row of weight 0 (padding) is not read,
+ *               has kl 0 and a gradient of zeros
+ *   stats_dev   [T][4] fp32, for moe_distill_loss_grad
+ *   kl_dev      [T] fp32;  loss_dev [1] fp32
+ *   dS_dev      the gradient of S, s_dtype and s_stride, formed in the same launch,
+ *               or NULL; may be S_dev
+ *   gloss_dev   device fp32 scalar, the gradient of loss, or NULL (1)
+ * The gradient is gloss weight tau (Q p_v - q_v) for an entry and gloss weight tau
+ * p_v (Q - q_r / p_r) elsewhere, Q = sum_j q_j + q_r. Student logits may be -inf
+ * (masked): p_v = 0, and kl is infinite where the teacher gives such an id (or the
+ * rest, if all of it is masked) weight. A row that is -inf throughout, or has no
+ * entries, has kl 0 and a gradient of zeros. NaN and +inf logits give NaN. Exponentials
+ * are summed in fp32 in a fixed order, sums over the entries and rows in fp64. dS may
+ * not overlap S otherwise and lies at the same offset from a 16-byte boundary. Needs
+ * V in 1..400000, k in 1..256, tau in 1e-3..1e3, T <= 2^20; T == 0: loss 0. Errors:
+ * MPB_E_ARG, MPB_E_SHAPE, MPB_E_HIP. Does not need mpb_init.
+ */
+int moe_distill_loss(const void* S_dev, int s_dtype, int64_t s_stride, const int32_t* ids_dev, const float* teacher_dev,
+                     const float* teacher_lse_dev, const float* weight_dev, int T, int V, int k, float tau,
+                     float* stats_dev, float* kl_dev, float* loss_dev, void* dS_dev, const float* gloss_dev,
+                     void* stream);
+
+/* The gradient of moe_distill_loss as a call of its own, from its stats: the same
+ * arguments, results and errors. */
+int moe_distill_loss_grad(const void* S_dev, int s_dtype, int64_t s_stride, const int32_t* ids_dev,
+                          const float* teacher_dev, const float* teacher_lse_dev, const float* weight_dev, int T, int V,
+                          int k, float tau, const float* stats_dev, void* dS_dev, const float* gloss_dev, void* stream);
 
 /*
  * Commit bitwidth b for linear-block i (§3.1 and §3.3: the planner lowers or

@@ -9,8 +9,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmpb.so")
 
-MPB_F16, MPB_BF16 = 0, 1
+MPB_F16, MPB_BF16, MPB_F32 = 0, 1, 2
 MPB_GATE_NONE, MPB_GATE_TOKEN, MPB_GATE_FULL = 0, 1, 2
+MPB_ACT_NONE, MPB_ACT_RELU, MPB_ACT_SILU, MPB_ACT_GELU, MPB_ACT_GELU_TANH = 0, 1, 2, 3, 4
+MPB_PAIRS_HALVES, MPB_PAIRS_NEIGHBOURS = 0, 1
 ERRORS = {-1: "MPB_E_ARG", -2: "MPB_E_SHAPE", -3: "MPB_E_RANGE", -4: "MPB_E_NOT_RESIDENT",
           -5: "MPB_E_WS", -6: "MPB_E_HIP", -7: "MPB_E_UNINIT", -8: "MPB_E_BUSY"}
 MPB_PAGE_GPU, MPB_PAGE_CPU, MPB_PAGE_IN_TRANSFER = 0, 1, 2
@@ -54,6 +56,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_L = ctypes.c_int64
 
 
 def lib() -> ctypes.CDLL:
@@ -87,6 +90,17 @@ def lib() -> ctypes.CDLL:
                                           _P, _SZ, _P]),
             "moe_adapters_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
             "moe_adapters": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+            "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
+            "moe_linear": (_I, [_P, _I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _I, _P, _SZ, _P]),
+            "moe_linear_grad_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+            "moe_linear_grad": (_I, [_P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+            "moe_head_norm": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _I, _I, _P, _L, _P,
+                                   _L, _P]),
+            "moe_head_norm_grad_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+            "moe_head_norm_grad": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _I, _I, _P, _L,
+                                        _P, _L, _P, _L, _P, _L, _P, _P, _P, _SZ, _P]),
+            "moe_distill_loss": (_I, [_P, _I, _L, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P]),
+            "moe_distill_loss_grad": (_I, [_P, _I, _L, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P]),
             "set_committed_bits": (_I, [_I, _I]),
             "mpb_committed_bytes": (ctypes.c_int64, [_P]),
             "mpb_get_committed_bits": (_I, [_I]),
@@ -247,6 +261,27 @@ class _Args:
             self.fail(f"{what} is on {t.device}, other tensors on device {self.index}")
         return t.data_ptr()
 
+    def strided(self, what, t, dtype, *shape):
+        """(pointer, elements from row to row) of a tensor whose rows are contiguous, whatever lies between them."""
+        if t is None:
+            return None, 0
+        if t.dtype is not dtype and not (dtype.itemsize == 2 and t.dtype is torch.int16):
+            self.fail(f"{what} is {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            self.fail(f"{what} has shape {tuple(t.shape)}, not {shape}", -2)
+        if t.get_device() != self.index:
+            self.fail(f"{what} is on {t.device}, other tensors on device {self.index}")
+        row = 1
+        for d in range(t.dim() - 1, 0, -1):
+            if t.stride(d) != row and t.shape[d] > 1:
+                self.fail(f"the rows of {what} are not contiguous")
+            row *= t.shape[d]
+        if t.shape[0] < 2:
+            return t.data_ptr(), row
+        if t.stride(0) < row:
+            self.fail(f"the rows of {what} overlap")
+        return t.data_ptr(), t.stride(0)
+
     def bytes(self, ws):
         """(pointer, bytes) of a workspace."""
         if ws is None:
@@ -375,6 +410,127 @@ def moe_adapters(X, x_dtype, A, B, ranks, scales, adapter, base, out, ws, stream
     return a.run(lib().moe_adapters, stream, a("X", X, xt, T, Kd), x_dtype, T, Kd, a("A", A, xt, n, R, Kd),
                  a("B", B, xt, n, N, R), a("ranks", ranks, _I32, n), a("scales", scales, _F32, n), n, R, N,
                  a("adapter", adapter, _I32, T), a("base", base, _F32, T, N), a("out", out, _F32, T, N), *a.bytes(ws))
+
+
+def _either(a, what, t, xt, x_dtype):
+    """(dtype, its number) of a tensor that has the activations' type or fp32."""
+    if t is None:
+        a.fail(f"{what} is missing")
+    return (_F32, MPB_F32) if t.dtype is _F32 else (xt, x_dtype)
+
+
+def moe_linear_workspace_bytes(T, Kd, N) -> int:
+    return lib().moe_linear_workspace_bytes(T, Kd, N)
+
+
+def moe_linear(X, x_dtype, W, bias, act, res, z, y, ws, stream=None):
+    """z = X W^T + bias, y = res + act(z); y (and res) [T][N] of X's type or fp32, z of X's type or None."""
+    a = _Args("moe_linear", X, W, y)
+    xt = _xtype(a.name, x_dtype)
+    if X.dim() != 2 or W.dim() != 2:
+        a.fail("X is [T][Kd], W [N][Kd]", -2)
+    (T, Kd), N = X.shape, W.shape[0]
+    yt, yd = _either(a, "y", y, xt, x_dtype)
+    return a.run(lib().moe_linear, stream, a("X", X, xt, T, Kd), x_dtype, a("W", W, xt, N, Kd), a("bias", bias, _F32, N),
+                 act, a("res", res, yt, T, N), T, Kd, N, a("z", z, xt, T, N), a("y", y, yt, T, N), yd, *a.bytes(ws))
+
+
+def moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype) -> int:
+    return lib().moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype)
+
+
+def moe_linear_grad(X, x_dtype, W, act, z, dy, dX, dW, dbias, ws, stream=None):
+    """dX, dW and dbias (each may be None) of moe_linear from z as it wrote it and dy of X's type or fp32."""
+    a = _Args("moe_linear_grad", X, W, dy)
+    xt = _xtype(a.name, x_dtype)
+    if X.dim() != 2 or W.dim() != 2:
+        a.fail("X is [T][Kd], W [N][Kd]", -2)
+    (T, Kd), N = X.shape, W.shape[0]
+    dt, dd = _either(a, "dy", dy, xt, x_dtype)
+    return a.run(lib().moe_linear_grad, stream, a("X", X, xt, T, Kd), x_dtype, a("W", W, xt, N, Kd), act,
+                 a("z", z, xt, T, N), a("dy", dy, dt, T, N), dd, T, Kd, N, a("dX", dX, xt, T, Kd),
+                 a("dW", dW, _F32, N, Kd), a("dbias", dbias, _F32, N), *a.bytes(ws))
+
+
+def _heads(a, x_dtype, q, k, gamma_q, gamma_k, pos, axis, freq):
+    """(shapes of q and k, activation type, the arguments from gamma_q to Dr but eps) of a call on heads."""
+    xt = _xtype(a.name, x_dtype)
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        a.fail("q is [T][Hq][D], k [T][Hk][D]", -2)
+    T, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    A = Dr = 0
+    if freq is not None:
+        if freq.dim() != 1 or pos is None or pos.dim() != 2:
+            a.fail("freq is [Dr / 2], pos [A][T]", -2)
+        A, Dr = pos.shape[0], 2 * freq.shape[0]
+    elif pos is not None or axis is not None:
+        a.fail("a rotation needs freq")
+    return xt, T, Hq, Hk, D, (a("gamma_q", gamma_q, _F32, D), a("gamma_k", gamma_k, _F32, D)), (
+        a("pos", pos, _I32, A, T), A, a("axis", axis, _I32, Dr // 2), a("freq", freq, _F32, Dr // 2), Dr)
+
+
+def moe_head_norm(q, k, x_dtype, gamma_q, gamma_k, eps, pos, axis, freq, pairs, q_out, k_out, stream=None):
+    """Norms and rotation of query and key heads [T][H][D] (views of one packed projection are fine); k may be None."""
+    a = _Args("moe_head_norm", q)
+    xt, T, Hq, Hk, D, gammas, rot = _heads(a, x_dtype, q, k, gamma_q, gamma_k, pos, axis, freq)
+    return a.run(lib().moe_head_norm, stream, *a.strided("q", q, xt, T, Hq, D), *a.strided("k", k, xt, T, Hk, D), x_dtype,
+                 T, Hq, Hk, D, *gammas, eps, *rot, pairs, *a.strided("q_out", q_out, xt, T, Hq, D),
+                 *a.strided("k_out", k_out, xt, T, Hk, D))
+
+
+def moe_head_norm_grad_workspace_bytes(T, Hq, Hk, D) -> int:
+    return lib().moe_head_norm_grad_workspace_bytes(T, Hq, Hk, D)
+
+
+def moe_head_norm_grad(q, k, x_dtype, gamma_q, gamma_k, eps, pos, axis, freq, pairs, dq_out, dk_out, dq, dk, dgamma_q,
+                       dgamma_k, ws, stream=None):
+    """Gradients of moe_head_norm; q (or k) may be None where its side has no gamma."""
+    a = _Args("moe_head_norm_grad", dq_out)
+    xt, T, Hq, Hk, D, gammas, rot = _heads(a, x_dtype, dq_out, dk_out, gamma_q, gamma_k, pos, axis, freq)
+    return a.run(lib().moe_head_norm_grad, stream, *a.strided("q", q, xt, T, Hq, D), *a.strided("k", k, xt, T, Hk, D),
+                 x_dtype, T, Hq, Hk, D, *gammas, eps, *rot, pairs, *a.strided("dq_out", dq_out, xt, T, Hq, D),
+                 *a.strided("dk_out", dk_out, xt, T, Hk, D), *a.strided("dq", dq, xt, T, Hq, D),
+                 *a.strided("dk", dk, xt, T, Hk, D), a("dgamma_q", dgamma_q, _F32, D),
+                 a("dgamma_k", dgamma_k, _F32, D), *a.bytes(ws))
+
+
+_ST = {**_XT, MPB_F32: torch.float32}
+
+
+def _distill(a, S, s_dtype, ids, teacher, teacher_lse, weight, tau, dS, gloss):
+    """(arguments up to tau, T, dS, gloss) of a distillation call."""
+    if s_dtype not in _ST:
+        a.fail(f"bad s_dtype {s_dtype!r}")
+    st = _ST[s_dtype]
+    if S.dim() != 2 or ids.dim() != 2:
+        a.fail("S is [T][V], ids [T][k]", -2)
+    (T, V), k = S.shape, ids.shape[1]
+    p, ld = a.strided("S", S, st, T, V)
+    d, dld = a.strided("dS", dS, st, T, V)
+    if dS is not None and dld != ld:
+        a.fail(f"dS has a row stride of {dld}, S of {ld}")
+    if gloss is not None and gloss.dim():
+        if gloss.numel() != 1:
+            a.fail(f"gloss has shape {tuple(gloss.shape)}, not one value", -2)
+        gloss = gloss.reshape(())
+    return (p, s_dtype, ld, a("ids", ids, _I32, T, k), a("teacher", teacher, _F32, T, k),
+            a("teacher_lse", teacher_lse, _F32, T), a("weight", weight, _F32, T), T, V, k, tau), T, d, a("gloss", gloss, _F32)
+
+
+def moe_distill_loss(S, s_dtype, ids, teacher, teacher_lse, weight, tau, stats, kl, loss, dS, gloss, stream=None):
+    """Loss of student logits S [T][V] against a teacher's top logits [T][k]; with dS its gradient in the same launch."""
+    a = _Args("moe_distill_loss", S, ids, teacher)
+    head, T, d, g = _distill(a, S, s_dtype, ids, teacher, teacher_lse, weight, tau, dS, gloss)
+    return a.run(lib().moe_distill_loss, stream, *head, a("stats", stats, _F32, T, 4), a("kl", kl, _F32, T),
+                 a("loss", loss, _F32, 1), d, g)
+
+
+def moe_distill_loss_grad(S, s_dtype, ids, teacher, teacher_lse, weight, tau, stats, dS, gloss, stream=None):
+    """The gradient of moe_distill_loss from the stats that it wrote."""
+    a = _Args("moe_distill_loss_grad", S, ids, teacher)
+    head, T, d, g = _distill(a, S, s_dtype, ids, teacher, teacher_lse, weight, tau, dS, gloss)
+    return a.run(lib().moe_distill_loss_grad, stream, *head, a("stats", stats, _F32, T, 4), d, g)
 
 
 def set_committed_bits(i, b):

@@ -1,0 +1,657 @@
+// Matrix products with bias, activation and residual in their epilogue, and their
+// gradients.
+//
+//   z = X W^T + bias,  y = res + act(z)              X [T][Kd], W [N][Kd]
+//   dz = dy act'(z);  dX = dz W;  dW = dz^T X;  dbias = sum_t dz
+//
+// One product kernel, C[m][n] = sum_k A(m, k) B(n, k), for all three: an operand
+// lies with its reduction contiguous (X and W forward, dz in dX) or as the rows of
+// the other index (W in dX, dz and X in dW), which LDS's transposing reads turn on
+// the way into the registers. Tiles of 64 of the reduction go straight from memory to LDS, two buffers,
+// one barrier a step; a wave holds its part of the output in registers and
+// multiplies 16 x 16 x 32 at a time. Accumulation is fp32, every sum has a fixed
+// order (reductions split over workgroups leave partial sums that a second launch
+// adds in order).
+//
+// A batch of up to 16 tokens reads W once and has nothing to share: k_skinny, W
+// straight into the registers.
+//
+// dz is formed once, in the activations' type, for both gradients. Where it is not
+// exactly dy (an activation, or fp32 dy) it is rounded for dX, whose result is
+// rounded to the same type anyway, and kept as two parts for dW, whose result is
+// fp32: 16 bits of bf16, 22 of fp16. fp16 parts are scaled by a power of two that
+// brings the largest |dz| to 2^14, so that the gradients of a mean, below fp16's
+// range, keep their bits.
+#include "k_block_common.h"
+#include "mpb.h"
+#include "mpb_internal.h"
+
+namespace mpb {
+
+namespace {
+
+typedef _Float16 hx4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bx4 __attribute__((ext_vector_type(4)));
+typedef short sx4 __attribute__((ext_vector_type(4)));
+typedef short sx8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <class D>
+struct Half;
+template <>
+struct Half<F16> {
+  typedef hx4 vec4;
+};
+template <>
+struct Half<BF16> {
+  typedef bx4 vec4;
+};
+
+template <class D>
+__device__ __forceinline__ acc4 product(typename D::vec a, typename D::vec b, acc4 c);
+template <>
+__device__ __forceinline__ acc4 product<F16>(hx8 a, hx8 b, acc4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ acc4 product<BF16>(bx8 a, bx8 b, acc4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- activations
+constexpr float kSqrtHalf = 0.707106781f, kInvSqrt2Pi = 0.398942280f;
+constexpr float kTanhA = 0.797884561f, kTanhB = 0.044715f;  // sqrt(2 / pi)
+
+// gelu_tanh is z sigmoid(2 u), u = a (z + b z^3): 1 + tanh(u) = 2 sigmoid(2 u),
+// which keeps its relative accuracy where tanh is close to -1.
+__device__ __forceinline__ float act_of(float z, int act) {
+  switch (act) {
+    case MPB_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case MPB_ACT_SILU: return z * sigmoid(z);
+    case MPB_ACT_GELU: return 0.5f * z * erfcf(-z * kSqrtHalf);
+    case MPB_ACT_GELU_TANH: return z * sigmoid(2.0f * kTanhA * (z + kTanhB * z * z * z));
+    default: return z;
+  }
+}
+// z is limited where the derivative has long been 0 or 1, so that no inf meets a 0.
+__device__ __forceinline__ float act_grad(float z, int act) {
+  switch (act) {
+    case MPB_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    case MPB_ACT_SILU: {
+      const float x = z != z ? z : fminf(fmaxf(z, -120.0f), 120.0f);
+      return sigmoid(x) * (1.0f + x * sigmoid(-x));
+    }
+    case MPB_ACT_GELU: {
+      const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f);
+      return 0.5f * erfcf(-x * kSqrtHalf) + x * kInvSqrt2Pi * expf(-0.5f * x * x);
+    }
+    case MPB_ACT_GELU_TANH: {
+      const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f);
+      const float u = 2.0f * kTanhA * (x + kTanhB * x * x * x), s = sigmoid(u);
+      return s + x * s * sigmoid(-u) * 2.0f * kTanhA * (1.0f + 3.0f * kTanhB * x * x);
+    }
+    default: return 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------- epilogue
+// NV (4 or 8) consecutive results of row m from column n on.
+template <class D, int NV>
+__device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, float (&v)[NV]) {
+  typedef typename D::elem elem;
+  typedef elem evec __attribute__((ext_vector_type(NV)));
+  typedef float fvec __attribute__((ext_vector_type(NV)));
+  typedef float fx4a __attribute__((ext_vector_type(4)));
+  const size_t at = (size_t)m * o.N + n;
+  if (o.scale) {
+    const float k = *o.scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] *= k;
+  }
+  if (o.bias) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      const fx4a b = *(const fx4a*)(o.bias + n + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] += b[j];
+    }
+  }
+  if (o.z) {
+    fvec z;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] = v[i];
+    *(evec*)((elem*)o.z + at) = __builtin_convertvector(z, evec);
+  }
+  if (o.act != MPB_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = act_of(v[i], o.act);
+  }
+  if (o.y32) {
+    float* y = (float*)o.y + at;
+    const float* res = (const float*)o.res + at;
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      fx4a w = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+      if (o.res) w += *(const fx4a*)(res + i);
+      *(fx4a*)(y + i) = w;
+    }
+  } else {
+    fvec w;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w[i] = v[i];
+    if (o.res) w += __builtin_convertvector(*(const evec*)((const elem*)o.res + at), fvec);
+    *(evec*)((elem*)o.y + at) = __builtin_convertvector(w, evec);
+  }
+}
+
+// ---------------------------------------------------------------- operands in LDS
+// 16 bytes a lane from src + off to LDS at byte `lds` + 16 lane (src and lds are the
+// wave's). The load has no register of its own that could be reused early, and
+// its address registers are read when it issues; the caller waits for vmcnt(0) before the
+// barrier that hands the buffer over. The builtin of this load makes the compiler
+// wait for it before any transposing read of LDS, of the other buffer too. m0 is
+// reserved to such instructions: nothing else in these kernels counts on its value.
+__device__ __forceinline__ void load_lds16(const char* src, uint32_t off, uint32_t lds) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot parse the operands
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src) : "memory");
+#endif
+}
+// A pointer that is the same in every lane, in scalar registers.
+__device__ __forceinline__ const char* wave_uniform(const char* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const char*)((uint64_t)hi << 32 | lo);
+}
+// Every load of the wave has arrived.
+__device__ __forceinline__ void loads_done() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#endif
+}
+
+// A tile of R rows (of A or B) by 64 of the reduction, 128 R bytes, in one of two forms:
+//  rows   row r at 128 r, its 16-byte pieces c at c ^ swz(r): the 16 rows that a
+//         fragment reads at once take turns on the banks
+//  turned reduction index k at 2 R k, its 32-byte pieces (16 rows) s at s ^ swz(k)
+// A wave writes 1 KiB at a time (lane i the i-th 16 bytes, which is all that a
+// direct load can do), so the swizzle is in the addresses that it loads from.
+template <int R, int NW, bool TURNED, int SH>
+struct Operand {
+  static constexpr int NI = R / 8 / NW;  // loads of a wave and step
+  const char* base;                      // the tile's first row (rows) or column (turned), at the first step
+  int64_t stride;                        // bytes of a source row
+  uint32_t off[NI];                      // the lane's bytes within a step's source
+  int k[NI];                             // reduction index of the lane's bytes within the step
+
+  static __device__ __forceinline__ int swz_row(int r) { return (r & 3) | ((r >> SH & 1) << 2); }
+  static __device__ __forceinline__ int swz_k(int kk) { return ((kk & 3) | ((kk >> 3 & 1) << 2)) & (R / 16 - 1); }
+
+  // rows: the operand's rows in all (rows past them repeat the last: their results are not stored)
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
+    stride = 2 * ld;
+    const int left = (int)(rows - r0 < R ? rows - r0 : R);
+    base = (const char*)p + (TURNED ? 2 * r0 : r0 * stride);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int o = ((i * NW + wave) << 10) + 16 * lane;
+      if constexpr (TURNED) {
+        const int kk = o / (2 * R), s = (o % (2 * R) / 32) ^ swz_k(kk);
+        const int col = 16 * s + 8 * (o >> 4 & 1);
+        off[i] = (uint32_t)(kk * stride + 2 * min(col, left - 8));
+        k[i] = kk;
+      } else {
+        const int r = o >> 7, c = (o >> 4 & 7) ^ swz_row(r);
+        off[i] = (uint32_t)(min(r, left - 1) * stride + 16 * c);
+        k[i] = 8 * c;
+      }
+    }
+  }
+  __device__ __forceinline__ const char* at(int step) const { return base + (TURNED ? step * 64 * stride : (int64_t)step * 128); }
+  // A whole step.
+  __device__ __forceinline__ void load(const char* from, uint32_t lds, int wave) const {
+    const char* src = wave_uniform(from);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      load_lds16(src, off[i], lds + ((i * NW + wave) << 10));
+  }
+  // The last step of a reduction that ends inside it: zeros from index `left` on.
+  __device__ __forceinline__ void load_tail(const char* src, uint32_t lds, int wave, int lane, int left) const {
+    ux4 v[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      v[i] = (ux4)(0u);
+      if (k[i] < left) v[i] = *(const ux4*)(src + off[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      *(__attribute__((address_space(3))) ux4*)(uintptr_t)(lds + ((i * NW + wave) << 10) + 16 * lane) = v[i];
+  }
+};
+
+// A fragment: lane l holds row (first + its row among 16) at reduction indices 8 (l / 16) ... + 7.
+__device__ __forceinline__ ux4 read_rows(uint32_t a) { return *(const __attribute__((address_space(3))) ux4*)(uintptr_t)a; }
+// Turned: each read gives the lane its row at 4 indices; its 16 lanes address 4
+// rows of 16 elements, 8 bytes each.
+__device__ __forceinline__ ux4 read_turned(uint32_t a, uint32_t step4) {
+  typedef __attribute__((address_space(3))) sx4 lds_sx4;
+  const sx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_sx4*)(uintptr_t)a);
+  const sx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_sx4*)(uintptr_t)(a + step4));
+  sx8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+  return __builtin_bit_cast(ux4, v);
+}
+
+// ---------------------------------------------------------------- the product
+// Workgroup b works on unit() b: the dispatcher hands b to XCD b % 8, and an XCD takes
+// neighbouring tiles (8 rows of tiles at a time), so that its L2 holds the operands that they share.
+__device__ __forceinline__ int unit(int b, int n) {
+  const int x = b & 7, q = n >> 3, r = n & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+
+template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearProduct p) {
+  typedef typename D::vec vec;
+  constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, MF = WM / 16, NF = WN / 16;
+  // Rows of B within a wave's fragments: fragment j's row r is column 4 NF (r / 4) +
+  // 4 j + r % 4 of the wave's part, so that a lane ends up with 4 NF consecutive
+  // columns of one row of C. Turned operands come in 16 consecutive columns.
+  constexpr int SHB = NF == 4 ? 4 : 3;
+  static_assert(NF == 4 || NF == 2, "");
+  extern __shared__ __align__(16) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int id = unit(blockIdx.x, gridDim.x), tiles = p.tm * p.tn;
+  const int split = id / tiles, tile = id - split * tiles;
+  const int grp = tile / (8 * p.tn), rest = tile - grp * 8 * p.tn, gm = min(8, p.tm - 8 * grp);
+  const int64_t m0 = (int64_t)(8 * grp + rest % gm) * BM;
+  const int64_t n0 = (int64_t)(rest / gm) * BN;
+
+  Operand<BM, NW, AT, 2> oa;
+  Operand<BN, NW, BT, SHB> ob;
+  oa.init(p.A, p.lda, m0, p.M, wave, lane);
+  ob.init(p.B, p.ldb, n0, p.N, wave, lane);
+  constexpr uint32_t kA = 128 * BM, kBuf = 128 * (BM + BN);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)smem;
+
+  // steps of this workgroup: the reduction once, or twice with A's two parts (first A, then A2)
+  const int steps = p.steps, s0 = split * p.per, s1 = min(s0 + p.per, steps * p.parts);
+  const int64_t part2 = (const char*)p.A2 - (const char*)p.A;
+  auto stage = [&](int s, uint32_t lds) {
+    const bool second = s >= steps;
+    const int at = second ? s - steps : s;
+    const char* a = oa.at(at) + (second ? part2 : 0);
+    const char* b = ob.at(at);
+    const int left = (int)p.K - 64 * at;
+    if (left >= 64) {
+      oa.load(a, lds, wave);
+      ob.load(b, lds + kA, wave);
+    } else {
+      oa.load_tail(a, lds, wave, lane, left);
+      ob.load_tail(b, lds + kA, wave, lane, left);
+    }
+  };
+
+  const int wm = (wave / NWN) * WM, wn = (wave % NWN) * WN, r = lane & 15, g = lane >> 4;
+  // fragment addresses within a buffer
+  uint32_t fa[AT ? MF : 1], fb[BT ? NF : 1];
+  if constexpr (AT) {
+    const int kk = 8 * g + (r >> 2);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) fa[i] = 2 * BM * kk + 32 * ((wm / 16 + i) ^ oa.swz_k(kk)) + 8 * (r & 3);
+  } else {
+    fa[0] = 128 * (wm + r) + 16 * (g ^ (r & 7));
+  }
+  if constexpr (BT) {
+    const int kk = 8 * g + (r >> 2);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) fb[j] = kA + 2 * BN * kk + 32 * ((wn / 16 + j) ^ ob.swz_k(kk)) + 8 * (r & 3);
+  } else {
+    fb[0] = kA + 128 * (wn + 4 * NF * (r >> 2) + (r & 3)) + 16 * (g ^ (r & 7));
+  }
+
+  acc4 acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = (acc4)(0.0f);
+
+  if (s0 < s1) stage(s0, lds0);
+  for (int s = s0; s < s1; ++s) {
+    const uint32_t buf = lds0 + ((s - s0) & 1) * kBuf;
+    // this step's operands have arrived, and every wave is done with the other buffer
+    loads_done();
+    __syncthreads();
+    if (s + 1 < s1) stage(s + 1, lds0 + (~(s - s0) & 1) * kBuf);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      ux4 b[NF], a[MF];
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        b[j] = BT ? read_turned(buf + fb[BT ? j : 0] + 64 * BN * ks, 8 * BN) : read_rows(buf + (fb[0] ^ (64 * ks)) + 512 * j);
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+        a[i] = AT ? read_turned(buf + fa[AT ? i : 0] + 64 * BM * ks, 8 * BM) : read_rows(buf + (fa[0] ^ (64 * ks)) + 2048 * i);
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+          acc[i][j] = product<D>(__builtin_bit_cast(vec, b[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
+    }
+  }
+
+  // lane (r, g): row r of each 16, columns 4 NF g ... (rows) or 16 j + 4 g ... (turned)
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    const int64_t m = m0 + wm + 16 * i + r;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int j = 0; j < NF; j += BT ? 1 : 2) {
+      const int64_t n = n0 + wn + (BT ? 16 * j + 4 * g : 4 * NF * g + 4 * j);
+      if (n >= p.N) continue;
+      constexpr int NV = BT ? 4 : 8;
+      float v[NV];
+#pragma unroll
+      for (int e = 0; e < NV; ++e) v[e] = acc[i][j + e / 4][e & 3];
+      if (p.partial) {
+        float* to = p.partial + ((size_t)split * p.M + m) * p.N + n;
+#pragma unroll
+        for (int e = 0; e < NV; e += 4) *(fx4*)(to + e) = fx4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+      } else {
+        finish<D, NV>(p.out, m, (int)n, v);
+      }
+    }
+  }
+}
+
+// Adds the partial sums of a split reduction in their order, 8 columns a thread.
+template <class D>
+__global__ __launch_bounds__(256) void k_join(LinearProduct p, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n8 = p.N / 8;
+  if (i >= p.M * n8) return;
+  const int64_t m = i / n8;
+  const int n = (int)(i - m * n8) * 8;
+  const float* src = p.partial + (size_t)m * p.N + n;
+  const size_t step = (size_t)p.M * p.N;
+  fx8 s = load8(src);
+  int k = 1;
+  for (; k + 3 < splits; k += 4) {
+    fx8 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = load8(src + (k + j) * step);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += v[j];
+  }
+  for (; k < splits; ++k) s += load8(src + k * step);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = s[j];
+  finish<D, 8>(p.out, m, n, v);
+}
+
+// ---------------------------------------------------------------- few tokens
+constexpr int kSkinnyWaves = 16;
+
+// 16 rows of W a workgroup; its 16 waves take every 16th piece of 64 of the
+// reduction, both operands straight into registers, and their sums are added in
+// wave order. Whole 128-byte lines of W, once.
+template <class D>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
+  typedef typename D::vec vec;
+  __shared__ float sums[kSkinnyWaves][16][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int T = (int)p.M;
+  const char* w = (const char*)p.B + ((n0 + r < p.N ? n0 + r : p.N - 1) * p.ldb + 8 * g) * 2;
+  const char* x = (const char*)p.A + ((int64_t)min(r, T - 1) * p.lda + 8 * g) * 2;
+  const int pieces = (int)(p.K / 64);
+  acc4 acc = (acc4)(0.0f);
+  constexpr int U = 4;  // pieces in flight
+  int c = wave;
+  for (; c + (U - 1) * kSkinnyWaves < pieces; c += U * kSkinnyWaves) {
+    vec a[U][2], b[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = (int64_t)(c + u * kSkinnyWaves) * 128 + 64 * h;
+        b[u][h] = stream_load((const vec*)(w + at));
+        a[u][h] = *(const vec*)(x + at);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) acc = product<D>(b[u][h], a[u][h], acc);
+  }
+  for (; c < pieces; c += kSkinnyWaves)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = (int64_t)c * 128 + 64 * h;
+      acc = product<D>(stream_load((const vec*)(w + at)), *(const vec*)(x + at), acc);
+    }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sums[wave][r][4 * g + e] = acc[e];
+  __syncthreads();
+  // 4 columns a thread
+  const int t = threadIdx.x >> 2, q = 4 * (threadIdx.x & 3);
+  if (t < T && n0 + q < p.N && t < 16) {
+    fx4 s = *(const fx4*)&sums[0][t][q];
+#pragma unroll
+    for (int i = 1; i < kSkinnyWaves; ++i) s += *(const fx4*)&sums[i][t][q];
+    float v[4] = {s[0], s[1], s[2], s[3]};
+    finish<D, 4>(p.out, t, (int)(n0 + q), v);
+  }
+}
+
+// ---------------------------------------------------------------- dz
+// dy act'(z) of 8 consecutive elements.
+template <class D>
+__device__ __forceinline__ fx8 dz8(const LinearGradParams& p, size_t at) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
+  fx8 d = p.dy32 ? load8((const float*)p.dy + at) : widen<D>(*(const vec*)((const elem*)p.dy + at));
+  if (p.act != MPB_ACT_NONE) {
+    const fx8 z = widen<D>(*(const vec*)((const elem*)p.z + at));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] *= act_grad(z[i], p.act);
+  }
+  return d;
+}
+
+// The largest finite |dz| of each workgroup's share.
+template <class D>
+__global__ __launch_bounds__(256) void k_dz_max(LinearGradParams p) {
+  __shared__ float red[4];
+  const int64_t n8 = (int64_t)p.T * p.N / 8;
+  float m = 0.0f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+    const fx8 d = dz8<D>(p, 8 * i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(d[j]);
+      if (a < INFINITY) m = fmaxf(m, a);
+    }
+  }
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) p.maxima[blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+// dz as one or two parts, and the sums over a group of rows for dbias. A thread
+// has 8 columns, a workgroup 512 of them and 4 waves of rows.
+template <class D>
+__global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
+  __shared__ float red[4][512];
+  __shared__ float s_max[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 512 + 8 * lane;
+  float scale = 1.0f;
+  if (p.maxima) {
+    float m = 0.0f;
+    for (int i = threadIdx.x; i < kDzMaxima; i += 256) m = fmaxf(m, p.maxima[i]);
+    m = wave_max(m);
+    if (lane == 0) s_max[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    // m = f 2^e with f in [1/2, 1): m scale below 2^14
+    int e = 0;
+    if (m > 0.0f) {
+      (void)frexpf(m, &e);
+      e = min(max(14 - e, -126), 126);
+    }
+    scale = ldexpf(1.0f, e);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.inv_scale = ldexpf(1.0f, -e);
+  }
+  fx8 sum = (fx8)(0.0f);
+  if (n < p.N) {
+    const int t0 = blockIdx.y * p.rows, t1 = min(p.T, t0 + p.rows);
+    for (int t = t0 + wave; t < t1; t += 4) {
+      const size_t at = (size_t)t * p.N + n;
+      const fx8 d = dz8<D>(p, at);
+      sum += d;
+      if (p.hi) {
+        const fx8 x = d * scale;
+        const vec h = narrow<D>(x);
+        *(vec*)((elem*)p.hi + at) = h;
+        if (p.lo) *(vec*)((elem*)p.lo + at) = narrow<D>(x - widen<D>(h));
+      }
+    }
+  }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[wave][8 * lane + i] = sum[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 512; c += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + c;
+    if (col < p.N) p.db_part[(size_t)blockIdx.y * p.N + col] = red[0][c] + red[1][c] + red[2][c] + red[3][c];
+  }
+}
+
+// dbias: the groups' sums in their order.
+__global__ __launch_bounds__(256) void k_dbias(const float* part, int groups, int N, float* db) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (n < N) {
+#pragma unroll 8
+    for (int i = wave; i < groups; i += 4) s += part[(size_t)i * N + n];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && n < N) db[n] = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+}
+
+// ---------------------------------------------------------------- launches
+template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT>
+hipError_t launch_tiles(LinearProduct& p, hipStream_t s) {
+  static unsigned long long raised = 0;
+  constexpr int lds = 2 * 128 * (BM + BN);
+  const hipError_t e = raise_lds_limit((const void*)&k_product<D, BM, BN, WM, WN, AT, BT>, lds, raised);
+  if (e != hipSuccess) return e;
+  k_product<D, BM, BN, WM, WN, AT, BT><<<p.tm * p.tn * p.splits, 64 * (BM / WM) * (BN / WN), lds, s>>>(p);
+  return hipGetLastError();
+}
+
+template <class D, bool AT, bool BT>
+hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partial, hipStream_t s) {
+  p.tm = plan.tm;
+  p.tn = plan.tn;
+  p.per = plan.per;
+  p.splits = plan.splits;
+  p.steps = plan.steps;
+  p.parts = plan.parts;
+  p.partial = plan.splits > 1 ? partial : nullptr;
+  const hipError_t e = plan.wide ? launch_tiles<D, 256, 256, 128, 64, AT, BT>(p, s) : launch_tiles<D, 128, 128, 64, 64, AT, BT>(p, s);
+  if (e != hipSuccess || plan.splits == 1) return e;
+  const int64_t n = p.M * (p.N / 8);
+  k_join<D><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.splits);
+  return hipGetLastError();
+}
+
+template <class D>
+hipError_t forward(const LinearProduct& p, float* ws, hipStream_t s) {
+  if (linear_skinny(p.M)) {
+    k_skinny<D><<<(unsigned)((p.N + 15) / 16), 64 * kSkinnyWaves, 0, s>>>(p);
+    return hipGetLastError();
+  }
+  return launch_product<D, false, false>(p, linear_plan(p.M, p.N, p.K, 1), ws, s);
+}
+
+template <class D>
+hipError_t gradients(LinearGradParams p, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  const bool formed = p.hi != nullptr;
+  if (p.T > 0 && (formed || p.dbias)) {
+    if (p.maxima) {
+      k_dz_max<D><<<kDzMaxima, 256, 0, s>>>(p);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const int groups = (p.T + p.rows - 1) / p.rows;
+    k_dz<D><<<dim3((p.N + 511) / 512, groups), 256, 0, s>>>(p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (p.dbias) {
+    k_dbias<<<(p.N + 63) / 64, 256, 0, s>>>(p.db_part, p.T > 0 ? (p.T + p.rows - 1) / p.rows : 0, p.N, p.dbias);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const void* dz = formed ? p.hi : p.dy;
+  const float* scale = p.maxima && p.T > 0 ? p.inv_scale : nullptr;  // written by k_dz
+  if (p.dX && p.T > 0) {
+    LinearProduct g{};
+    g.A = g.A2 = dz; g.B = p.W; g.lda = p.N; g.ldb = p.Kd;
+    g.M = p.T; g.N = p.Kd; g.K = p.N;
+    g.out = LinearOut{nullptr, nullptr, nullptr, p.dX, scale, MPB_ACT_NONE, 0, p.Kd};
+    if ((e = launch_product<D, false, true>(g, linear_plan(g.M, g.N, g.K, 1), p.partial, s)) != hipSuccess) return e;
+  }
+  if (p.dW) {
+    LinearProduct g{};
+    g.A = dz; g.A2 = formed ? p.lo : dz; g.B = p.X; g.lda = p.N; g.ldb = p.Kd;
+    g.M = p.N; g.N = p.Kd; g.K = p.T;
+    g.out = LinearOut{nullptr, nullptr, nullptr, p.dW, scale, MPB_ACT_NONE, 1, p.Kd};
+    if ((e = launch_product<D, true, true>(g, linear_plan(g.M, g.N, g.K, formed ? 2 : 1), p.partial, s)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+// Wide tiles (256 x 256, one workgroup a CU) where they fill the 256 CUs at least
+// three quarters; else 128 x 128, two workgroups a CU, the reduction split until there are about 512, in
+// pieces of at least 4 steps.
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
+  LinearPlan q{};
+  q.steps = (int)((K + 63) / 64);
+  q.parts = parts;
+  const int64_t total = (int64_t)q.steps * parts;
+  const int64_t wide = ((M + 255) / 256) * ((N + 255) / 256);
+  q.wide = wide >= 192;
+  const int64_t b = q.wide ? 256 : 128;
+  q.tm = (int)((M + b - 1) / b);
+  q.tn = (int)((N + b - 1) / b);
+  int64_t splits = 1;
+  if (!q.wide) {
+    splits = 512 / ((int64_t)q.tm * q.tn);
+    if (splits > total / 4) splits = total / 4;
+    if (splits > 16) splits = 16;
+    if (splits < 1) splits = 1;
+  }
+  q.per = (int)((total + splits - 1) / splits);
+  if (q.per < 1) q.per = 1;
+  q.splits = (int)((total + q.per - 1) / q.per);
+  if (q.splits < 1) q.splits = 1;
+  return q;
+}
+
+hipError_t launch_linear(const LinearProduct& p, bool bf16, float* ws, hipStream_t s) {
+  return bf16 ? forward<BF16>(p, ws, s) : forward<F16>(p, ws, s);
+}
+
+hipError_t launch_linear_grad(const LinearGradParams& p, bool bf16, hipStream_t s) {
+  return bf16 ? gradients<BF16>(p, s) : gradients<F16>(p, s);
+}
+
+}  // namespace mpb

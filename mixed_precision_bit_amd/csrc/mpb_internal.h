@@ -316,6 +316,107 @@ struct AdapterWs {
 AdapterWs adapter_ws(int T, int Kd, int n, int R);
 hipError_t launch_adapters(const AdapterParams& p, const AdapterWs& w, bool bf16, hipStream_t s);
 
+// Norms of query and key heads with their rotation (k_head_norm.hip).
+struct HeadNormParams {
+  const void* q;         // [T][Hq][D], q_ld elements from token to token
+  const void* k;         // [T][Hk][D], k_ld
+  const float* g_q;      // [D] or null (no norm)
+  const float* g_k;      // [D] or null
+  const int32_t* pos;    // [A][T] (with Dr > 0)
+  const int32_t* axis;   // [Dr / 2] or null (0)
+  const float* freq;     // [Dr / 2]
+  void* q_out;           // qo_ld (backward: unused, qo_ld and ko_ld are those of the outputs' gradients)
+  void* k_out;           // ko_ld
+  int64_t q_ld, k_ld, qo_ld, ko_ld;
+  float eps;
+  int T, Hq, Hk, D, Dr, A, pairs;
+  int parts;             // waves of a token (set by the launch)
+};
+struct HeadNormGradParams {
+  HeadNormParams f;
+  const void* dq_out;    // f.qo_ld
+  const void* dk_out;    // f.ko_ld
+  void* dq;              // dq_ld
+  void* dk;              // dk_ld
+  int64_t dq_ld, dk_ld;
+  float* dg_q;           // [D] or null
+  float* dg_k;           // [D] or null
+  float* part;           // [2][head_norm_grad_groups][D]
+};
+hipError_t launch_head_norm(HeadNormParams p, bool bf16, hipStream_t s);
+int head_norm_grad_groups(int T, int Hq, int Hk, int D);
+hipError_t launch_head_norm_grad(HeadNormGradParams p, bool bf16, hipStream_t s);
+
+// Distillation of a teacher's top logits (k_distill.hip).
+constexpr int kDistillMaxK = 256;  // the entries of a row have a thread each
+struct DistillParams {
+  const void* S;           // [T][V], ld
+  const int32_t* ids;      // [T][k]
+  const float* teacher;    // [T][k]
+  const float* t_lse;      // [T] or null
+  const float* weight;     // [T] or null (1 / T)
+  const float* gloss;      // scalar or null (1)
+  float* stats;            // [T][4] max and sum of exp without the entries, and of all
+  float* kl;               // [T]
+  float* loss;             // [1]
+  void* dS;                // [T][V], ld, or null
+  int64_t ld;
+  float tau;
+  int T, V, k;
+  int words;               // of the bitmap (set by the launch)
+};
+hipError_t launch_distill(DistillParams p, int dtype, bool loss, hipStream_t s);
+
+// Matrix products with bias, activation and residual (k_linear.hip).
+struct LinearOut {
+  const float* bias;       // [N] or null
+  const void* res;         // [M][N] of y's type, or null
+  void* z;                 // [M][N] activations, or null
+  void* y;                 // [M][N] activations or fp32
+  const float* scale;      // device scalar that multiplies the product, or null
+  int act, y32;
+  int64_t N;
+};
+// C[m][n] = sum_k A(m, k) B(n, k). Rows of lda / ldb elements.
+struct LinearProduct {
+  const void* A;
+  const void* A2;          // A's second part (with parts 2)
+  const void* B;
+  int64_t lda, ldb, M, N, K;
+  LinearOut out;
+  int steps, per;          // steps of 64 of the reduction; steps of a workgroup
+  float* partial;          // [splits][M][N] or null (not split)
+  int parts, tm, tn, splits;
+};
+struct LinearPlan {
+  int steps, per, parts, tm, tn, splits;
+  bool wide;
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts);
+inline bool linear_skinny(int64_t M) { return M <= 16; }
+hipError_t launch_linear(const LinearProduct& p, bool bf16, float* ws, hipStream_t s);
+
+constexpr int kDzMaxima = 1024;  // workgroups of the search for the largest |dz|
+struct LinearGradParams {
+  const void* X;           // [T][Kd]
+  const void* W;           // [N][Kd]
+  const void* z;           // [T][N] (with an activation)
+  const void* dy;          // [T][N] activations or fp32
+  void* dX;                // [T][Kd] or null
+  float* dW;               // [N][Kd] or null
+  float* dbias;            // [N] or null
+  // workspace
+  void* hi;                // [T][N] dz, or null (dz is dy)
+  void* lo;                // [T][N] what hi's rounding left, or null
+  float* maxima;           // [kDzMaxima], or null (not scaled)
+  float* inv_scale;
+  float* db_part;          // [groups][N]
+  float* partial;
+  int T, Kd, N, act, dy32;
+  int rows;                // tokens of a group of k_dz
+};
+hipError_t launch_linear_grad(const LinearGradParams& p, bool bf16, hipStream_t s);
+
 // Records msg as the calling thread's last error and returns code.
 int set_error(int code, const char* msg);
 // Checks a layer geometry against the ranges the library supports; on failure
