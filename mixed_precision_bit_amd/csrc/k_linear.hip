@@ -185,7 +185,10 @@ struct Operand {
   int k[NI];                             // reduction index of the lane's bytes within the step
 
   static __device__ __forceinline__ int swz_row(int r) { return (r & 3) | ((r >> SH & 1) << 2); }
-  static __device__ __forceinline__ int swz_k(int kk) { return ((kk & 3) | ((kk >> 3 & 1) << 2)) & (R / 16 - 1); }
+  // (rows of 384 bytes shift by half the banks already: two bits are left to change)
+  static __device__ __forceinline__ int swz_k(int kk) {
+    return R % 128 == 0 ? (kk & 3) | ((kk >> 3 & 1) << 2) : (kk & 3) ^ (kk >> 3 & 1);
+  }
 
   // rows: the operand's rows in all (rows past them repeat the last: their results are not stored)
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
@@ -565,7 +568,9 @@ hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partia
   p.steps = plan.steps;
   p.parts = plan.parts;
   p.partial = plan.splits > 1 ? partial : nullptr;
-  const hipError_t e = plan.wide ? launch_tiles<D, 256, 256, 128, 64, AT, BT>(p, s) : launch_tiles<D, 128, 128, 64, 64, AT, BT>(p, s);
+  const hipError_t e = plan.rows == 256   ? launch_tiles<D, 256, 256, 128, 64, AT, BT>(p, s)
+                       : plan.rows == 192 ? launch_tiles<D, 192, 256, 96, 64, AT, BT>(p, s)
+                                          : launch_tiles<D, 128, 128, 64, 64, AT, BT>(p, s);
   if (e != hipSuccess || plan.splits == 1) return e;
   const int64_t n = p.M * (p.N / 8);
   k_join<D><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.splits);
@@ -619,26 +624,29 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
 
 }  // namespace
 
-// Wide tiles (256 x 256, one workgroup a CU) where they fill the 256 CUs at least
-// three quarters; else 128 x 128, two workgroups a CU, the reduction split until there are about 512, in
-// pieces of at least 4 steps.
+// Tiles of 256 x 256 or 192 x 256, one workgroup a CU, or of 128 x 128, two a CU,
+// whichever needs the least time by its rounds over the 256 CUs; small tiles feed the
+// matrix cores from LDS at some three quarters of the rate. With fewer than 512 small tiles the
+// reduction is split until there are about as many, in pieces of at least 4 steps.
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
   LinearPlan q{};
   q.steps = (int)((K + 63) / 64);
   q.parts = parts;
   const int64_t total = (int64_t)q.steps * parts;
-  const int64_t wide = ((M + 255) / 256) * ((N + 255) / 256);
-  q.wide = wide >= 192;
-  const int64_t b = q.wide ? 256 : 128;
-  q.tm = (int)((M + b - 1) / b);
-  q.tn = (int)((N + b - 1) / b);
-  int64_t splits = 1;
-  if (!q.wide) {
-    splits = 512 / ((int64_t)q.tm * q.tn);
-    if (splits > total / 4) splits = total / 4;
-    if (splits > 16) splits = 16;
-    if (splits < 1) splits = 1;
-  }
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  auto rounds = [](int64_t n, int64_t a) { return (n + a - 1) / a; };
+  const int64_t c256 = rounds(tiles(256, 256), 256) * 256 * 256, c192 = rounds(tiles(192, 256), 256) * 192 * 256;
+  int64_t splits = 512 / tiles(128, 128);
+  if (splits > total / 4) splits = total / 4;
+  if (splits > 16) splits = 16;
+  if (splits < 1) splits = 1;
+  const int64_t c128 = rounds(tiles(128, 128) * splits, 512) * 2 * 128 * 128 * 4 / 3 / splits;
+  const int64_t wide = c256 <= c192 ? c256 : c192;
+  q.rows = wide > c128 ? 128 : c256 <= c192 ? 256 : 192;
+  const int64_t bn = q.rows == 128 ? 128 : 256;
+  q.tm = (int)((M + q.rows - 1) / q.rows);
+  q.tn = (int)((N + bn - 1) / bn);
+  if (q.rows != 128) splits = 1;
   q.per = (int)((total + splits - 1) / splits);
   if (q.per < 1) q.per = 1;
   q.splits = (int)((total + q.per - 1) / q.per);

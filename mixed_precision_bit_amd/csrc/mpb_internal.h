@@ -390,7 +390,7 @@ struct LinearProduct {
 };
 struct LinearPlan {
   int steps, per, parts, tm, tn, splits;
-  bool wide;
+  int rows;                // of a tile of A: 256 or 192 (and 256 columns), 128 (and 128)
 };
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts);
 inline bool linear_skinny(int64_t M) { return M <= 16; }
