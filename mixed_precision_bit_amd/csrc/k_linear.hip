@@ -182,7 +182,6 @@ struct Operand {
   const char* base;                      // the tile's first row (rows) or column (turned), at the first step
   int64_t stride;                        // bytes of a source row
   uint32_t off[NI];                      // the lane's bytes within a step's source
-  int k[NI];                             // reduction index of the lane's bytes within the step
 
   static __device__ __forceinline__ int swz_row(int r) { return (r & 3) | ((r >> SH & 1) << 2); }
   // (rows of 384 bytes shift by half the banks already: two bits are left to change)
@@ -202,11 +201,9 @@ struct Operand {
         const int kk = o / (2 * R), s = (o % (2 * R) / 32) ^ swz_k(kk);
         const int col = 16 * s + 8 * (o >> 4 & 1);
         off[i] = (uint32_t)(kk * stride + 2 * min(col, left - 8));
-        k[i] = kk;
       } else {
         const int r = o >> 7, c = (o >> 4 & 7) ^ swz_row(r);
         off[i] = (uint32_t)(min(r, left - 1) * stride + 16 * c);
-        k[i] = 8 * c;
       }
     }
   }
@@ -220,26 +217,26 @@ struct Operand {
   }
   // The last step of a reduction that ends inside it: zeros from index `left` on.
   __device__ __forceinline__ void load_tail(const char* src, uint32_t lds, int wave, int lane, int left) const {
-    ux4 v[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      v[i] = (ux4)(0u);
-      if (k[i] < left) v[i] = *(const ux4*)(src + off[i]);
+      const int o = ((i * NW + wave) << 10) + 16 * lane;
+      const int k = TURNED ? o / (2 * R) : 8 * ((o >> 4 & 7) ^ swz_row(o >> 7));  // of the lane's bytes
+      ux4 v = (ux4)(0u);
+      if (k < left) v = *(const ux4*)(src + off[i]);
+      *(__attribute__((address_space(3))) ux4*)(uintptr_t)(lds + o) = v;
+      __builtin_amdgcn_sched_barrier(0);  // one at a time: the registers are taken
     }
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      *(__attribute__((address_space(3))) ux4*)(uintptr_t)(lds + ((i * NW + wave) << 10) + 16 * lane) = v[i];
   }
 };
 
 // A fragment: lane l holds row (first + its row among 16) at reduction indices 8 (l / 16) ... + 7.
-__device__ __forceinline__ ux4 read_rows(uint32_t a) { return *(const __attribute__((address_space(3))) ux4*)(uintptr_t)a; }
+__device__ __forceinline__ ux4 read_rows(const lds_char* a) { return *(const __attribute__((address_space(3))) ux4*)a; }
 // Turned: each read gives the lane its row at 4 indices; its 16 lanes address 4
 // rows of 16 elements, 8 bytes each.
-__device__ __forceinline__ ux4 read_turned(uint32_t a, uint32_t step4) {
+__device__ __forceinline__ ux4 read_turned(lds_char* a, int step4) {
   typedef __attribute__((address_space(3))) sx4 lds_sx4;
-  const sx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_sx4*)(uintptr_t)a);
-  const sx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_sx4*)(uintptr_t)(a + step4));
+  const sx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_sx4*)a);
+  const sx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_sx4*)(a + step4));
   sx8 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
@@ -320,28 +317,66 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = (acc4)(0.0f);
 
-  if (s0 < s1) stage(s0, lds0);
-  for (int s = s0; s < s1; ++s) {
-    const uint32_t buf = lds0 + ((s - s0) & 1) * kBuf;
-    // this step's operands have arrived, and every wave is done with the other buffer
+  // A step has two halves of 32. The fragments of B have two sets of registers, those
+  // of A one: a row of fragments is multiplied and then read again for the next half,
+  // so every read has most of a half (and the other waves' products) to arrive in.
+  ux4 a[MF], b0[NF], b1[NF];
+  auto at = [&](uint32_t buf, uint32_t o) { return (lds_char*)(uintptr_t)(buf + o); };
+  auto read_a = [&](uint32_t buf, int ks, int i) {
+    a[i] = AT ? read_turned(at(buf, fa[AT ? i : 0]) + 64 * BM * ks, 8 * BM) : read_rows(at(buf, fa[0] ^ (64 * ks)) + 2048 * i);
+  };
+  auto read_b = [&](ux4 (&f)[NF], uint32_t buf, int ks) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+      f[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]) + 64 * BN * ks, 8 * BN) : read_rows(at(buf, fb[0] ^ (64 * ks)) + 512 * j);
+  };
+  auto multiply = [&](const ux4 (&f)[NF], int i) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = product<D>(__builtin_bit_cast(vec, f[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);  // in this order
+  };
+  if (s0 < s1) {
+    stage(s0, lds0);
     loads_done();
     __syncthreads();
-    if (s + 1 < s1) stage(s + 1, lds0 + (~(s - s0) & 1) * kBuf);
+    if (s0 + 1 < s1) stage(s0 + 1, lds0 + kBuf);
+    uint32_t buf = lds0, other = lds0 + kBuf;
+    read_b(b0, buf, 0);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      ux4 b[NF], a[MF];
+    for (int i = 0; i < MF; ++i) read_a(buf, 0, i);
+    for (int s = s0; s + 1 < s1; ++s) {
+      read_b(b1, buf, 1);
 #pragma unroll
-      for (int j = 0; j < NF; ++j)
-        b[j] = BT ? read_turned(buf + fb[BT ? j : 0] + 64 * BN * ks, 8 * BN) : read_rows(buf + (fb[0] ^ (64 * ks)) + 512 * j);
+      for (int i = 0; i < MF; ++i) {
+        multiply(b0, i);
+        read_a(buf, 1, i);
+      }
+      multiply(b1, 0);
+      multiply(b1, 1);
+      // the next step's operands have arrived, and every wave has read this step's
+      loads_done();
+      __syncthreads();
+      if (s + 2 < s1) stage(s + 2, buf);
+      read_b(b0, other, 0);
+      read_a(other, 0, 0);
+      read_a(other, 0, 1);
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
-        a[i] = AT ? read_turned(buf + fa[AT ? i : 0] + 64 * BM * ks, 8 * BM) : read_rows(buf + (fa[0] ^ (64 * ks)) + 2048 * i);
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-          acc[i][j] = product<D>(__builtin_bit_cast(vec, b[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
+      for (int i = 2; i < MF; ++i) {
+        multiply(b1, i);
+        read_a(other, 0, i);
+      }
+      const uint32_t t = buf;
+      buf = other;
+      other = t;
     }
+    read_b(b1, buf, 1);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      multiply(b0, i);
+      read_a(buf, 1, i);
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) multiply(b1, i);
   }
 
   // lane (r, g): row r of each 16, columns 4 NF g ... (rows) or 16 j + 4 g ... (turned)
