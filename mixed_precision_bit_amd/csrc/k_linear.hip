@@ -22,6 +22,8 @@
 // fp32: 16 bits of bf16, 22 of fp16. fp16 parts are scaled by a power of two that
 // brings the largest |dz| to 2^14, so that the gradients of a mean, below fp16's
 // range, keep their bits.
+#include <type_traits>
+
 #include "k_block_common.h"
 #include "mpb.h"
 #include "mpb_internal.h"
@@ -163,70 +165,43 @@ __device__ __forceinline__ const char* wave_uniform(const char* p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return (const char*)((uint64_t)hi << 32 | lo);
 }
-// Every load of the wave has arrived.
-__device__ __forceinline__ void loads_done() {
+// All but the wave's last N loads have arrived.
+template <int N>
+__device__ __forceinline__ void loads_but() {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 #endif
 }
 
-// A tile of R rows (of A or B) by 64 of the reduction, 128 R bytes, in one of two forms:
-//  rows   row r at 128 r, its 16-byte pieces c at c ^ swz(r): the 16 rows that a
-//         fragment reads at once take turns on the banks
-//  turned reduction index k at 2 R k, its 32-byte pieces (16 rows) s at s ^ swz(k)
-// A wave writes 1 KiB at a time (lane i the i-th 16 bytes, which is all that a
-// direct load can do), so the swizzle is in the addresses that it loads from.
-template <int R, int NW, bool TURNED, int SH>
+// A stage is 32 of the reduction. R rows (of A or B) take 64 R bytes of it, in one of two forms:
+//  rows   row r at 64 r, its 16-byte pieces c at c ^ swz_row(r)
+//  turned reduction index k at 2 R k, its 32-byte pieces (16 rows) s at s ^ swz_k(k)
+// so that what a fragment reads at once takes turns on the banks. A direct load writes a wave's 1 KiB
+// (lane i the i-th 16 bytes), so the swizzle is in the addresses that it loads from.
+template <int R, bool TURNED, int SH>
 struct Operand {
-  static constexpr int NI = R / 8 / NW;  // loads of a wave and step
-  const char* base;                      // the tile's first row (rows) or column (turned), at the first step
-  int64_t stride;                        // bytes of a source row
-  uint32_t off[NI];                      // the lane's bytes within a step's source
-
-  static __device__ __forceinline__ int swz_row(int r) { return (r & 3) | ((r >> SH & 1) << 2); }
+  static __device__ __forceinline__ int swz_row(int r) { return (r >> 1 & 1) | (r >> SH & 1) << 1; }
   // (rows of 384 bytes shift by half the banks already: two bits are left to change)
   static __device__ __forceinline__ int swz_k(int kk) {
     return R % 128 == 0 ? (kk & 3) | ((kk >> 3 & 1) << 2) : (kk & 3) ^ (kk >> 3 & 1);
   }
-
-  // rows: the operand's rows in all (rows past them repeat the last: their results are not stored)
-  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
-    stride = 2 * ld;
-    const int left = (int)(rows - r0 < R ? rows - r0 : R);
-    base = (const char*)p + (TURNED ? 2 * r0 : r0 * stride);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int o = ((i * NW + wave) << 10) + 16 * lane;
-      if constexpr (TURNED) {
-        const int kk = o / (2 * R), s = (o % (2 * R) / 32) ^ swz_k(kk);
-        const int col = 16 * s + 8 * (o >> 4 & 1);
-        off[i] = (uint32_t)(kk * stride + 2 * min(col, left - 8));
-      } else {
-        const int r = o >> 7, c = (o >> 4 & 7) ^ swz_row(r);
-        off[i] = (uint32_t)(min(r, left - 1) * stride + 16 * c);
-      }
+  // Reduction index of the bytes o of a stage.
+  static __device__ __forceinline__ int k_of(int o) { return TURNED ? o / (2 * R) : 8 * ((o >> 4 & 3) ^ swz_row(o >> 6)); }
+  // Offset in the source of the bytes o of a stage. Rows past the `left` that there are
+  // repeat the last: their results are not stored.
+  static __device__ __forceinline__ uint32_t source(int o, int64_t stride, int left) {
+    if constexpr (TURNED) {
+      const int col = 16 * ((o % (2 * R) / 32) ^ swz_k(k_of(o))) + 8 * (o >> 4 & 1);
+      return (uint32_t)(k_of(o) * stride + 2 * min(col, left - 8));
+    } else {
+      return (uint32_t)(min(o >> 6, left - 1) * stride + 2 * k_of(o));
     }
   }
-  __device__ __forceinline__ const char* at(int step) const { return base + (TURNED ? step * 64 * stride : (int64_t)step * 128); }
-  // A whole step.
-  __device__ __forceinline__ void load(const char* from, uint32_t lds, int wave) const {
-    const char* src = wave_uniform(from);
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      load_lds16(src, off[i], lds + ((i * NW + wave) << 10));
+  // The tile's first byte at reduction index 0, and the bytes of a stage's advance.
+  static __device__ __forceinline__ const char* first(const void* p, int64_t r0, int64_t stride) {
+    return (const char*)p + (TURNED ? 2 * r0 : r0 * stride);
   }
-  // The last step of a reduction that ends inside it: zeros from index `left` on.
-  __device__ __forceinline__ void load_tail(const char* src, uint32_t lds, int wave, int lane, int left) const {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int o = ((i * NW + wave) << 10) + 16 * lane;
-      const int k = TURNED ? o / (2 * R) : 8 * ((o >> 4 & 7) ^ swz_row(o >> 7));  // of the lane's bytes
-      ux4 v = (ux4)(0u);
-      if (k < left) v = *(const ux4*)(src + off[i]);
-      *(__attribute__((address_space(3))) ux4*)(uintptr_t)(lds + o) = v;
-      __builtin_amdgcn_sched_barrier(0);  // one at a time: the registers are taken
-    }
-  }
+  static __device__ __forceinline__ int64_t advance(int64_t stride) { return TURNED ? 32 * stride : 64; }
 };
 
 // A fragment: lane l holds row (first + its row among 16) at reduction indices 8 (l / 16) ... + 7.
@@ -255,6 +230,7 @@ template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearProduct p) {
   typedef typename D::vec vec;
   constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, MF = WM / 16, NF = WN / 16;
+  constexpr int kStages = 5;  // buffers
   // Rows of B within a wave's fragments: fragment j's row r is column 4 NF (r / 4) +
   // 4 j + r % 4 of the wave's part, so that a lane ends up with 4 NF consecutive
   // columns of one row of C. Turned operands come in 16 consecutive columns.
@@ -268,47 +244,86 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
   const int64_t m0 = (int64_t)(8 * grp + rest % gm) * BM;
   const int64_t n0 = (int64_t)(rest / gm) * BN;
 
-  Operand<BM, NW, AT, 2> oa;
-  Operand<BN, NW, BT, SHB> ob;
-  oa.init(p.A, p.lda, m0, p.M, wave, lane);
-  ob.init(p.B, p.ldb, n0, p.N, wave, lane);
-  constexpr uint32_t kA = 128 * BM, kBuf = 128 * (BM + BN);
+  typedef Operand<BM, AT, 2> OA;
+  typedef Operand<BN, BT, SHB> OB;
+  // A stage comes as pieces of 1 KiB, A's PA and then B's; wave w loads pieces w, w + NW, ...
+  constexpr int PA = BM / 16, PB = BN / 16, NP = (PA + PB + NW - 1) / NW, SPARE = (PA + PB) % NW;
+  constexpr uint32_t kA = 64 * BM, kStage = 64 * (BM + BN);
+  const int64_t sa = 2 * p.lda, sb = 2 * p.ldb;
+  uint32_t off[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int q = i * NW + wave, o = 1024 * q + 16 * lane;
+    off[i] = q < PA        ? OA::source(o, sa, (int)min((int64_t)BM, p.M - m0))
+             : q < PA + PB ? OB::source(o - kA, sb, (int)min((int64_t)BN, p.N - n0))
+                           : 0;
+  }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)smem;
 
-  // steps of this workgroup: the reduction once, or twice with A's two parts (first A, then A2)
-  const int steps = p.steps, s0 = split * p.per, s1 = min(s0 + p.per, steps * p.parts);
-  const int64_t part2 = (const char*)p.A2 - (const char*)p.A;
-  auto stage = [&](int s, uint32_t lds) {
-    const bool second = s >= steps;
-    const int at = second ? s - steps : s;
-    const char* a = oa.at(at) + (second ? part2 : 0);
-    const char* b = ob.at(at);
-    const int left = (int)p.K - 64 * at;
-    if (left >= 64) {
-      oa.load(a, lds, wave);
-      ob.load(b, lds + kA, wave);
-    } else {
-      oa.load_tail(a, lds, wave, lane, left);
-      ob.load_tail(b, lds + kA, wave, lane, left);
+  // stages of this workgroup: the reduction once, or twice with A's two parts (first A, then A2)
+  const int stages = p.stages, s0 = split * p.per, s1 = min(s0 + p.per, stages * p.parts);
+  int next = s0 < stages ? s0 : s0 - stages, left = (int)p.K - 32 * next;  // of its part; reduction left
+  const char* pa = OA::first(s0 < stages ? p.A : p.A2, m0, sa) + next * OA::advance(sa);
+  const char* pb = OB::first(p.B, n0, sb) + next * OB::advance(sb);
+  auto of_a = [&](int i) { return (i + 1) * NW <= PA || (i * NW < PA && i * NW + wave < PA); };
+  auto issue_whole = [&](uint32_t lds) {
+    const char *a = wave_uniform(pa), *b = wave_uniform(pb);
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (!SPARE || i < NP - 1 || wave < SPARE) load_lds16(of_a(i) ? a : b, off[i], lds + 1024 * (i * NW + wave));
+    pa += OA::advance(sa);
+    pb += OB::advance(sb);
+    left -= 32;
+    ++next;
+  };
+  auto issue = [&](uint32_t lds) {
+    if (left >= 32) {
+      issue_whole(lds);
+    } else {  // the reduction ends inside the stage: zeros behind its end
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (SPARE && i == NP - 1 && wave >= SPARE) break;
+        const int o = 1024 * (i * NW + wave) + 16 * lane;
+        ux4 v = (ux4)(0u);
+        if ((of_a(i) ? OA::k_of(o) : OB::k_of(o - kA)) < left)
+          v = *(const __attribute__((address_space(1))) ux4*)(uintptr_t)((of_a(i) ? pa : pb) + off[i]);
+        *(__attribute__((address_space(3))) ux4*)(uintptr_t)(lds + o) = v;
+        __builtin_amdgcn_sched_barrier(0);  // one at a time: the registers are taken
+      }
+      ++next;
     }
+    if (next == stages) {
+      next = 0;
+      left = (int)p.K;
+      pa = OA::first(p.A2, m0, sa);
+      pb = OB::first(p.B, n0, sb);
+    }
+  };
+  // All but the last N stages that the wave issued have arrived. (One that ends the
+  // reduction has no direct loads, and its own came after every earlier one.)
+  auto arrived_but = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (SPARE == 0 || wave < SPARE)
+      loads_but<N * NP>();
+    else
+      loads_but<N * (NP - 1)>();
   };
 
   const int wm = (wave / NWN) * WM, wn = (wave % NWN) * WN, r = lane & 15, g = lane >> 4;
-  // fragment addresses within a buffer
+  // fragment addresses within a stage
   uint32_t fa[AT ? MF : 1], fb[BT ? NF : 1];
+  const int kk = 8 * g + (r >> 2);
   if constexpr (AT) {
-    const int kk = 8 * g + (r >> 2);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) fa[i] = 2 * BM * kk + 32 * ((wm / 16 + i) ^ oa.swz_k(kk)) + 8 * (r & 3);
+    for (int i = 0; i < MF; ++i) fa[i] = 2 * BM * kk + 32 * ((wm / 16 + i) ^ OA::swz_k(kk)) + 8 * (r & 3);
   } else {
-    fa[0] = 128 * (wm + r) + 16 * (g ^ (r & 7));
+    fa[0] = 64 * (wm + r) + 16 * (g ^ (r >> 1 & 3));
   }
   if constexpr (BT) {
-    const int kk = 8 * g + (r >> 2);
 #pragma unroll
-    for (int j = 0; j < NF; ++j) fb[j] = kA + 2 * BN * kk + 32 * ((wn / 16 + j) ^ ob.swz_k(kk)) + 8 * (r & 3);
+    for (int j = 0; j < NF; ++j) fb[j] = kA + 2 * BN * kk + 32 * ((wn / 16 + j) ^ OB::swz_k(kk)) + 8 * (r & 3);
   } else {
-    fb[0] = kA + 128 * (wn + 4 * NF * (r >> 2) + (r & 3)) + 16 * (g ^ (r & 7));
+    fb[0] = kA + 64 * (wn + 4 * NF * (r >> 2) + (r & 3)) + 16 * (g ^ (r >> 1 & 3));
   }
 
   acc4 acc[MF][NF];
@@ -317,66 +332,73 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = (acc4)(0.0f);
 
-  // A step has two halves of 32. The fragments of B have two sets of registers, those
-  // of A one: a row of fragments is multiplied and then read again for the next half,
-  // so every read has most of a half (and the other waves' products) to arrive in.
+  // The fragments of B have two sets of registers, those of A one: a row of fragments
+  // is multiplied and then read again for the next stage, so every read has most of a
+  // stage (and the other waves' products) to arrive in.
   ux4 a[MF], b0[NF], b1[NF];
   auto at = [&](uint32_t buf, uint32_t o) { return (lds_char*)(uintptr_t)(buf + o); };
-  auto read_a = [&](uint32_t buf, int ks, int i) {
-    a[i] = AT ? read_turned(at(buf, fa[AT ? i : 0]) + 64 * BM * ks, 8 * BM) : read_rows(at(buf, fa[0] ^ (64 * ks)) + 2048 * i);
+  auto read_a = [&](uint32_t buf, int i) {
+    a[i] = AT ? read_turned(at(buf, fa[AT ? i : 0]), 8 * BM) : read_rows(at(buf, fa[0]) + 1024 * i);
   };
-  auto read_b = [&](ux4 (&f)[NF], uint32_t buf, int ks) {
+  auto read_b = [&](ux4 (&f)[NF], uint32_t buf) {
 #pragma unroll
-    for (int j = 0; j < NF; ++j)
-      f[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]) + 64 * BN * ks, 8 * BN) : read_rows(at(buf, fb[0] ^ (64 * ks)) + 512 * j);
+    for (int j = 0; j < NF; ++j) f[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]), 8 * BN) : read_rows(at(buf, fb[0]) + 256 * j);
   };
   auto multiply = [&](const ux4 (&f)[NF], int i) {
 #pragma unroll
-    for (int j = 0; j < NF; ++j) acc[i][j] = product<D>(__builtin_bit_cast(vec, f[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
+    for (int j = 0; j < NF; ++j)
+      acc[i][j] = product<D>(__builtin_bit_cast(vec, f[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);  // in this order
   };
-  if (s0 < s1) {
-    stage(s0, lds0);
-    loads_done();
+  uint32_t buf = lds0;
+  // Stage s with B's fragments in `now`, and the reads of stage s + 1. Steady: the stage
+  // to issue is there and whole, and its part goes on behind it.
+  auto stage = [&](auto steady, int s, const ux4 (&now)[NF], ux4 (&then)[NF]) {
+    multiply(now, 0);
+    multiply(now, 1);
+    // stage s + 1 has arrived, and every wave has read stage s, whose buffer is free
+    if (steady || s + kStages - 1 < s1) arrived_but(std::integral_constant<int, kStages - 2>());
+    else loads_but<0>();
     __syncthreads();
-    if (s0 + 1 < s1) stage(s0 + 1, lds0 + kBuf);
-    uint32_t buf = lds0, other = lds0 + kBuf;
-    read_b(b0, buf, 0);
+    if (steady) issue_whole(buf);
+    else if (s + kStages < s1) issue(buf);
+    buf = buf + kStage == lds0 + kStages * kStage ? lds0 : buf + kStage;
+    read_b(then, buf);
+    read_a(buf, 0);
+    read_a(buf, 1);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) read_a(buf, 0, i);
-    for (int s = s0; s + 1 < s1; ++s) {
-      read_b(b1, buf, 1);
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        multiply(b0, i);
-        read_a(buf, 1, i);
-      }
-      multiply(b1, 0);
-      multiply(b1, 1);
-      // the next step's operands have arrived, and every wave has read this step's
-      loads_done();
-      __syncthreads();
-      if (s + 2 < s1) stage(s + 2, buf);
-      read_b(b0, other, 0);
-      read_a(other, 0, 0);
-      read_a(other, 0, 1);
-#pragma unroll
-      for (int i = 2; i < MF; ++i) {
-        multiply(b1, i);
-        read_a(other, 0, i);
-      }
-      const uint32_t t = buf;
-      buf = other;
-      other = t;
+    for (int i = 2; i < MF; ++i) {
+      multiply(now, i);
+      read_a(buf, i);
     }
-    read_b(b1, buf, 1);
+  };
+  if (s0 < s1) {
+    for (int i = 0; i < kStages && s0 + i < s1; ++i) issue(lds0 + i * kStage);
+    if (s0 + kStages <= s1) arrived_but(std::integral_constant<int, kStages - 1>());
+    else loads_but<0>();
+    __syncthreads();
+    read_b(b0, buf);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      multiply(b0, i);
-      read_a(buf, 1, i);
+    for (int i = 0; i < MF; ++i) read_a(buf, i);
+    int s = s0;
+    while (s + 2 < s1) {
+      for (; s + 1 + kStages < s1 && left >= 96; s += 2) {
+        stage(std::true_type(), s, b0, b1);
+        stage(std::true_type(), s + 1, b1, b0);
+      }
+      if (s + 2 < s1) {
+        stage(std::false_type(), s, b0, b1);
+        stage(std::false_type(), s + 1, b1, b0);
+        s += 2;
+      }
+    }
+    if (s + 1 < s1) {
+      stage(std::false_type(), s, b0, b1);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) b0[j] = b1[j];
     }
 #pragma unroll
-    for (int i = 0; i < MF; ++i) multiply(b1, i);
+    for (int i = 0; i < MF; ++i) multiply(b0, i);
   }
 
   // lane (r, g): row r of each 16, columns 4 NF g ... (rows) or 16 j + 4 g ... (turned)
@@ -587,7 +609,7 @@ __global__ __launch_bounds__(256) void k_dbias(const float* part, int groups, in
 template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT>
 hipError_t launch_tiles(LinearProduct& p, hipStream_t s) {
   static unsigned long long raised = 0;
-  constexpr int lds = 2 * 128 * (BM + BN);
+  constexpr int lds = 5 * 64 * (BM + BN);
   const hipError_t e = raise_lds_limit((const void*)&k_product<D, BM, BN, WM, WN, AT, BT>, lds, raised);
   if (e != hipSuccess) return e;
   k_product<D, BM, BN, WM, WN, AT, BT><<<p.tm * p.tn * p.splits, 64 * (BM / WM) * (BN / WN), lds, s>>>(p);
@@ -600,7 +622,7 @@ hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partia
   p.tn = plan.tn;
   p.per = plan.per;
   p.splits = plan.splits;
-  p.steps = plan.steps;
+  p.stages = plan.stages;
   p.parts = plan.parts;
   p.partial = plan.splits > 1 ? partial : nullptr;
   const hipError_t e = plan.rows == 256   ? launch_tiles<D, 256, 256, 128, 64, AT, BT>(p, s)
@@ -662,17 +684,17 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
 // Tiles of 256 x 256 or 192 x 256, one workgroup a CU, or of 128 x 128, two a CU,
 // whichever needs the least time by its rounds over the 256 CUs; small tiles feed the
 // matrix cores from LDS at some three quarters of the rate. With fewer than 512 small tiles the
-// reduction is split until there are about as many, in pieces of at least 4 steps.
+// reduction is split until there are about as many, in pieces of at least 8 stages of 32.
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
   LinearPlan q{};
-  q.steps = (int)((K + 63) / 64);
+  q.stages = (int)((K + 31) / 32);
   q.parts = parts;
-  const int64_t total = (int64_t)q.steps * parts;
+  const int64_t total = (int64_t)q.stages * parts;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   auto rounds = [](int64_t n, int64_t a) { return (n + a - 1) / a; };
   const int64_t c256 = rounds(tiles(256, 256), 256) * 256 * 256, c192 = rounds(tiles(192, 256), 256) * 192 * 256;
   int64_t splits = 512 / tiles(128, 128);
-  if (splits > total / 4) splits = total / 4;
+  if (splits > total / 8) splits = total / 8;
   if (splits > 16) splits = 16;
   if (splits < 1) splits = 1;
   const int64_t c128 = rounds(tiles(128, 128) * splits, 512) * 2 * 128 * 128 * 4 / 3 / splits;

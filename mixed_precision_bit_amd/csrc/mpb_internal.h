@@ -384,12 +384,12 @@ struct LinearProduct {
   const void* B;
   int64_t lda, ldb, M, N, K;
   LinearOut out;
-  int steps, per;          // steps of 64 of the reduction; steps of a workgroup
+  int stages, per;         // stages of 32 of the reduction; those of a workgroup
   float* partial;          // [splits][M][N] or null (not split)
   int parts, tm, tn, splits;
 };
 struct LinearPlan {
-  int steps, per, parts, tm, tn, splits;
+  int stages, per, parts, tm, tn, splits;
   int rows;                // of a tile of A: 256 or 192 (and 256 columns), 128 (and 128)
 };
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts);
