@@ -332,73 +332,47 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = (acc4)(0.0f);
 
-  // The fragments of B have two sets of registers, those of A one: a row of fragments
-  // is multiplied and then read again for the next stage, so every read has most of a
-  // stage (and the other waves' products) to arrive in.
-  ux4 a[MF], b0[NF], b1[NF];
+  // A stage has two phases: its fragments are read (and a later stage is issued), then
+  // multiplied. With 8 waves, two a SIMD, waves 4 to 7 run one phase behind waves 0 to 3: the
+  // matrix cores work for one half while the other reads.
+  constexpr bool kTwoHalves = NW == 8;
+  constexpr int kAhead = kStages - 1;  // stages in flight
+  ux4 a[MF], b[NF];
   auto at = [&](uint32_t buf, uint32_t o) { return (lds_char*)(uintptr_t)(buf + o); };
-  auto read_a = [&](uint32_t buf, int i) {
-    a[i] = AT ? read_turned(at(buf, fa[AT ? i : 0]), 8 * BM) : read_rows(at(buf, fa[0]) + 1024 * i);
-  };
-  auto read_b = [&](ux4 (&f)[NF], uint32_t buf) {
+  uint32_t buf = lds0, free = lds0 + kAhead * kStage;  // of stage s, of stage s - 1
+  auto stage = [&](auto steady, int s) {
 #pragma unroll
-    for (int j = 0; j < NF; ++j) f[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]), 8 * BN) : read_rows(at(buf, fb[0]) + 256 * j);
-  };
-  auto multiply = [&](const ux4 (&f)[NF], int i) {
+    for (int j = 0; j < NF; ++j) b[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]), 8 * BN) : read_rows(at(buf, fb[0]) + 256 * j);
 #pragma unroll
-    for (int j = 0; j < NF; ++j)
-      acc[i][j] = product<D>(__builtin_bit_cast(vec, f[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);  // in this order
-  };
-  uint32_t buf = lds0;
-  // Stage s with B's fragments in `now`, and the reads of stage s + 1. Steady: the stage
-  // to issue is there and whole, and its part goes on behind it.
-  auto stage = [&](auto steady, int s, const ux4 (&now)[NF], ux4 (&then)[NF]) {
-    multiply(now, 0);
-    multiply(now, 1);
-    // stage s + 1 has arrived, and every wave has read stage s, whose buffer is free
-    if (steady || s + kStages - 1 < s1) arrived_but(std::integral_constant<int, kStages - 2>());
+    for (int i = 0; i < MF; ++i) a[i] = AT ? read_turned(at(buf, fa[AT ? i : 0]), 8 * BM) : read_rows(at(buf, fa[0]) + 1024 * i);
+    if (steady) issue_whole(free);
+    else if (s + kAhead < s1) issue(free);
+    // stage s + 1 has arrived
+    if (steady || s + kAhead < s1) arrived_but(std::integral_constant<int, kAhead - 1>());
     else loads_but<0>();
-    __syncthreads();
-    if (steady) issue_whole(buf);
-    else if (s + kStages < s1) issue(buf);
-    buf = buf + kStage == lds0 + kStages * kStage ? lds0 : buf + kStage;
-    read_b(then, buf);
-    read_a(buf, 0);
-    read_a(buf, 1);
+    __syncthreads();  // ... for every wave, and every wave of this half has read stage s
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int i = 2; i < MF; ++i) {
-      multiply(now, i);
-      read_a(buf, i);
-    }
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        acc[i][j] = product<D>(__builtin_bit_cast(vec, b[j]), __builtin_bit_cast(vec, a[i]), acc[i][j]);
+    __builtin_amdgcn_s_setprio(0);
+    if (kTwoHalves) __syncthreads();
+    free = buf;
+    buf = buf + kStage == lds0 + kStages * kStage ? lds0 : buf + kStage;
   };
   if (s0 < s1) {
-    for (int i = 0; i < kStages && s0 + i < s1; ++i) issue(lds0 + i * kStage);
-    if (s0 + kStages <= s1) arrived_but(std::integral_constant<int, kStages - 1>());
+    for (int i = 0; i < kAhead && s0 + i < s1; ++i) issue(lds0 + i * kStage);
+    if (s0 + kAhead <= s1) arrived_but(std::integral_constant<int, kAhead - 1>());
     else loads_but<0>();
     __syncthreads();
-    read_b(b0, buf);
-#pragma unroll
-    for (int i = 0; i < MF; ++i) read_a(buf, i);
-    int s = s0;
-    while (s + 2 < s1) {
-      for (; s + 1 + kStages < s1 && left >= 96; s += 2) {
-        stage(std::true_type(), s, b0, b1);
-        stage(std::true_type(), s + 1, b1, b0);
-      }
-      if (s + 2 < s1) {
-        stage(std::false_type(), s, b0, b1);
-        stage(std::false_type(), s + 1, b1, b0);
-        s += 2;
-      }
+    if (kTwoHalves && wave >= NW / 2) __syncthreads();
+    for (int s = s0; s < s1;) {
+      for (; s + kAhead < s1 && left >= 64; ++s) stage(std::true_type(), s);
+      if (s < s1) stage(std::false_type(), s++);
     }
-    if (s + 1 < s1) {
-      stage(std::false_type(), s, b0, b1);
-#pragma unroll
-      for (int j = 0; j < NF; ++j) b0[j] = b1[j];
-    }
-#pragma unroll
-    for (int i = 0; i < MF; ++i) multiply(b0, i);
+    if (kTwoHalves && wave < NW / 2) __syncthreads();
   }
 
   // lane (r, g): row r of each 16, columns 4 NF g ... (rows) or 16 j + 4 g ... (turned)
