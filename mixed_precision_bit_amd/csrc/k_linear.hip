@@ -32,23 +32,10 @@ namespace mpb {
 
 namespace {
 
-typedef _Float16 hx4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bx4 __attribute__((ext_vector_type(4)));
 typedef short sx4 __attribute__((ext_vector_type(4)));
 typedef short sx8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) void lds_void;
-
-template <class D>
-struct Half;
-template <>
-struct Half<F16> {
-  typedef hx4 vec4;
-};
-template <>
-struct Half<BF16> {
-  typedef bx4 vec4;
-};
 
 template <class D>
 __device__ __forceinline__ acc4 product(typename D::vec a, typename D::vec b, acc4 c);
@@ -65,14 +52,22 @@ __device__ __forceinline__ acc4 product<BF16>(bx8 a, bx8 b, acc4 c) {
 constexpr float kSqrtHalf = 0.707106781f, kInvSqrt2Pi = 0.398942280f;
 constexpr float kTanhA = 0.797884561f, kTanhB = 0.044715f;  // sqrt(2 / pi)
 
+// For results of 16 bits: within |x| 2^-24 of itself, 2^-9 being asked, in half the
+// operations (4093 x 5632 x 2816 with gelu_tanh: TODO).
+__device__ __forceinline__ float sigmoid16(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269502f * x));
+}
+
 // gelu_tanh is z sigmoid(2 u), u = a (z + b z^3): 1 + tanh(u) = 2 sigmoid(2 u),
 // which keeps its relative accuracy where tanh is close to -1.
+template <bool NARROW>
 __device__ __forceinline__ float act_of(float z, int act) {
+  auto sig = [](float x) { return NARROW ? sigmoid16(x) : sigmoid(x); };
   switch (act) {
     case MPB_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case MPB_ACT_SILU: return z * sigmoid(z);
+    case MPB_ACT_SILU: return z * sig(z);
     case MPB_ACT_GELU: return 0.5f * z * erfcf(-z * kSqrtHalf);
-    case MPB_ACT_GELU_TANH: return z * sigmoid(2.0f * kTanhA * (z + kTanhB * z * z * z));
+    case MPB_ACT_GELU_TANH: return z * sig(2.0f * kTanhA * (z + kTanhB * z * z * z));
     default: return z;
   }
 }
@@ -98,53 +93,53 @@ __device__ __forceinline__ float act_grad(float z, int act) {
 }
 
 // ---------------------------------------------------------------- epilogue
-// NV (4 or 8) consecutive results of row m from column n on.
-template <class D, int NV>
-__device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, float (&v)[NV]) {
+// What becomes of a product: a gradient in the activations' type or fp32 (times a
+// scale), or moe_linear's epilogue with y in either.
+enum { kGrad16, kGrad32, kOut16, kOut32 };
+
+// NV (4 or 8) consecutive columns of a row, as they are loaded from the residual: the
+// load of one group goes out before the group in front of it is stored.
+template <class D, int NV, int KIND>
+struct Residual {
   typedef typename D::elem elem;
   typedef elem evec __attribute__((ext_vector_type(NV)));
   typedef float fvec __attribute__((ext_vector_type(NV)));
-  typedef float fx4a __attribute__((ext_vector_type(4)));
+  evec narrow_;
+  fvec wide_;
+  __device__ __forceinline__ void load(const LinearOut& o, int64_t m, int n) {
+    const size_t at = (size_t)m * o.N + n;
+    if constexpr (KIND == kOut16) {
+      if (o.res) narrow_ = *(const evec*)((const elem*)o.res + at);
+    } else if constexpr (KIND == kOut32) {
+      if (o.res) wide_ = *(const fvec*)((const float*)o.res + at);
+    }
+  }
+};
+
+// NV results of row m from column n on.
+template <class D, int NV, int KIND>
+__device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, float (&v)[NV], const Residual<D, NV, KIND>& res) {
+  typedef typename Residual<D, NV, KIND>::elem elem;
+  typedef typename Residual<D, NV, KIND>::evec evec;
+  typedef typename Residual<D, NV, KIND>::fvec fvec;
   const size_t at = (size_t)m * o.N + n;
-  if (o.scale) {
-    const float k = *o.scale;
+  fvec w;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] *= k;
-  }
-  if (o.bias) {
-#pragma unroll
-    for (int i = 0; i < NV; i += 4) {
-      const fx4a b = *(const fx4a*)(o.bias + n + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i + j] += b[j];
-    }
-  }
-  if (o.z) {
-    fvec z;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) z[i] = v[i];
-    *(evec*)((elem*)o.z + at) = __builtin_convertvector(z, evec);
-  }
-  if (o.act != MPB_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = act_of(v[i], o.act);
-  }
-  if (o.y32) {
-    float* y = (float*)o.y + at;
-    const float* res = (const float*)o.res + at;
-#pragma unroll
-    for (int i = 0; i < NV; i += 4) {
-      fx4a w = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-      if (o.res) w += *(const fx4a*)(res + i);
-      *(fx4a*)(y + i) = w;
-    }
+  for (int i = 0; i < NV; ++i) w[i] = v[i];
+  constexpr bool kNarrow = KIND == kGrad16 || KIND == kOut16;
+  if constexpr (KIND == kGrad16 || KIND == kGrad32) {
+    if (o.scale) w *= *o.scale;
   } else {
-    fvec w;
+    if (o.bias) w += *(const fvec*)(o.bias + n);
+    if (o.z) *(evec*)((elem*)o.z + at) = __builtin_convertvector(w, evec);
+    if (o.act != MPB_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) w[i] = v[i];
-    if (o.res) w += __builtin_convertvector(*(const evec*)((const elem*)o.res + at), fvec);
-    *(evec*)((elem*)o.y + at) = __builtin_convertvector(w, evec);
+      for (int i = 0; i < NV; ++i) w[i] = act_of<kNarrow>(w[i], o.act);
+    }
+    if (o.res) w += kNarrow ? __builtin_convertvector(res.narrow_, fvec) : res.wide_;
   }
+  if constexpr (kNarrow) *(evec*)((elem*)o.y + at) = __builtin_convertvector(w, evec);
+  else *(fvec*)((float*)o.y + at) = w;
 }
 
 // ---------------------------------------------------------------- operands in LDS
@@ -226,7 +221,7 @@ __device__ __forceinline__ int unit(int b, int n) {
   return x * q + min(x, r) + (b >> 3);
 }
 
-template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT>
+template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT, int KIND>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearProduct p) {
   typedef typename D::vec vec;
   constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, MF = WM / 16, NF = WN / 16;
@@ -376,31 +371,44 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
   }
 
   // lane (r, g): row r of each 16, columns 4 NF g ... (rows) or 16 j + 4 g ... (turned)
+  constexpr int NV = BT ? 4 : 8, NG = WN / 4 / NV;  // columns of a group, groups of a row
+  const int64_t m = m0 + wm + r;
+  auto column = [&](int k) { return n0 + wn + (BT ? 16 * k + 4 * g : 4 * NF * g + 8 * k); };
+  if (p.partial) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        if (m + 16 * i >= p.M || column(k) >= p.N) continue;
+        float* to = p.partial + ((size_t)split * p.M + m + 16 * i) * p.N + column(k);
+#pragma unroll
+        for (int e = 0; e < NV / 4; ++e) *(acc4*)(to + 4 * e) = acc[i][k * (NV / 4) + e];
+      }
+    return;
+  }
+  Residual<D, NV, KIND> res[2][NG];
+  auto load_row = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+      if (m + 16 * i < p.M && column(k) < p.N) res[i & 1][k].load(p.out, m + 16 * i, (int)column(k));
+  };
+  load_row(0);
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int64_t m = m0 + wm + 16 * i + r;
-    if (m >= p.M) continue;
+    if (i + 1 < MF) load_row(i + 1);
 #pragma unroll
-    for (int j = 0; j < NF; j += BT ? 1 : 2) {
-      const int64_t n = n0 + wn + (BT ? 16 * j + 4 * g : 4 * NF * g + 4 * j);
-      if (n >= p.N) continue;
-      constexpr int NV = BT ? 4 : 8;
+    for (int k = 0; k < NG; ++k) {
+      if (m + 16 * i >= p.M || column(k) >= p.N) continue;
       float v[NV];
 #pragma unroll
-      for (int e = 0; e < NV; ++e) v[e] = acc[i][j + e / 4][e & 3];
-      if (p.partial) {
-        float* to = p.partial + ((size_t)split * p.M + m) * p.N + n;
-#pragma unroll
-        for (int e = 0; e < NV; e += 4) *(fx4*)(to + e) = fx4{v[e], v[e + 1], v[e + 2], v[e + 3]};
-      } else {
-        finish<D, NV>(p.out, m, (int)n, v);
-      }
+      for (int e = 0; e < NV; ++e) v[e] = acc[i][k * (NV / 4) + e / 4][e & 3];
+      finish<D, NV, KIND>(p.out, m + 16 * i, (int)column(k), v, res[i & 1][k]);
     }
   }
 }
 
 // Adds the partial sums of a split reduction in their order, 8 columns a thread.
-template <class D>
+template <class D, int KIND>
 __global__ __launch_bounds__(256) void k_join(LinearProduct p, int splits) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n8 = p.N / 8;
   if (i >= p.M * n8) return;
@@ -421,7 +429,9 @@ __global__ __launch_bounds__(256) void k_join(LinearProduct p, int splits) {
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = s[j];
-  finish<D, 8>(p.out, m, n, v);
+  Residual<D, 8, KIND> res;
+  res.load(p.out, m, n);
+  finish<D, 8, KIND>(p.out, m, n, v, res);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -430,7 +440,7 @@ constexpr int kSkinnyWaves = 16;
 // 16 rows of W a workgroup; its 16 waves take every 16th piece of 64 of the
 // reduction, both operands straight into registers, and their sums are added in
 // wave order. Whole 128-byte lines of W, once.
-template <class D>
+template <class D, int KIND>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
   typedef typename D::vec vec;
   __shared__ float sums[kSkinnyWaves][16][16];
@@ -474,7 +484,9 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
 #pragma unroll
     for (int i = 1; i < kSkinnyWaves; ++i) s += *(const fx4*)&sums[i][t][q];
     float v[4] = {s[0], s[1], s[2], s[3]};
-    finish<D, 4>(p.out, t, (int)(n0 + q), v);
+    Residual<D, 4, KIND> res;
+    res.load(p.out, t, (int)(n0 + q));
+    finish<D, 4, KIND>(p.out, t, (int)(n0 + q), v, res);
   }
 }
 
@@ -580,17 +592,17 @@ __global__ __launch_bounds__(256) void k_dbias(const float* part, int groups, in
 }
 
 // ---------------------------------------------------------------- launches
-template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT>
+template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT, int KIND>
 hipError_t launch_tiles(LinearProduct& p, hipStream_t s) {
   static unsigned long long raised = 0;
   constexpr int lds = 5 * 64 * (BM + BN);
-  const hipError_t e = raise_lds_limit((const void*)&k_product<D, BM, BN, WM, WN, AT, BT>, lds, raised);
+  const hipError_t e = raise_lds_limit((const void*)&k_product<D, BM, BN, WM, WN, AT, BT, KIND>, lds, raised);
   if (e != hipSuccess) return e;
-  k_product<D, BM, BN, WM, WN, AT, BT><<<p.tm * p.tn * p.splits, 64 * (BM / WM) * (BN / WN), lds, s>>>(p);
+  k_product<D, BM, BN, WM, WN, AT, BT, KIND><<<p.tm * p.tn * p.splits, 64 * (BM / WM) * (BN / WN), lds, s>>>(p);
   return hipGetLastError();
 }
 
-template <class D, bool AT, bool BT>
+template <class D, bool AT, bool BT, int KIND>
 hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partial, hipStream_t s) {
   p.tm = plan.tm;
   p.tn = plan.tn;
@@ -599,22 +611,22 @@ hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partia
   p.stages = plan.stages;
   p.parts = plan.parts;
   p.partial = plan.splits > 1 ? partial : nullptr;
-  const hipError_t e = plan.rows == 256   ? launch_tiles<D, 256, 256, 128, 64, AT, BT>(p, s)
-                       : plan.rows == 192 ? launch_tiles<D, 192, 256, 96, 64, AT, BT>(p, s)
-                                          : launch_tiles<D, 128, 128, 64, 64, AT, BT>(p, s);
+  const hipError_t e = plan.rows == 256   ? launch_tiles<D, 256, 256, 128, 64, AT, BT, KIND>(p, s)
+                       : plan.rows == 192 ? launch_tiles<D, 192, 256, 96, 64, AT, BT, KIND>(p, s)
+                                          : launch_tiles<D, 128, 128, 64, 64, AT, BT, KIND>(p, s);
   if (e != hipSuccess || plan.splits == 1) return e;
   const int64_t n = p.M * (p.N / 8);
-  k_join<D><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.splits);
+  k_join<D, KIND><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.splits);
   return hipGetLastError();
 }
 
-template <class D>
+template <class D, int KIND>
 hipError_t forward(const LinearProduct& p, float* ws, hipStream_t s) {
   if (linear_skinny(p.M)) {
-    k_skinny<D><<<(unsigned)((p.N + 15) / 16), 64 * kSkinnyWaves, 0, s>>>(p);
+    k_skinny<D, KIND><<<(unsigned)((p.N + 15) / 16), 64 * kSkinnyWaves, 0, s>>>(p);
     return hipGetLastError();
   }
-  return launch_product<D, false, false>(p, linear_plan(p.M, p.N, p.K, 1), ws, s);
+  return launch_product<D, false, false, KIND>(p, linear_plan(p.M, p.N, p.K, 1), ws, s);
 }
 
 template <class D>
@@ -641,14 +653,14 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
     g.A = g.A2 = dz; g.B = p.W; g.lda = p.N; g.ldb = p.Kd;
     g.M = p.T; g.N = p.Kd; g.K = p.N;
     g.out = LinearOut{nullptr, nullptr, nullptr, p.dX, scale, MPB_ACT_NONE, 0, p.Kd};
-    if ((e = launch_product<D, false, true>(g, linear_plan(g.M, g.N, g.K, 1), p.partial, s)) != hipSuccess) return e;
+    if ((e = launch_product<D, false, true, kGrad16>(g, linear_plan(g.M, g.N, g.K, 1), p.partial, s)) != hipSuccess) return e;
   }
   if (p.dW) {
     LinearProduct g{};
     g.A = dz; g.A2 = formed ? p.lo : dz; g.B = p.X; g.lda = p.N; g.ldb = p.Kd;
     g.M = p.N; g.N = p.Kd; g.K = p.T;
     g.out = LinearOut{nullptr, nullptr, nullptr, p.dW, scale, MPB_ACT_NONE, 1, p.Kd};
-    if ((e = launch_product<D, true, true>(g, linear_plan(g.M, g.N, g.K, formed ? 2 : 1), p.partial, s)) != hipSuccess) return e;
+    if ((e = launch_product<D, true, true, kGrad32>(g, linear_plan(g.M, g.N, g.K, formed ? 2 : 1), p.partial, s)) != hipSuccess) return e;
   }
   return hipSuccess;
 }
@@ -686,7 +698,8 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
 }
 
 hipError_t launch_linear(const LinearProduct& p, bool bf16, float* ws, hipStream_t s) {
-  return bf16 ? forward<BF16>(p, ws, s) : forward<F16>(p, ws, s);
+  if (p.out.y32) return bf16 ? forward<BF16, kOut32>(p, ws, s) : forward<F16, kOut32>(p, ws, s);
+  return bf16 ? forward<BF16, kOut16>(p, ws, s) : forward<F16, kOut16>(p, ws, s);
 }
 
 hipError_t launch_linear_grad(const LinearGradParams& p, bool bf16, hipStream_t s) {
