@@ -437,13 +437,12 @@ int moe_linear(const void* X_dev, int x_dtype, const void* W_dev, const float* b
  *               may be NULL (W_dev is read for dX, X_dev for dW)
  * relu' is 0 at 0. Sums are fp32 in a fixed order (deterministic). Where dz is not
  * dy itself (an activation, or fp32 dy) the products take it in 16-bit parts: dX,
- * which is rounded to that type, from dz rounded to x_dtype, dW from dz to 16 bits
- * (bf16) or 22 (fp16; those of a value not below 2^-16 of the largest |dz|, to
- * 2^-38 of that below), dbias from dz itself. fp16 parts carry a power of two, so that small
- * gradients keep their bits whatever their range; an infinite or NaN dz gives
- * infinite or NaN sums. T == 0 zeroes dW and dbias. ws_dev: at least
- * moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype) bytes. Limits and errors
- * as above.
+ * which is rounded to that type, from dz rounded to x_dtype, dW from dz to 22 bits (and
+ * to 2^-38 of the largest |dy|; bf16 X to 2^-38 of its largest), dbias from dz itself.
+ * fp16 parts carry a power of two, so that small gradients keep their bits whatever
+ * their range; an infinite or NaN dz gives infinite or NaN sums. T == 0 zeroes dW
+ * and dbias. ws_dev: at least moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype)
+ * bytes. Limits and errors as above.
  */
 size_t moe_linear_grad_workspace_bytes(int T, int Kd, int N, int act, int dy_dtype);
 int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, const void* z_dev, const void* dy_dev,

@@ -16,12 +16,13 @@
 // A batch of up to 16 tokens reads W once and has nothing to share: k_skinny, W
 // straight into the registers.
 //
-// dz is formed once, in the activations' type, for both gradients. Where it is not
-// exactly dy (an activation, or fp32 dy) it is rounded for dX, whose result is
-// rounded to the same type anyway, and kept as two parts for dW, whose result is
-// fp32: 16 bits of bf16, 22 of fp16. fp16 parts are scaled by a power of two that
-// brings the largest |dz| to 2^14, so that the gradients of a mean, below fp16's
-// range, keep their bits.
+// dz is formed once for both gradients. Where it is not exactly dy (an activation, or
+// fp32 dy) it is rounded to the activations' type for dX, whose result is rounded to that type
+// anyway. dW, whose result is fp32, takes it as two fp16 parts of 22 bits together
+// (bf16 parts have 16: 2.6e-6 of the result's norm off at 4093 tokens, an fp32 library
+// product 1.2e-6; a third one would cost a third of dW's time again), and bf16 X as
+// fp16 beside it. What becomes fp16 is scaled by a power of two that brings its
+// largest value to 2^13: the gradients of a mean, below fp16's range, keep their bits.
 #include <type_traits>
 
 #include "k_block_common.h"
@@ -53,7 +54,7 @@ constexpr float kSqrtHalf = 0.707106781f, kInvSqrt2Pi = 0.398942280f;
 constexpr float kTanhA = 0.797884561f, kTanhB = 0.044715f;  // sqrt(2 / pi)
 
 // For results of 16 bits: within |x| 2^-24 of itself, 2^-9 being asked, in half the
-// operations (4093 x 5632 x 2816 with gelu_tanh: TODO).
+// operations (4093 x 5632 x 2816 with gelu_tanh: 148 us with the other, 143 with this).
 __device__ __forceinline__ float sigmoid16(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269502f * x));
 }
@@ -71,22 +72,34 @@ __device__ __forceinline__ float act_of(float z, int act) {
     default: return z;
   }
 }
+// sigmoid(x) and sigmoid(-x), each within 6 x 2^-24 of itself (see sigmoid).
+struct Sigmoids {
+  float of, of_minus;
+};
+__device__ __forceinline__ Sigmoids sigmoids(float x) {
+  const float a = fabsf(x), t = a * 1.44269502f;
+  const float rest = fmaf(a, 1.92596303e-8f, fmaf(a, 1.44269502f, -t));
+  const float p = __builtin_amdgcn_exp2f(-t), e = fmaf(p * rest, -0.693147182f, p), d = 1.0f + e;
+  const float y = __builtin_amdgcn_rcpf(d), r = fmaf(fmaf(-d, y, 1.0f), y, y), er = e * r;
+  return x < 0.0f ? Sigmoids{er, r} : Sigmoids{r, er};
+}
 // z is limited where the derivative has long been 0 or 1, so that no inf meets a 0.
 __device__ __forceinline__ float act_grad(float z, int act) {
   switch (act) {
     case MPB_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     case MPB_ACT_SILU: {
       const float x = z != z ? z : fminf(fmaxf(z, -120.0f), 120.0f);
-      return sigmoid(x) * (1.0f + x * sigmoid(-x));
+      const Sigmoids s = sigmoids(x);
+      return s.of * fmaf(x, s.of_minus, 1.0f);
     }
     case MPB_ACT_GELU: {
       const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f);
       return 0.5f * erfcf(-x * kSqrtHalf) + x * kInvSqrt2Pi * expf(-0.5f * x * x);
     }
     case MPB_ACT_GELU_TANH: {
-      const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f);
-      const float u = 2.0f * kTanhA * (x + kTanhB * x * x * x), s = sigmoid(u);
-      return s + x * s * sigmoid(-u) * 2.0f * kTanhA * (1.0f + 3.0f * kTanhB * x * x);
+      const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f), x2 = x * x;
+      const Sigmoids s = sigmoids(2.0f * kTanhA * x * fmaf(kTanhB, x2, 1.0f));
+      return fmaf(x * s.of * s.of_minus, 2.0f * kTanhA * fmaf(3.0f * kTanhB, x2, 1.0f), s.of);
     }
     default: return 1.0f;
   }
@@ -129,6 +142,7 @@ __device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, flo
   constexpr bool kNarrow = KIND == kGrad16 || KIND == kOut16;
   if constexpr (KIND == kGrad16 || KIND == kGrad32) {
     if (o.scale) w *= *o.scale;
+    if (o.scale2) w *= *o.scale2;  // one after the other: their product may be out of range
   } else {
     if (o.bias) w += *(const fvec*)(o.bias + n);
     if (o.z) *(evec*)((elem*)o.z + at) = __builtin_convertvector(w, evec);
@@ -505,28 +519,52 @@ __device__ __forceinline__ fx8 dz8(const LinearGradParams& p, size_t at) {
   return d;
 }
 
-// The largest finite |dz| of each workgroup's share.
+// The largest finite |v| of each workgroup's share: of dy, and in the second half of
+// the grid of X where it is to become fp16.
 template <class D>
-__global__ __launch_bounds__(256) void k_dz_max(LinearGradParams p) {
+__global__ __launch_bounds__(256) void k_max(LinearGradParams p) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
   __shared__ float red[4];
-  const int64_t n8 = (int64_t)p.T * p.N / 8;
+  const bool of_x = blockIdx.y == 1;
+  const int64_t n8 = (int64_t)p.T * (of_x ? p.Kd : p.N) / 8;
   float m = 0.0f;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
-    const fx8 d = dz8<D>(p, 8 * i);
+  auto take = [&](const fx8& d) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float a = fabsf(d[j]);
       if (a < INFINITY) m = fmaxf(m, a);
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step) {
+    if (!of_x && p.dy32) take(load8((const float*)p.dy + 8 * i));
+    else take(widen<D>(*(const vec*)((const elem*)(of_x ? p.X : p.dy) + 8 * i)));
   }
   m = wave_max(m);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0) p.maxima[blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if (threadIdx.x == 0) p.maxima[blockIdx.y * kMaxima + blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
 
-// dz as one or two parts, and the sums over a group of rows for dbias. A thread
-// has 8 columns, a workgroup 512 of them and 4 waves of rows.
+// The exponent e of the scale that brings the largest of k_max's values into [2^13,
+// 2^14): an activation's slope of up to 1.13 and the rounding to fp16 stay in range.
+__device__ __forceinline__ int scale_of(const float* maxima, float (&red)[4]) {
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < kMaxima; i += 256) m = fmaxf(m, maxima[i]);
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  __syncthreads();
+  if (m == 0.0f) return 0;
+  int e = 0;
+  (void)frexpf(m, &e);  // m = f 2^e, f in [1/2, 1)
+  return min(max(14 - e, -126), 126);
+}
+
+// dz for dX and in two parts for dW, and the sums over a group of rows for dbias. A
+// thread has 8 columns, a workgroup 512 of them and 4 waves of rows.
 template <class D>
 __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
   typedef typename D::vec vec;
@@ -537,21 +575,11 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
   const int64_t n = (int64_t)blockIdx.x * 512 + 8 * lane;
   float scale = 1.0f;
   if (p.maxima) {
-    float m = 0.0f;
-    for (int i = threadIdx.x; i < kDzMaxima; i += 256) m = fmaxf(m, p.maxima[i]);
-    m = wave_max(m);
-    if (lane == 0) s_max[wave] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    // m = f 2^e with f in [1/2, 1): m scale below 2^14
-    int e = 0;
-    if (m > 0.0f) {
-      (void)frexpf(m, &e);
-      e = min(max(14 - e, -126), 126);
-    }
+    const int e = scale_of(p.maxima, s_max);
     scale = ldexpf(1.0f, e);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.inv_scale = ldexpf(1.0f, -e);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.inv_scale[0] = ldexpf(1.0f, -e);
   }
+  constexpr bool kHalf = std::is_same<D, F16>::value;
   fx8 sum = (fx8)(0.0f);
   if (n < p.N) {
     const int t0 = blockIdx.y * p.rows, t1 = min(p.T, t0 + p.rows);
@@ -559,11 +587,12 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
       const size_t at = (size_t)t * p.N + n;
       const fx8 d = dz8<D>(p, at);
       sum += d;
-      if (p.hi) {
-        const fx8 x = d * scale;
-        const vec h = narrow<D>(x);
-        *(vec*)((elem*)p.hi + at) = h;
-        if (p.lo) *(vec*)((elem*)p.lo + at) = narrow<D>(x - widen<D>(h));
+      const fx8 x = d * scale;
+      if (p.dz) *(vec*)((elem*)p.dz + at) = narrow<D>(kHalf ? x : d);
+      if (p.part1) {
+        const hx8 h = narrow<F16>(x);
+        *(hx8*)((_Float16*)p.part1 + at) = h;
+        *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
       }
     }
   }
@@ -575,6 +604,21 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
     const int64_t col = (int64_t)blockIdx.x * 512 + c;
     if (col < p.N) p.db_part[(size_t)blockIdx.y * p.N + col] = red[0][c] + red[1][c] + red[2][c] + red[3][c];
   }
+}
+
+// bf16 X as scaled fp16, and the factor that takes both scales out of dW. A value's 8
+// bits fit unless it is below 2^-30 of the largest.
+__global__ __launch_bounds__(256) void k_x16(LinearGradParams p) {
+  __shared__ float s_max[4];
+  const int ez = scale_of(p.maxima, s_max), ex = scale_of(p.maxima + kMaxima, s_max);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.inv_scale[1] = ldexpf(1.0f, -ex);
+    p.inv_scale[2] = ldexpf(1.0f, -ez);
+  }
+  const float scale = ldexpf(1.0f, ex);
+  const int64_t n8 = (int64_t)p.T * p.Kd / 8, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step)
+    *(hx8*)((_Float16*)p.x16 + 8 * i) = narrow<F16>(widen<BF16>(*(const bx8*)((const __bf16*)p.X + 8 * i)) * scale);
 }
 
 // dbias: the groups' sums in their order.
@@ -631,36 +675,46 @@ hipError_t forward(const LinearProduct& p, float* ws, hipStream_t s) {
 
 template <class D>
 hipError_t gradients(LinearGradParams p, hipStream_t s) {
+  constexpr bool kHalf = std::is_same<D, F16>::value;
   hipError_t e = hipSuccess;
-  const bool formed = p.hi != nullptr;
+  const bool formed = p.dz || p.part1;
+  const int groups = (p.T + p.rows - 1) / p.rows;
   if (p.T > 0 && (formed || p.dbias)) {
     if (p.maxima) {
-      k_dz_max<D><<<kDzMaxima, 256, 0, s>>>(p);
+      k_max<D><<<dim3(kMaxima, p.x16 ? 2 : 1), 256, 0, s>>>(p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const int groups = (p.T + p.rows - 1) / p.rows;
     k_dz<D><<<dim3((p.N + 511) / 512, groups), 256, 0, s>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (p.x16) {
+      k_x16<<<2048, 256, 0, s>>>(p);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
   }
   if (p.dbias) {
-    k_dbias<<<(p.N + 63) / 64, 256, 0, s>>>(p.db_part, p.T > 0 ? (p.T + p.rows - 1) / p.rows : 0, p.N, p.dbias);
+    k_dbias<<<(p.N + 63) / 64, 256, 0, s>>>(p.db_part, groups, p.N, p.dbias);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const void* dz = formed ? p.hi : p.dy;
-  const float* scale = p.maxima && p.T > 0 ? p.inv_scale : nullptr;  // written by k_dz
+  const bool scaled = p.maxima && p.T > 0;  // the scales are there
   if (p.dX && p.T > 0) {
     LinearProduct g{};
-    g.A = g.A2 = dz; g.B = p.W; g.lda = p.N; g.ldb = p.Kd;
+    g.A = g.A2 = p.dz ? p.dz : p.dy; g.B = p.W; g.lda = p.N; g.ldb = p.Kd;
     g.M = p.T; g.N = p.Kd; g.K = p.N;
-    g.out = LinearOut{nullptr, nullptr, nullptr, p.dX, scale, MPB_ACT_NONE, 0, p.Kd};
+    g.out.y = p.dX; g.out.N = p.Kd;
+    g.out.scale = scaled && kHalf ? p.inv_scale : nullptr;
     if ((e = launch_product<D, false, true, kGrad16>(g, linear_plan(g.M, g.N, g.K, 1), p.partial, s)) != hipSuccess) return e;
   }
   if (p.dW) {
     LinearProduct g{};
-    g.A = dz; g.A2 = formed ? p.lo : dz; g.B = p.X; g.lda = p.N; g.ldb = p.Kd;
+    g.A = p.part1 ? p.part1 : p.dy; g.A2 = p.part1 ? p.part2 : p.dy; g.B = p.x16 ? p.x16 : p.X; g.lda = p.N; g.ldb = p.Kd;
     g.M = p.N; g.N = p.Kd; g.K = p.T;
-    g.out = LinearOut{nullptr, nullptr, nullptr, p.dW, scale, MPB_ACT_NONE, 1, p.Kd};
-    if ((e = launch_product<D, true, true, kGrad32>(g, linear_plan(g.M, g.N, g.K, formed ? 2 : 1), p.partial, s)) != hipSuccess) return e;
+    g.out.y = p.dW; g.out.N = p.Kd;
+    g.out.scale = scaled ? p.inv_scale + (p.x16 ? 1 : 0) : nullptr;
+    g.out.scale2 = scaled && p.x16 ? p.inv_scale + 2 : nullptr;
+    const LinearPlan plan = linear_plan(g.M, g.N, g.K, p.part1 ? 2 : 1);
+    // two parts are fp16 whatever the activations are
+    e = p.part1 ? launch_product<F16, true, true, kGrad32>(g, plan, p.partial, s) : launch_product<D, true, true, kGrad32>(g, plan, p.partial, s);
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }

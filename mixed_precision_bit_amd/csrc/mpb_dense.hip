@@ -54,13 +54,14 @@ size_t partial_bytes(const mpb::LinearPlan& p, int64_t M, int64_t N) {
   return p.splits > 1 ? up((size_t)p.splits * M * N * sizeof(float)) : 0;
 }
 
-// Regions of moe_linear_grad's workspace. dz is formed where it is not dy itself.
+// Regions of moe_linear_grad's workspace. dz is formed where it is not dy itself: as
+// activations for dX, and for dW as two fp16 parts, of which fp16 shares the first.
 struct GradWs {
-  size_t hi, lo, maxima, inv_scale, db_part, partial, total;
+  size_t dz, part1, part2, x16, maxima, inv_scale, db_part, partial, total;
   int rows;
   bool formed;
 };
-GradWs grad_ws(int T, int Kd, int N, int act, bool dy32) {
+GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
   GradWs w{};
   w.formed = act != MPB_ACT_NONE || dy32;
   // some 1024 workgroups of 512 columns, groups of at least 16 tokens
@@ -76,10 +77,12 @@ GradWs grad_ws(int T, int Kd, int N, int act, bool dy32) {
     return o;
   };
   const size_t part = (size_t)T * N * 2;
-  w.hi = take(w.formed ? part : 0);
-  w.lo = take(w.formed ? part : 0);
-  w.maxima = take(mpb::kDzMaxima * sizeof(float));
-  w.inv_scale = take(sizeof(float));
+  w.dz = take(w.formed ? part : 0);
+  w.part1 = bf16 ? take(w.formed ? part : 0) : w.dz;
+  w.part2 = take(w.formed ? part : 0);
+  w.x16 = take(w.formed && bf16 ? (size_t)T * Kd * 2 : 0);
+  w.maxima = take(2 * mpb::kMaxima * sizeof(float));
+  w.inv_scale = take(3 * sizeof(float));
   w.db_part = take((size_t)((T + w.rows - 1) / w.rows) * N * sizeof(float));
   const size_t px = T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, 1), T, Kd) : 0;
   const size_t pw = partial_bytes(mpb::linear_plan(N, Kd, T, w.formed ? 2 : 1), N, Kd);
@@ -158,7 +161,7 @@ int moe_linear(const void* X_dev, int x_dtype, const void* W_dev, const float* b
   mpb::LinearProduct p{};
   p.A = p.A2 = X_dev; p.B = W_dev; p.lda = p.ldb = Kd;
   p.M = T; p.N = N; p.K = Kd;
-  p.out = mpb::LinearOut{bias_dev, res_dev, z_dev, y_dev, nullptr, act, y_dtype == MPB_F32, N};
+  p.out = mpb::LinearOut{bias_dev, res_dev, z_dev, y_dev, nullptr, nullptr, act, y_dtype == MPB_F32, N};
   const hipError_t e = mpb::launch_linear(p, x_dtype == MPB_BF16, (float*)ws_dev, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, n);
   return MPB_OK;
@@ -168,7 +171,7 @@ int moe_linear(const void* X_dev, int x_dtype, const void* W_dev, const float* b
 
 size_t moe_linear_grad_workspace_bytes(int T, int Kd, int N, int act, int dy_dtype) {
   if (!linear_shape(T, Kd, N) || act < MPB_ACT_NONE || act > MPB_ACT_GELU_TANH) return 0;
-  return grad_ws(T, Kd, N, act, dy_dtype == MPB_F32).total;
+  return grad_ws(T, Kd, N, act, dy_dtype == MPB_F32, true).total;  // of either activation type
 }
 
 int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, const void* z_dev, const void* dy_dev,
@@ -184,23 +187,26 @@ int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, 
     return fail(MPB_E_ARG, n + ": null pointer");
   if (!all_aligned16(X_dev, W_dev, z_dev, dy_dev, dX_dev, dW_dev, dbias_dev))
     return fail(MPB_E_ARG, n + ": rows must be 16-byte aligned");
-  const GradWs w = grad_ws(T, Kd, N, act, dy_dtype == MPB_F32);
-  rc = check_ws(n, ws_dev, ws_bytes, w.total);
+  const bool bf16 = x_dtype == MPB_BF16;
+  const GradWs w = grad_ws(T, Kd, N, act, dy_dtype == MPB_F32, bf16);
+  rc = check_ws(n, ws_dev, ws_bytes, moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype));
   if (rc) return rc;
   char* ws = (char*)ws_dev;
   mpb::LinearGradParams p{};
   p.X = X_dev; p.W = W_dev; p.z = z_dev; p.dy = dy_dev;
   p.dX = dX_dev; p.dW = dW_dev; p.dbias = dbias_dev;
-  const bool products = dX_dev || dW_dev;
-  p.hi = w.formed && products ? ws + w.hi : nullptr;
-  p.lo = w.formed && dW_dev ? ws + w.lo : nullptr;
-  p.maxima = p.hi && x_dtype == MPB_F16 ? (float*)(ws + w.maxima) : nullptr;
+  const bool parts = w.formed && dW_dev;
+  p.dz = w.formed && dX_dev ? ws + w.dz : nullptr;
+  p.part1 = parts ? ws + w.part1 : nullptr;
+  p.part2 = parts ? ws + w.part2 : nullptr;
+  p.x16 = parts && bf16 ? ws + w.x16 : nullptr;
+  p.maxima = parts || (p.dz && !bf16) ? (float*)(ws + w.maxima) : nullptr;
   p.inv_scale = (float*)(ws + w.inv_scale);
   p.db_part = (float*)(ws + w.db_part);
   p.partial = (float*)(ws + w.partial);
   p.T = T; p.Kd = Kd; p.N = N; p.act = act; p.dy32 = dy_dtype == MPB_F32;
   p.rows = w.rows;
-  const hipError_t e = mpb::launch_linear_grad(p, x_dtype == MPB_BF16, (hipStream_t)stream);
+  const hipError_t e = mpb::launch_linear_grad(p, bf16, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, n);
   return MPB_OK;
 } catch (...) {

@@ -373,7 +373,8 @@ struct LinearOut {
   const void* res;         // [M][N] of y's type, or null
   void* z;                 // [M][N] activations, or null
   void* y;                 // [M][N] activations or fp32
-  const float* scale;      // device scalar that multiplies the product, or null
+  const float* scale;      // device scalars that multiply the product, or null
+  const float* scale2;
   int act, y32;
   int64_t N;
 };
@@ -396,7 +397,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts);
 inline bool linear_skinny(int64_t M) { return M <= 16; }
 hipError_t launch_linear(const LinearProduct& p, bool bf16, float* ws, hipStream_t s);
 
-constexpr int kDzMaxima = 1024;  // workgroups of the search for the largest |dz|
+constexpr int kMaxima = 1024;  // workgroups of a search for the largest value
 struct LinearGradParams {
   const void* X;           // [T][Kd]
   const void* W;           // [N][Kd]
@@ -405,11 +406,13 @@ struct LinearGradParams {
   void* dX;                // [T][Kd] or null
   float* dW;               // [N][Kd] or null
   float* dbias;            // [N] or null
-  // workspace
-  void* hi;                // [T][N] dz, or null (dz is dy)
-  void* lo;                // [T][N] what hi's rounding left, or null
-  float* maxima;           // [kDzMaxima], or null (not scaled)
-  float* inv_scale;
+  // workspace; the first three are null where dz is dy, or no product needs them
+  void* dz;                // [T][N] dz as activations (fp16: scaled)
+  void* part1;             // [T][N] dz as scaled fp16 (fp16: the same buffer as dz)
+  void* part2;             // [T][N] what its rounding left
+  void* x16;               // [T][Kd] bf16 X as scaled fp16 (with part1), or null
+  float* maxima;           // [2][kMaxima] of |dy| and |X|, or null (nothing is scaled)
+  float* inv_scale;        // [3] of dz; of X and of dz (with x16)
   float* db_part;          // [groups][N]
   float* partial;
   int T, Kd, N, act, dy32;
