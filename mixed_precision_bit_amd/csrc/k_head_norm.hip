@@ -151,8 +151,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_head_norm(HeadNormParams p) {
       if (16 * l < p.Dr) turn<HALVES>(a, b, cs, sn);
       const size_t out = (size_t)t * (key ? p.ko_ld : p.qo_ld) + (size_t)h * p.D;
       elem* dst = (elem*)(key ? p.k_out : p.q_out);
-      *(vec*)(dst + out + oa) = narrow<D>(a);
-      *(vec*)(dst + out + ob) = narrow<D>(b);
+      stream_store((vec*)(dst + out + oa), narrow<D>(a));
+      stream_store((vec*)(dst + out + ob), narrow<D>(b));
     }
   }
 }
@@ -192,8 +192,14 @@ __device__ __forceinline__ void store_dgamma(const fx8& a, const fx8& b, float* 
   __syncthreads();
 }
 
+// A wave's share of one group of heads as loaded: the gradient's and x's two vectors.
+template <class D>
+struct GradGroup {
+  typename D::vec a, b, xa, xb;
+};
+
 template <class D, int NL, bool HALVES>
-__global__ __launch_bounds__(64 * kWaves) void k_head_norm_grad(HeadNormGradParams q) {
+__global__ __launch_bounds__(64 * kWaves, 3) void k_head_norm_grad(HeadNormGradParams q) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
   constexpr int HG = 64 / NL;
@@ -206,55 +212,85 @@ __global__ __launch_bounds__(64 * kWaves) void k_head_norm_grad(HeadNormGradPara
   lane_offsets(p, l, oa, ob);
   const float inv_d = 1.0f / (float)p.D;
   fx8 gqa = (fx8)(0.0f), gqb = gqa, gka = gqa, gkb = gqa;
-  const int64_t items = (int64_t)p.T * p.parts;
-  for (int64_t item = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * kWaves) {
-    const int t = (int)(item / p.parts), part = (int)(item - (int64_t)t * p.parts);
-    fx8 cs, sn;
-    if (mine) lane_angles(p, l, t, cs, sn);
-    for (int g = part; g < n.nq + n.nk; g += p.parts) {
-      const bool key = g >= n.nq;
-      const int h = (key ? g - n.nq : g) * HG + lane / NL;
-      const bool on = mine && h < (key ? p.Hk : p.Hq);
-      const float* gamma = key ? p.g_k : p.g_q;
-      fx8 a = (fx8)(0.0f), b = a, xa = a, xb = a;
+  const int64_t items = (int64_t)p.T * p.parts, step = (int64_t)gridDim.x * kWaves;
+  int64_t item = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  int t = 0, g = 0;
+  auto begin = [&]() {
+    t = (int)(item / p.parts);
+    g = (int)(item - (int64_t)t * p.parts);
+  };
+  auto head = [&](int g, bool& key, bool& on) {
+    key = g >= n.nq;
+    const int h = (key ? g - n.nq : g) * HG + lane / NL;
+    on = mine && h < (key ? p.Hk : p.Hq);
+    return h;
+  };
+  auto load = [&](GradGroup<D>& v, int t, int g) {
+    bool key, on;
+    const int h = head(g, key, on);
+    v.a = v.b = v.xa = v.xb = (vec)(0);
+    if (!on) return;
+    const size_t at = (size_t)t * (key ? p.ko_ld : p.qo_ld) + (size_t)h * p.D;
+    const elem* d = (const elem*)(key ? q.dk_out : q.dq_out);
+    v.a = *(const vec*)(d + at + oa);
+    v.b = *(const vec*)(d + at + ob);
+    if (key ? p.g_k : p.g_q) {
+      const size_t in = (size_t)t * (key ? p.k_ld : p.q_ld) + (size_t)h * p.D;
+      const elem* x = (const elem*)(key ? p.k : p.q);
+      v.xa = *(const vec*)(x + in + oa);
+      v.xb = *(const vec*)(x + in + ob);
+    }
+  };
+  GradGroup<D> next;
+  fx8 cs, sn;
+  bool fresh = true;  // a token's first group
+  if (item < items) {
+    begin();
+    load(next, t, g);
+  }
+  while (item < items) {
+    const GradGroup<D> now = next;
+    const int ti = t, gi = g;
+    const bool first = fresh;
+    // the next group's loads go out before this one is worked on
+    g += p.parts;
+    fresh = g >= n.nq + n.nk;
+    if (fresh) {
+      item += step;
+      if (item < items) begin();
+    }
+    if (item < items) load(next, t, g);
+    if (first && mine) lane_angles(p, l, ti, cs, sn);
+    bool key, on;
+    const int h = head(gi, key, on);
+    const float* gamma = key ? p.g_k : p.g_q;
+    fx8 a = widen<D>(now.a), b = widen<D>(now.b);
+    if (on && 16 * l < p.Dr) turn<HALVES>(a, b, cs, -sn);
+    if (gamma) {
+      fx8 xa = widen<D>(now.xa), xb = widen<D>(now.xb);
+      const float r = rsqrtf(head_sum<NL>(sum_sq(xa, xb)) * inv_d + p.eps);
+      xa *= r;
+      xb *= r;
+      if (key) {
+        gka += a * xa;
+        gkb += b * xb;
+      } else {
+        gqa += a * xa;
+        gqb += b * xb;
+      }
       if (on) {
-        const size_t at = (size_t)t * (key ? p.ko_ld : p.qo_ld) + (size_t)h * p.D;
-        const elem* d = (const elem*)(key ? q.dk_out : q.dq_out);
-        a = widen<D>(*(const vec*)(d + at + oa));
-        b = widen<D>(*(const vec*)(d + at + ob));
-        if (gamma) {
-          const size_t in = (size_t)t * (key ? p.k_ld : p.q_ld) + (size_t)h * p.D;
-          const elem* x = (const elem*)(key ? p.k : p.q);
-          xa = widen<D>(*(const vec*)(x + in + oa));
-          xb = widen<D>(*(const vec*)(x + in + ob));
-        }
-        if (16 * l < p.Dr) turn<HALVES>(a, b, cs, -sn);
+        a *= load8(gamma + oa);
+        b *= load8(gamma + ob);
       }
-      if (gamma) {
-        const float r = rsqrtf(head_sum<NL>(sum_sq(xa, xb)) * inv_d + p.eps);
-        xa *= r;
-        xb *= r;
-        if (key) {
-          gka += a * xa;
-          gkb += b * xb;
-        } else {
-          gqa += a * xa;
-          gqb += b * xb;
-        }
-        if (on) {
-          a *= load8(gamma + oa);
-          b *= load8(gamma + ob);
-        }
-        const float m = head_sum<NL>(dot(a, b, xa, xb)) * inv_d;
-        a = r * (a - xa * m);
-        b = r * (b - xb * m);
-      }
-      if (on) {
-        const size_t out = (size_t)t * (key ? q.dk_ld : q.dq_ld) + (size_t)h * p.D;
-        elem* dst = (elem*)(key ? q.dk : q.dq);
-        *(vec*)(dst + out + oa) = narrow<D>(a);
-        *(vec*)(dst + out + ob) = narrow<D>(b);
-      }
+      const float m = head_sum<NL>(dot(a, b, xa, xb)) * inv_d;
+      a = r * (a - xa * m);
+      b = r * (b - xb * m);
+    }
+    if (on) {
+      const size_t out = (size_t)ti * (key ? q.dk_ld : q.dq_ld) + (size_t)h * p.D;
+      elem* dst = (elem*)(key ? q.dk : q.dq);
+      stream_store((vec*)(dst + out + oa), narrow<D>(a));
+      stream_store((vec*)(dst + out + ob), narrow<D>(b));
     }
   }
   if (q.dg_q) store_dgamma<NL>(gqa, gqb, q.part + (size_t)blockIdx.x * p.D, p.D, oa, ob, l, lds);
@@ -328,7 +364,7 @@ int parts_of(int T, int Hq, int Hk, int D) {
 
 int head_norm_grad_groups(int T, int Hq, int Hk, int D) {
   const int64_t blocks = ((int64_t)T * parts_of(T, Hq, Hk, D) + kWaves - 1) / kWaves;
-  return (int)(blocks < 1024 ? blocks : 1024);
+  return (int)(blocks < 768 ? blocks : 768);  // three a CU are resident
 }
 
 hipError_t launch_head_norm(HeadNormParams p, bool bf16, hipStream_t s) {
