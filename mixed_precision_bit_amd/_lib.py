@@ -265,22 +265,26 @@ class _Args:
         """(pointer, elements from row to row) of a tensor whose rows are contiguous, whatever lies between them."""
         if t is None:
             return None, 0
+        st, row = t.stride(), shape[1] if len(shape) == 2 else shape[1] * shape[2]
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and st[-1] == 1 and st[0] >= row and (
+                len(shape) == 2 or st[1] == shape[2]) and shape[0] > 1:
+            return t.data_ptr(), st[0]
         if t.dtype is not dtype and not (dtype.itemsize == 2 and t.dtype is torch.int16):
             self.fail(f"{what} is {t.dtype}, not {dtype}")
         if t.shape != shape:
             self.fail(f"{what} has shape {tuple(t.shape)}, not {shape}", -2)
         if t.get_device() != self.index:
             self.fail(f"{what} is on {t.device}, other tensors on device {self.index}")
-        row = 1
-        for d in range(t.dim() - 1, 0, -1):
-            if t.stride(d) != row and t.shape[d] > 1:
+        want = 1
+        for d in range(len(shape) - 1, 0, -1):
+            if st[d] != want and shape[d] > 1:
                 self.fail(f"the rows of {what} are not contiguous")
-            row *= t.shape[d]
-        if t.shape[0] < 2:
+            want *= shape[d]
+        if shape[0] < 2:
             return t.data_ptr(), row
-        if t.stride(0) < row:
+        if st[0] < row:
             self.fail(f"the rows of {what} overlap")
-        return t.data_ptr(), t.stride(0)
+        return t.data_ptr(), st[0]
 
     def bytes(self, ws):
         """(pointer, bytes) of a workspace."""

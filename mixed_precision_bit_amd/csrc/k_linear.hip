@@ -431,15 +431,15 @@ __global__ __launch_bounds__(256) void k_join(LinearProduct p, int splits) {
   const float* src = p.partial + (size_t)m * p.N + n;
   const size_t step = (size_t)p.M * p.N;
   fx8 s = load8(src);
-  int k = 1;
-  for (; k + 3 < splits; k += 4) {
-    fx8 v[4];
+  for (int k = 1; k < splits; k += 8) {  // eight loads in flight
+    fx8 v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = load8(src + (k + j) * step);
+    for (int j = 0; j < 8; ++j)
+      if (k + j < splits) v[j] = load8(src + (k + j) * step);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s += v[j];
+    for (int j = 0; j < 8; ++j)
+      if (k + j < splits) s += v[j];
   }
-  for (; k < splits; ++k) s += load8(src + k * step);
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = s[j];
@@ -451,52 +451,64 @@ __global__ __launch_bounds__(256) void k_join(LinearProduct p, int splits) {
 // ---------------------------------------------------------------- few tokens
 constexpr int kSkinnyWaves = 16;
 
-// 16 rows of W a workgroup; its 16 waves take every 16th piece of 64 of the
-// reduction, both operands straight into registers, and their sums are added in
-// wave order. Whole 128-byte lines of W, once.
-template <class D, int KIND>
+// 16 rows of W a workgroup and up to 16 MF tokens; its 16 waves take every 16th piece
+// of 64 of the reduction (whole 128-byte lines of W, once), both operands straight into
+// registers, U halves of pieces in flight. Their sums meet in LDS: waves 8 to 15
+// hand theirs to waves 0 to 7, whose sums are added in wave order.
+template <class D, int KIND, int MF>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
   typedef typename D::vec vec;
-  __shared__ float sums[kSkinnyWaves][16][16];
+  constexpr int U = MF == 1 ? 8 : MF == 2 ? 6 : MF <= 4 ? 4 : 2, kHalfWaves = kSkinnyWaves / 2;
+  __shared__ float sums[kHalfWaves][16 * MF][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int T = (int)p.M;
   const char* w = (const char*)p.B + ((n0 + r < p.N ? n0 + r : p.N - 1) * p.ldb + 8 * g) * 2;
-  const char* x = (const char*)p.A + ((int64_t)min(r, T - 1) * p.lda + 8 * g) * 2;
+  const char* x = (const char*)p.A + 16 * g;
+  uint32_t xo[MF];  // rows past the last repeat it: their results are not stored
+#pragma unroll
+  for (int i = 0; i < MF; ++i) xo[i] = (uint32_t)(min(16 * i + r, T - 1) * p.lda * 2);
   const int pieces = (int)(p.K / 64);
-  acc4 acc = (acc4)(0.0f);
-  constexpr int U = 4;  // pieces in flight
+  acc4 acc[MF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i) acc[i] = (acc4)(0.0f);
   int c = wave;
-  for (; c + (U - 1) * kSkinnyWaves < pieces; c += U * kSkinnyWaves) {
-    vec a[U][2], b[U][2];
+  auto run = [&](auto n) {  // n halves of pieces
+    constexpr int N = decltype(n)::value;
+    vec b[N], a[N][MF];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < N; ++u) {
+      const uint32_t at = (uint32_t)(c + u / 2 * kSkinnyWaves) * 128 + 64 * (u & 1);
+      b[u] = stream_load((const vec*)(w + at));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = (int64_t)(c + u * kSkinnyWaves) * 128 + 64 * h;
-        b[u][h] = stream_load((const vec*)(w + at));
-        a[u][h] = *(const vec*)(x + at);
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) acc = product<D>(b[u][h], a[u][h], acc);
-  }
-  for (; c < pieces; c += kSkinnyWaves)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t at = (int64_t)c * 128 + 64 * h;
-      acc = product<D>(stream_load((const vec*)(w + at)), *(const vec*)(x + at), acc);
+      for (int i = 0; i < MF; ++i) a[u][i] = *(const vec*)(x + at + xo[i]);
     }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) sums[wave][r][4 * g + e] = acc[e];
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < MF; ++i) acc[i] = product<D>(b[u], a[u][i], acc[i]);
+    c += N / 2 * kSkinnyWaves;
+  };
+  while (c + (U / 2 - 1) * kSkinnyWaves < pieces) run(std::integral_constant<int, U>());
+  if constexpr (U > 2) {
+    while (c < pieces) run(std::integral_constant<int, 2>());
+  }
+  if (wave >= kHalfWaves) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i) *(acc4*)&sums[wave - kHalfWaves][16 * i + r][4 * g] = acc[i];
+  }
+  __syncthreads();
+  if (wave < kHalfWaves) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i) *(acc4*)&sums[wave][16 * i + r][4 * g] += acc[i];
+  }
   __syncthreads();
   // 4 columns a thread
   const int t = threadIdx.x >> 2, q = 4 * (threadIdx.x & 3);
-  if (t < T && n0 + q < p.N && t < 16) {
+  if (t < T && t < 16 * MF && n0 + q < p.N) {
     fx4 s = *(const fx4*)&sums[0][t][q];
 #pragma unroll
-    for (int i = 1; i < kSkinnyWaves; ++i) s += *(const fx4*)&sums[i][t][q];
+    for (int i = 1; i < kHalfWaves; ++i) s += *(const fx4*)&sums[i][t][q];
     float v[4] = {s[0], s[1], s[2], s[3]};
     Residual<D, 4, KIND> res;
     res.load(p.out, t, (int)(n0 + q));
@@ -564,31 +576,35 @@ __device__ __forceinline__ int scale_of(const float* maxima, float (&red)[4]) {
 }
 
 // dz for dX and in two parts for dW, and the sums over a group of rows for dbias. A
-// thread has 8 columns, a workgroup 512 of them and 4 waves of rows.
-template <class D>
+// thread has 8 columns, LC threads a row: whole waves where there are several groups,
+// whose sums k_dbias adds; 8 threads and 32 rows at a time where one group has all rows
+// and its sums are dbias (200 x 2048: one launch of 4 us for two of 4 and 3).
+template <class D, int LC>
 __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
-  __shared__ float red[4][512];
+  constexpr int R = 256 / LC;  // rows at a time
+  constexpr bool kHalf = std::is_same<D, F16>::value;
+  __shared__ float red[R][8 * LC];
   __shared__ float s_max[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 512 + 8 * lane;
+  const int col = 8 * (threadIdx.x % LC), slot = threadIdx.x / LC;
+  const int64_t n = (int64_t)blockIdx.x * (8 * LC) + col;
   float scale = 1.0f;
   if (p.maxima) {
     const int e = scale_of(p.maxima, s_max);
     scale = ldexpf(1.0f, e);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.inv_scale[0] = ldexpf(1.0f, -e);
   }
-  constexpr bool kHalf = std::is_same<D, F16>::value;
   fx8 sum = (fx8)(0.0f);
   if (n < p.N) {
     const int t0 = blockIdx.y * p.rows, t1 = min(p.T, t0 + p.rows);
-    for (int t = t0 + wave; t < t1; t += 4) {
+#pragma unroll 4
+    for (int t = t0 + slot; t < t1; t += R) {
       const size_t at = (size_t)t * p.N + n;
       const fx8 d = dz8<D>(p, at);
       sum += d;
       const fx8 x = d * scale;
-      if (p.dz) *(vec*)((elem*)p.dz + at) = narrow<D>(kHalf ? x : d);
+      if (p.dz && p.dz != p.part1) *(vec*)((elem*)p.dz + at) = narrow<D>(kHalf ? x : d);
       if (p.part1) {
         const hx8 h = narrow<F16>(x);
         *(hx8*)((_Float16*)p.part1 + at) = h;
@@ -598,11 +614,16 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
   }
   if (!p.dbias) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[wave][8 * lane + i] = sum[i];
+  for (int i = 0; i < 8; ++i) red[slot][col + i] = sum[i];
   __syncthreads();
-  for (int c = threadIdx.x; c < 512; c += 256) {
-    const int64_t col = (int64_t)blockIdx.x * 512 + c;
-    if (col < p.N) p.db_part[(size_t)blockIdx.y * p.N + col] = red[0][c] + red[1][c] + red[2][c] + red[3][c];
+  float* to = gridDim.y == 1 ? p.dbias : p.db_part + (size_t)blockIdx.y * p.N;
+  for (int c = threadIdx.x; c < 8 * LC; c += 256) {
+    const int64_t at = (int64_t)blockIdx.x * (8 * LC) + c;
+    if (at >= p.N) break;
+    float s = red[0][c];
+#pragma unroll
+    for (int i = 1; i < R; ++i) s += red[i][c];
+    to[at] = s;
   }
 }
 
@@ -666,8 +687,18 @@ hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partia
 
 template <class D, int KIND>
 hipError_t forward(const LinearProduct& p, float* ws, hipStream_t s) {
-  if (linear_skinny(p.M)) {
-    k_skinny<D, KIND><<<(unsigned)((p.N + 15) / 16), 64 * kSkinnyWaves, 0, s>>>(p);
+  if (linear_skinny(p.M, p.N, p.K)) {
+    const unsigned grid = (unsigned)((p.N + 15) / 16);
+    constexpr int threads = 64 * kSkinnyWaves;
+    switch ((p.M + 15) / 16) {
+      case 1: k_skinny<D, KIND, 1><<<grid, threads, 0, s>>>(p); break;
+      case 2: k_skinny<D, KIND, 2><<<grid, threads, 0, s>>>(p); break;
+      case 3: k_skinny<D, KIND, 3><<<grid, threads, 0, s>>>(p); break;
+      case 4: k_skinny<D, KIND, 4><<<grid, threads, 0, s>>>(p); break;
+      case 5: k_skinny<D, KIND, 5><<<grid, threads, 0, s>>>(p); break;
+      case 6: k_skinny<D, KIND, 6><<<grid, threads, 0, s>>>(p); break;
+      default: k_skinny<D, KIND, 8><<<grid, threads, 0, s>>>(p); break;
+    }
     return hipGetLastError();
   }
   return launch_product<D, false, false, KIND>(p, linear_plan(p.M, p.N, p.K, 1), ws, s);
@@ -684,14 +715,15 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
       k_max<D><<<dim3(kMaxima, p.x16 ? 2 : 1), 256, 0, s>>>(p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    k_dz<D><<<dim3((p.N + 511) / 512, groups), 256, 0, s>>>(p);
+    if (groups == 1) k_dz<D, 8><<<(p.N + 63) / 64, 256, 0, s>>>(p);
+    else k_dz<D, 64><<<dim3((p.N + 511) / 512, groups), 256, 0, s>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (p.x16) {
       k_x16<<<2048, 256, 0, s>>>(p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }
-  if (p.dbias) {
+  if (p.dbias && groups != 1) {
     k_dbias<<<(p.N + 63) / 64, 256, 0, s>>>(p.db_part, groups, p.N, p.dbias);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
@@ -723,8 +755,11 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
 
 // Tiles of 256 x 256 or 192 x 256, one workgroup a CU, or of 128 x 128, two a CU,
 // whichever needs the least time by its rounds over the 256 CUs; small tiles feed the
-// matrix cores from LDS at some three quarters of the rate. With fewer than 512 small tiles the
-// reduction is split until there are about as many, in pieces of at least 8 stages of 32.
+// matrix cores from LDS at some three quarters of the rate. With fewer than 256 small
+// tiles the reduction is split until there are about as many, in pieces of at least 8
+// stages of 32 (72 x 5120 x 4096 19.1 us with 240 workgroups, 22.4 with 440; 500 x 2048 x
+// 2048 20.5 with 256, 26.4 with 512: partial sums and their join cost more than the second workgroup of a CU
+// gives).
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
   LinearPlan q{};
   q.stages = (int)((K + 31) / 32);
@@ -733,7 +768,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   auto rounds = [](int64_t n, int64_t a) { return (n + a - 1) / a; };
   const int64_t c256 = rounds(tiles(256, 256), 256) * 256 * 256, c192 = rounds(tiles(192, 256), 256) * 192 * 256;
-  int64_t splits = 512 / tiles(128, 128);
+  int64_t splits = 256 / tiles(128, 128);
   if (splits > total / 8) splits = total / 8;
   if (splits > 16) splits = 16;
   if (splits < 1) splits = 1;

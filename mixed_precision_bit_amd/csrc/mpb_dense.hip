@@ -64,9 +64,9 @@ struct GradWs {
 GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
   GradWs w{};
   w.formed = act != MPB_ACT_NONE || dy32;
-  // some 1024 workgroups of 512 columns, groups of at least 16 tokens
+  // one group up to 256 tokens, else some 1024 workgroups of 512 columns
   const int64_t cols = (N + 511) / 512;
-  int64_t groups = 1024 / cols;
+  int64_t groups = T <= 256 ? 1 : 1024 / cols;
   if (groups < 1) groups = 1;
   w.rows = (int)((T + groups - 1) / groups);
   if (w.rows < 16) w.rows = 16;
@@ -141,7 +141,7 @@ extern "C" {
 
 size_t moe_linear_workspace_bytes(int T, int Kd, int N) {
   if (!linear_shape(T, Kd, N)) return 0;
-  const size_t b = T == 0 || mpb::linear_skinny(T) ? 0 : partial_bytes(mpb::linear_plan(T, N, Kd, 1), T, N);
+  const size_t b = T == 0 || mpb::linear_skinny(T, N, Kd) ? 0 : partial_bytes(mpb::linear_plan(T, N, Kd, 1), T, N);
   return b < 256 ? 256 : b;
 }
 

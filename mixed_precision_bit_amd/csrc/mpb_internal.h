@@ -394,7 +394,11 @@ struct LinearPlan {
   int rows;                // of a tile of A: 256 or 192 (and 256 columns), 128 (and 128)
 };
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts);
-inline bool linear_skinny(int64_t M) { return M <= 16; }
+// Whether k_skinny takes a product. It reads A again for every 16 columns, 1 / 8 byte a
+// product of A's rows past the first (one row is read once for all lanes), at some 9 TB/s from the caches:
+// up to 4 us of that is less than the join of a split reduction (2048 x 2048: 64
+// tokens 12 us either way, 17 tokens 7.5 against 12.4; 5120 x 4096: 12 tokens 18 either way).
+inline bool linear_skinny(int64_t M, int64_t N, int64_t K) { return M <= 128 && (M - 1) * N * K <= 270000000; }
 hipError_t launch_linear(const LinearProduct& p, bool bf16, float* ws, hipStream_t s);
 
 constexpr int kMaxima = 1024;  // workgroups of a search for the largest value
