@@ -11,11 +11,11 @@
 //
 // A workgroup takes a row. The entries' ids become a bitmap in LDS; one pass over
 // the row keeps the running maximum and sum of exponentials of what is not an
-// entry (so that p_r is a sum of its own, not 1 minus the rest), the entries are
-// gathered by a thread each, and the few sums over them run in fp64. The gradient
-// in the same launch reads the row again, from the Infinity Cache: 256 CUs hold
-// rows of 80 MB at most sizes. Nothing is written twice: the pass over the row leaves the
-// entries out, and each entry's thread writes its own.
+// entry (so that p_r is a sum of its own, not 1 minus the rest). The entries belong to
+// wave 0, four a lane, which forms the teacher's side while the others read; the
+// logarithms are differences of logits, and they and the sums over the entries are fp64.
+// Nothing is written twice: the pass over the row leaves the entries out, and each
+// entry's lane writes its own.
 //
 // Rows may begin at any element: up to 7 elements before the first 16-byte
 // boundary and after the last are taken one by one.
@@ -70,10 +70,21 @@ struct Running {
   }
 };
 
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Over the wave, the same bits in every lane (see wave_all).
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
-  return v;
+  v += dpp<0xb1>(v);
+  v += dpp<0x4e>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
 }
 
 // Where a row lies: h elements before the first 16-byte boundary, nv vectors of 8.
@@ -91,21 +102,39 @@ __device__ __forceinline__ Row row_of(const typename D::elem* s, int V) {
 // vector i has byte i + 1.
 __device__ __forceinline__ int bit_of(const Row& r, int v) { return v - r.h + 8; }
 
+constexpr int kPerLane = kDistillMaxK / 64;  // entries of a lane of wave 0
+
 template <class D, bool LOSS, bool GRAD>
-__global__ __launch_bounds__(1024) void k_distill(DistillParams p) {
+__global__ __launch_bounds__(1024, 8) void k_distill(DistillParams p) {
   typedef typename D::elem elem;
   extern __shared__ uint32_t bits[];
-  __shared__ float red_m[16], red_l[16];
-  __shared__ double red_d[4][4];
+  __shared__ float red_m[16], red_l[16], s_coef, s_mr;
+  // the entries' while the row is read (registers would cost the second workgroup of a CU)
   __shared__ int s_ids[kDistillMaxK];
-  __shared__ double s_q[kDistillMaxK];
+  __shared__ float s_st[kDistillMaxK];
+  __shared__ double s_q[kDistillMaxK], s_lq[kDistillMaxK];
   __shared__ int s_dup;
-  const int tid = threadIdx.x, nt = blockDim.x, wave = tid >> 6, t = blockIdx.x, V = p.V, k = p.k;
+  const int tid = threadIdx.x, nt = blockDim.x, wave = tid >> 6, lane = tid & 63, t = blockIdx.x, V = p.V, k = p.k;
   const elem* S = (const elem*)p.S + (size_t)t * p.ld;
   elem* dS = GRAD ? (elem*)p.dS + (size_t)t * p.ld : nullptr;
   const Row r = row_of<D>(S, V);
   const int tail = r.h + 8 * r.nv;  // first element after the vectors
   const float w = p.weight ? p.weight[t] : 1.0f / (float)p.T;
+  int id[kPerLane];
+  float yt[kPerLane];
+  if (wave == 0) {
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      const int j = lane + 64 * e;
+      id[e] = -1;
+      yt[e] = 0.0f;
+      if (j < k) {
+        id[e] = p.ids[(size_t)t * k + j];
+        yt[e] = p.teacher[(size_t)t * k + j];
+        if ((unsigned)id[e] >= (unsigned)V) id[e] = -1;
+      }
+    }
+  }
 
   if (w == 0.0f) {  // padding: what the row holds is not looked at
     if (LOSS && tid == 0) {
@@ -124,25 +153,75 @@ __global__ __launch_bounds__(1024) void k_distill(DistillParams p) {
   for (int i = tid; i < p.words; i += nt) bits[i] = 0;
   if (tid == 0) s_dup = 0;
   __syncthreads();
-  int id = -1;
-  float st = -FLT_MAX;
-  if (tid < k) {
-    id = p.ids[(size_t)t * k + tid];
-    if ((unsigned)id >= (unsigned)V) id = -1;
-    s_ids[tid] = id;
-    if (id >= 0) {
-      st = (float)S[id];
-      const int b = bit_of(r, id);
+  if (wave == 0) {
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      s_ids[lane + 64 * e] = id[e];
+      if (id[e] < 0) continue;
+      s_st[lane + 64 * e] = (float)S[id[e]];
+      const int b = bit_of(r, id[e]);
       if (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1) s_dup = 1;
     }
   }
   __syncthreads();
   const uint8_t* bytes = (const uint8_t*)bits;
   const float c = kLog2e / p.tau;
+  const double inv_tau = 1.0 / (double)p.tau;
+
+  // the teacher's side, by wave 0: q and log q of every id once (its first entry has the
+  // sum of all of them), their sum and number
+  const bool with_rest = p.t_lse != nullptr;
+  if (wave == 0) {
+    double q[kPerLane], lq[kPerLane], L = with_rest ? (double)p.t_lse[t] : 0.0;
+    if (!with_rest) {  // over the entries themselves
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e)
+        if (id[e] >= 0) top = fmaxf(top, yt[e]);
+      top = mpb::wave_max(top);
+      double sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e)
+        if (id[e] >= 0 && top > -INFINITY) sum += expf((float)(((double)yt[e] - (double)top) * inv_tau));
+      L = (double)top * inv_tau + log(wave_sum(sum));
+    }
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      lq[e] = (double)yt[e] * inv_tau - L;
+      q[e] = id[e] >= 0 && yt[e] != -INFINITY ? (double)expf((float)lq[e]) : 0.0;
+      s_q[lane + 64 * e] = q[e];
+    }
+    if (s_dup) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      bool first[kPerLane];
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) {
+        first[e] = true;
+        if (id[e] < 0) continue;
+        q[e] = 0.0;
+        for (int j = 0; j < k; ++j) {
+          if (s_ids[j] != id[e]) continue;
+          if (j < lane + 64 * e) first[e] = false;
+          q[e] += s_q[j];
+        }
+        lq[e] = log(q[e]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();  // every lane has read the ids and sums
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) {
+        if (!first[e]) s_ids[lane + 64 * e] = -1, q[e] = 0.0;
+        s_q[lane + 64 * e] = q[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) s_lq[lane + 64 * e] = lq[e];
+  }
 
   // the row without its entries
-  Running rest;
   if constexpr (LOSS) {
+    Running rest;
     constexpr int U = 4;  // vectors in flight
     auto take = [&](fx8 x, unsigned skip) {
       if (skip) {
@@ -177,113 +256,82 @@ __global__ __launch_bounds__(1024) void k_distill(DistillParams p) {
     if (tail + tid < V) one(tail + tid);  // fewer than 8 of each
     const float wm = mpb::wave_max(rest.m);
     const float wl = mpb::wave_sum(rest.l * __builtin_amdgcn_exp2f((rest.m - wm) * c));
-    if ((tid & 63) == 0) red_m[wave] = wm, red_l[wave] = wl;
+    if (lane == 0) red_m[wave] = wm, red_l[wave] = wl;
+    __syncthreads();
   }
 
-  // the teacher's probabilities, by the first 4 waves (k entries at most 256)
-  const bool with_rest = p.t_lse != nullptr;
-  double y = 0.0, q = 0.0, L = 0.0;
-  const double inv_tau = 1.0 / (double)p.tau;
-  if (id >= 0) y = (double)p.teacher[(size_t)t * k + tid] * inv_tau;
-  if (with_rest) {
-    L = p.t_lse[t];
-    if (id >= 0) q = exp(y - L);
-  } else {  // over the entries themselves
-    float m = id >= 0 ? (float)y : -INFINITY;
-    if (wave < 4) {
-      m = mpb::wave_max(m);
-      if ((tid & 63) == 0) red_d[0][wave] = m;
+  // the row's sums and results, by wave 0
+  if (wave == 0) {
+    float mr, lr, m, l, st[kPerLane];
+    double q[kPerLane], lq[kPerLane], sq = 0.0;
+    int listed = 0;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      const int j = lane + 64 * e;
+      id[e] = s_ids[j];
+      q[e] = s_q[j];
+      lq[e] = s_lq[j];
+      st[e] = id[e] < 0 ? -FLT_MAX : s_st[j];
+      sq += q[e];
+      listed += __popcll(__ballot(id[e] >= 0));
     }
-    __syncthreads();
-    const int nw = nt >> 6;
-    double top = red_d[0][0];
-    for (int i = 1; i < 4 && i < nw; ++i) top = fmax(top, red_d[0][i]);
-    if (id >= 0 && top > -INFINITY) q = exp(y - top);  // nothing but -inf: no entry counts
-    const double e = wave_sum(q);
-    if (wave < 4 && (tid & 63) == 0) red_d[1][wave] = e;
-    __syncthreads();
-    double sum = 0.0;
-    for (int i = 0; i < 4 && i < nw; ++i) sum += red_d[1][i];
-    if (sum > 0.0) q /= sum;
-  }
-  // entries of one id stand together: the first of them carries the sum
-  if (tid < k) s_q[tid] = q;
-  __syncthreads();
-  bool first = id >= 0;
-  if (s_dup && id >= 0) {
-    q = 0.0;
-    for (int j = 0; j < k; ++j) {
-      if (s_ids[j] != id) continue;
-      if (j < tid) first = false;
-      q += s_q[j];
-    }
-  }
-  if (!first) q = 0.0;
-
-  // the row's sums: all of it, and without its entries
-  float mr, lr, m, l;
-  if constexpr (LOSS) {
-    Running all;
-    for (int i = 0; i < nt >> 6; ++i) all.join(red_m[i], red_l[i], c);
-    mr = all.m;
-    lr = all.l;
-  } else {
-    const fx4 v = *(const fx4*)(p.stats + 4 * (size_t)t);
-    mr = v[0], lr = v[1], m = v[2], l = v[3];
-  }
-  __syncthreads();  // red_d is free again
-  if (wave < 4) {
-    const double sq = wave_sum(q), n = wave_sum(first ? 1.0 : 0.0);
-    const float tm = mpb::wave_max(first ? st : -FLT_MAX);
-    if ((tid & 63) == 0) red_d[0][wave] = sq, red_d[1][wave] = n, red_d[2][wave] = tm;
-  }
-  __syncthreads();
-  double sq = 0.0, listed = 0.0;
-  float tm = -FLT_MAX;
-  for (int i = 0; i < 4 && i < nt >> 6; ++i) sq += red_d[0][i], listed += red_d[1][i], tm = fmaxf(tm, (float)red_d[2][i]);
-  const bool unlisted = listed < (double)V;
-  const double qr = with_rest && unlisted ? fmax(0.0, 1.0 - sq) : 0.0;
-  if constexpr (LOSS) {
-    m = fmaxf(mr, tm);
-    __syncthreads();
-    if (wave < 4) {
-      const double e = wave_sum(first ? exp(((double)st - (double)m) * inv_tau) : 0.0);
-      if ((tid & 63) == 0) red_d[0][wave] = e;
-    }
-    __syncthreads();
-    double sum = (double)lr * exp(((double)mr - (double)m) * inv_tau);
-    for (int i = 0; i < 4 && i < nt >> 6; ++i) sum += red_d[0][i];
-    l = (float)sum;
-    // kl, with log p = (s - m) / tau - log l
-    double kl = 0.0;
-    if (q > 0.0) kl = q * (log(q) - (((double)st - (double)m) * inv_tau - log(sum)));
-    else if (q != q) kl = q;
-    __syncthreads();
-    if (wave < 4) {
+    sq = wave_sum(sq);
+    const double qr = with_rest && listed < V ? fmax(0.0, 1.0 - sq) : 0.0;
+    if constexpr (LOSS) {
+      const bool on = lane < nt >> 6;
+      const float wm = on ? red_m[lane] : -FLT_MAX;
+      mr = mpb::wave_max(wm);
+      lr = mpb::wave_sum(on ? red_l[lane] * __builtin_amdgcn_exp2f((wm - mr) * c) : 0.0f);
+      float tm = -FLT_MAX;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) tm = fmaxf(tm, st[e]);
+      m = fmaxf(mr, mpb::wave_max(tm));
+      double sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e)
+        if (id[e] >= 0) sum += expf((float)(((double)st[e] - (double)m) * inv_tau));
+      sum = wave_sum(sum) + (double)lr * expf((float)(((double)mr - (double)m) * inv_tau));
+      l = (float)sum;
+      // log p = (s - m) / tau - log(sum)
+      const double ls = log(sum);
+      double kl = 0.0;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) {
+        if (q[e] > 0.0) kl += q[e] * (lq[e] - (((double)st[e] - (double)m) * inv_tau - ls));
+        else if (q[e] != q[e]) kl = q[e];
+      }
       kl = wave_sum(kl);
-      if ((tid & 63) == 0) red_d[0][wave] = kl;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      kl = 0.0;
-      for (int i = 0; i < 4 && i < nt >> 6; ++i) kl += red_d[0][i];
-      if (qr > 0.0) kl += qr * (log(qr) - (((double)mr - (double)m) * inv_tau + log((double)lr) - log(sum)));
+      if (qr > 0.0) kl += qr * (log(qr) - (((double)mr - (double)m) * inv_tau + log((double)lr) - ls));
       if (sum == 0.0) kl = 0.0;  // every logit is -inf: the row takes no part
-      p.kl[t] = (float)kl;
-      *(fx4*)(p.stats + 4 * (size_t)t) = fx4{mr, lr, m, l};
+      if (lane == 0) {
+        p.kl[t] = (float)kl;
+        *(fx4*)(p.stats + 4 * (size_t)t) = fx4{mr, lr, m, l};
+      }
+    } else {
+      const fx4 v = *(const fx4*)(p.stats + 4 * (size_t)t);
+      mr = v[0], lr = v[1], m = v[2], l = v[3];
+    }
+    if constexpr (GRAD) {
+      const float scale = l == 0.0f ? 0.0f : w * p.tau * (p.gloss ? *p.gloss : 1.0f);
+      const double Q = sq + qr;
+      // p_v (Q - q_r / p_r) = exp((s - mr) / tau) (Q p_r - q_r) / lr
+      const double pr = (double)lr / (double)l * exp(((double)mr - (double)m) * inv_tau);
+      if (lane == 0) {
+        s_coef = lr == 0.0f ? 0.0f : scale * (float)((Q * pr - qr) / (double)lr);
+        s_mr = mr;
+      }
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) {
+        if (id[e] < 0) continue;
+        const double pv = (double)expf((float)(((double)st[e] - (double)m) * inv_tau)) / (double)l;
+        dS[id[e]] = (elem)(l == 0.0f ? 0.0f : scale * (float)(pv * Q - q[e]));
+      }
     }
   }
 
   if constexpr (GRAD) {
-    const float scale = l == 0.0f ? 0.0f : w * p.tau * (p.gloss ? *p.gloss : 1.0f);
-    const double Q = sq + qr;
-    // p_v (Q - q_r / p_r) = exp((s - mr) / tau) (Q p_r - q_r) / lr
-    const double pr = (double)lr / (double)l * exp(((double)mr - (double)m) * inv_tau);
-    const float coef = lr == 0.0f ? 0.0f : scale * (float)((Q * pr - qr) / (double)lr);
-    if (first) {
-      const double pv = exp(((double)st - (double)m) * inv_tau) / (double)l;
-      dS[id] = (elem)(l == 0.0f ? 0.0f : scale * (float)(pv * Q - q));
-    }
+    __syncthreads();
+    const float coef = s_coef, mr = s_mr;
     auto put = [&](int i, fx8 x) {
       const unsigned skip = bytes[i + 1];
 #pragma unroll
@@ -301,16 +349,17 @@ __global__ __launch_bounds__(1024) void k_distill(DistillParams p) {
       const int b = bit_of(r, v);
       if (!(bits[b >> 5] >> (b & 31) & 1)) dS[v] = (elem)(coef * __builtin_amdgcn_exp2f(((float)S[v] - mr) * c));
     };
+    // backwards: what was read last is nearest
     constexpr int U = 4;
-    int i = tid;
-    for (; i + (U - 1) * nt < r.nv; i += U * nt) {
+    int i = r.nv - 1 - tid;
+    for (; i - (U - 1) * nt >= 0; i -= U * nt) {
       fx8 x[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) x[j] = read8<D>(S + r.h + 8 * (size_t)(i + j * nt));
+      for (int j = 0; j < U; ++j) x[j] = read8<D>(S + r.h + 8 * (size_t)(i - j * nt));
 #pragma unroll
-      for (int j = 0; j < U; ++j) put(i + j * nt, x[j]);
+      for (int j = 0; j < U; ++j) put(i - j * nt, x[j]);
     }
-    for (; i < r.nv; i += nt) put(i, read8<D>(S + r.h + 8 * (size_t)i));
+    for (; i >= 0; i -= nt) put(i, read8<D>(S + r.h + 8 * (size_t)i));
     if (tid < r.h) one(tid);
     if (tail + tid < V) one(tail + tid);
   }
@@ -337,8 +386,12 @@ __global__ __launch_bounds__(1024) void k_distill_sum(DistillParams p) {
 template <class D>
 hipError_t launch(const DistillParams& p, bool loss, hipStream_t s) {
   if (p.T > 0) {
-    // 8 vectors a thread at the longest rows, whole waves, 4 of them at least (256 entries)
-    const int n = (p.V + 63) / 64, nt = n >= 1024 ? 1024 : n <= 256 ? 256 : (n + 63) / 64 * 64;
+    // Up to 512 threads, four rows a CU, which hide each other's ends (1021 x 65536 fp16:
+    // loss 34 us, 44 with 1024); 1024 where there are no four rows for every CU, or where
+    // their second reading would not find them in the 256 MB Infinity Cache (2048 x
+    // 151677 bf16 with the gradient: 304 us with 1024 threads, 347 with 512).
+    const bool wide = p.T <= 512 || (loss && p.dS && (double)p.V * sizeof(typename D::elem) * 1024 > 2e8);
+    const int n = (p.V + 31) / 32, most = wide ? 1024 : 512, nt = n >= most ? most : n <= 256 ? 256 : (n + 63) / 64 * 64;
     const size_t lds = 4 * (size_t)p.words;
     auto* k = loss ? (p.dS ? k_distill<D, true, true> : k_distill<D, true, false>) : k_distill<D, false, true>;
     k<<<p.T, nt, lds, s>>>(p);
