@@ -14,6 +14,9 @@ from . import _lib as M
 
 XDTYPE = {"f16": M.MPB_F16, "bf16": M.MPB_BF16}
 XTORCH = {"f16": torch.float16, "bf16": torch.bfloat16}
+ACT = {"none": M.MPB_ACT_NONE, "relu": M.MPB_ACT_RELU, "silu": M.MPB_ACT_SILU, "gelu": M.MPB_ACT_GELU,
+       "gelu_tanh": M.MPB_ACT_GELU_TANH}
+PAIRS = {"halves": M.MPB_PAIRS_HALVES, "neighbours": M.MPB_PAIRS_NEIGHBOURS}
 
 
 def _dev(a: np.ndarray, device) -> torch.Tensor:
@@ -147,11 +150,11 @@ class DeviceLayer:
         return x
 
     def adapt(self, X, xdtype, adapters, out, stream=None):
-        """Adds every token's adapter to out [T][H] in place. adapters: a dict with A [n][R][H], B [n][H][R],
-        adapter [T], and ranks [n] and scales [n] if they differ from R and 1."""
+        """Adds every token's adapter to out [T][N] in place (N is H for the layer itself). adapters: a dict with A
+        [n][R][Kd], B [n][N][R] for X [T][Kd], adapter [T], and ranks [n] and scales [n] if they differ from R and 1."""
         A = adapters["A"]
         with self._on(stream):
-            ws = torch.empty(M.moe_adapters_workspace_bytes(X.shape[0], self.H, A.shape[0], A.shape[1]),
+            ws = torch.empty(M.moe_adapters_workspace_bytes(X.shape[0], X.shape[1], A.shape[0], A.shape[1]),
                              dtype=torch.uint8, device=self.device)
         M.moe_adapters(X, XDTYPE[xdtype], A, adapters["B"], adapters.get("ranks"), adapters.get("scales"),
                        adapters["adapter"], out, out, ws, stream)
@@ -212,3 +215,86 @@ class DeviceLayer:
         M.moe_router_loss_grad(X, XDTYPE[xdtype], self.W_r, idx, mask, s["logits"], s["lse"], s["counts"], alpha, beta,
                                gw, gloss, dX, dW, db, ws, stream)
         return dX, dW, db
+
+    # ---------------------------------------------------------------- the dense operators beside the layer
+    def project(self, X, xdtype, W, bias=None, act="none", res=None, keep=False, f32=False, adapters=None, stream=None):
+        """res + act(X W^T + bias) for X [T][Kd] and W [N][Kd], of X's type or (f32) fp32. adapters (see adapt) are added
+        to a projection without activation, which is then fp32. keep: returns (y, z), z for project_grad."""
+        T, N = X.shape[0], W.shape[0]
+        if adapters is not None and ACT[act] != M.MPB_ACT_NONE:
+            raise M.MpbError("project", -1, "adapters are added to a projection without activation")
+        with self._on(stream):
+            y = torch.empty((T, N), dtype=torch.float32 if f32 or adapters is not None else XTORCH[xdtype], device=self.device)
+            z = torch.empty((T, N), dtype=XTORCH[xdtype], device=self.device) if keep else None
+            ws = torch.empty(M.moe_linear_workspace_bytes(T, X.shape[1], N), dtype=torch.uint8, device=self.device)
+        M.moe_linear(X, XDTYPE[xdtype], W, bias, ACT[act], res, z, y, ws, stream)
+        if adapters is not None:
+            self.adapt(X, xdtype, adapters, y, stream)
+        return (y, z) if keep else y
+
+    def project_grad(self, X, xdtype, W, dy, act="none", z=None, stream=None):
+        """Gradients of project from dy (X's type or fp32) and, with an activation, z: a dict of X, W and bias."""
+        (T, Kd), N = X.shape, W.shape[0]
+        f32 = dict(dtype=torch.float32, device=self.device)
+        dyt = M.MPB_F32 if dy.dtype is torch.float32 else XDTYPE[xdtype]
+        with self._on(stream):
+            g = {"X": torch.empty((T, Kd), dtype=XTORCH[xdtype], device=self.device), "W": torch.empty((N, Kd), **f32),
+                 "bias": torch.empty(N, **f32)}
+            ws = torch.empty(M.moe_linear_grad_workspace_bytes(T, Kd, N, ACT[act], dyt), dtype=torch.uint8,
+                             device=self.device)
+        M.moe_linear_grad(X, XDTYPE[xdtype], W, ACT[act], z, dy, g["X"], g["W"], g["bias"], ws, stream)
+        return g
+
+    def heads(self, q, k, xdtype, gamma_q=None, gamma_k=None, pos=None, freq=None, axis=None, pairs="halves", eps=1e-6,
+              stream=None):
+        """Norms of the heads q [T][Hq][D] and k [T][Hk][D] (views of a packed projection, k may be None) and their
+        rotation by pos [A][T] (freq [Dr / 2], axis [Dr / 2] with several axes). Returns contiguous q and k."""
+        with self._on(stream):
+            out = [None if t is None else torch.empty(t.shape, dtype=XTORCH[xdtype], device=self.device) for t in (q, k)]
+        M.moe_head_norm(q, k, XDTYPE[xdtype], gamma_q, gamma_k, eps, pos, axis, freq, PAIRS[pairs], *out, stream)
+        return tuple(out)
+
+    def heads_grad(self, q, k, xdtype, dq_out, dk_out, gamma_q=None, gamma_k=None, pos=None, freq=None, axis=None,
+                   pairs="halves", eps=1e-6, stream=None):
+        """Gradients of heads: a dict of q, k, gamma_q and gamma_k (None where there is none)."""
+        T, Hq, D = dq_out.shape
+        Hk = 0 if dk_out is None else dk_out.shape[1]
+        with self._on(stream):
+            g = {n: None if t is None else torch.empty(t.shape, dtype=XTORCH[xdtype], device=self.device)
+                 for n, t in (("q", dq_out), ("k", dk_out))}
+            g |= {n: None if t is None else torch.empty_like(t) for n, t in (("gamma_q", gamma_q), ("gamma_k", gamma_k))}
+            ws = torch.empty(M.moe_head_norm_grad_workspace_bytes(T, Hq, Hk, D), dtype=torch.uint8, device=self.device)
+        M.moe_head_norm_grad(q, k, XDTYPE[xdtype], gamma_q, gamma_k, eps, pos, axis, freq, PAIRS[pairs], dq_out, dk_out,
+                             g["q"], g["k"], g["gamma_q"], g["gamma_k"], ws, stream)
+        return g
+
+    @staticmethod
+    def _like_logits(S):
+        """A tensor with S's shape, row stride and place against a 16-byte boundary; zeros between the rows, so that
+        the logits of a vocabulary padded for project_grad get a gradient of the padded width."""
+        (T, V), ld, at = S.shape, S.stride(0), S.data_ptr() % 16 // S.element_size()
+        if T == 1 and not V <= ld <= 2 * V:  # one row's stride says nothing
+            ld = V
+        buf = torch.empty(T * ld + at, dtype=S.dtype, device=S.device)
+        if ld > V:
+            torch.as_strided(buf, (T, ld - V), (ld, 1), at + V).zero_()
+        return torch.as_strided(buf, (T, V), (ld, 1), at)
+
+    def distill(self, S, ids, teacher, teacher_lse=None, weight=None, tau=1.0, grad=False, gloss=None, stream=None):
+        """Loss of student logits S [T][V] (fp16, bf16 or fp32) against a teacher's top logits [T][k]: a dict of loss
+        [1], kl [T], with grad the gradient dS (with S's row stride, zeros between the rows), and what distill_grad
+        needs. S may be the first V columns of wider logits."""
+        T, f32 = S.shape[0], dict(dtype=torch.float32, device=self.device)
+        sd = {torch.float16: M.MPB_F16, torch.bfloat16: M.MPB_BF16, torch.float32: M.MPB_F32}[S.dtype]
+        with self._on(stream):
+            s = {"stats": torch.empty((T, 4), **f32), "kl": torch.empty(T, **f32), "loss": torch.empty(1, **f32),
+                 "dS": self._like_logits(S) if grad else None, "args": (S, sd, ids, teacher, teacher_lse, weight, tau)}
+        M.moe_distill_loss(*s["args"], s["stats"], s["kl"], s["loss"], s["dS"], gloss, stream)
+        return s
+
+    def distill_grad(self, s, gloss=None, stream=None):
+        """The gradient of distill's loss times gloss, as a pass of its own."""
+        with self._on(stream):
+            dS = self._like_logits(s["args"][0])
+        M.moe_distill_loss_grad(*s["args"], s["stats"], dS, gloss, stream)
+        return dS
