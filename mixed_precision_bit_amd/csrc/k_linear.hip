@@ -17,12 +17,12 @@
 // straight into the registers.
 //
 // dz is formed once for both gradients. Where it is not exactly dy (an activation, or
-// fp32 dy) it is rounded to the activations' type for dX, whose result is rounded to that type
-// anyway. dW, whose result is fp32, takes it as two fp16 parts of 22 bits together
-// (bf16 parts have 16: 2.6e-6 of the result's norm off at 4093 tokens, an fp32 library
-// product 1.2e-6; a third one would cost a third of dW's time again), and bf16 X as
-// fp16 beside it. What becomes fp16 is scaled by a power of two that brings its
-// largest value to 2^13: the gradients of a mean, below fp16's range, keep their bits.
+// fp32 dy) it becomes fp16 parts, whatever the activations are, scaled by a power of two
+// that brings the largest value to 2^13 (the gradients of a mean, below fp16's range,
+// keep their bits): one part of 11 bits for dX, whose result is rounded to 16 bits anyway,
+// two of 22 together for dW, whose result is fp32. bf16 X and W become scaled fp16 beside them.
+// bf16 parts cost the same and lose more: dX 2.3e-3 of its norm off with one instead of
+// 1.7e-3, dW 2.6e-6 with two instead of 7e-7 (an fp32 library product: 1.2e-6; 4093 tokens).
 #include <type_traits>
 
 #include "k_block_common.h"
@@ -106,15 +106,15 @@ __device__ __forceinline__ float act_grad(float z, int act) {
 }
 
 // ---------------------------------------------------------------- epilogue
-// What becomes of a product: a gradient in the activations' type or fp32 (times a
-// scale), or moe_linear's epilogue with y in either.
-enum { kGrad16, kGrad32, kOut16, kOut32 };
+// What becomes of a product: a gradient in the operands' type, in bf16 (of fp16
+// operands) or fp32, times a scale, or moe_linear's epilogue with y of 16 bits or fp32.
+enum { kGrad16, kGradBf, kGrad32, kOut16, kOut32 };
 
 // NV (4 or 8) consecutive columns of a row, as they are loaded from the residual: the
 // load of one group goes out before the group in front of it is stored.
 template <class D, int NV, int KIND>
 struct Residual {
-  typedef typename D::elem elem;
+  typedef typename std::conditional<KIND == kGradBf, BF16, D>::type::elem elem;
   typedef elem evec __attribute__((ext_vector_type(NV)));
   typedef float fvec __attribute__((ext_vector_type(NV)));
   evec narrow_;
@@ -139,8 +139,8 @@ __device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, flo
   fvec w;
 #pragma unroll
   for (int i = 0; i < NV; ++i) w[i] = v[i];
-  constexpr bool kNarrow = KIND == kGrad16 || KIND == kOut16;
-  if constexpr (KIND == kGrad16 || KIND == kGrad32) {
+  constexpr bool kNarrow = KIND != kGrad32 && KIND != kOut32;
+  if constexpr (KIND <= kGrad32) {
     if (o.scale) w *= *o.scale;
     if (o.scale2) w *= *o.scale2;  // one after the other: their product may be out of range
   } else {
@@ -531,15 +531,17 @@ __device__ __forceinline__ fx8 dz8(const LinearGradParams& p, size_t at) {
   return d;
 }
 
-// The largest finite |v| of each workgroup's share: of dy, and in the second half of
-// the grid of X where it is to become fp16.
+// The largest finite |v| of each workgroup's share of dy (blockIdx.y 0), and of X (1)
+// and W (2) where they are to become fp16.
 template <class D>
 __global__ __launch_bounds__(256) void k_max(LinearGradParams p) {
   typedef typename D::vec vec;
   typedef typename D::elem elem;
   __shared__ float red[4];
-  const bool of_x = blockIdx.y == 1;
-  const int64_t n8 = (int64_t)p.T * (of_x ? p.Kd : p.N) / 8;
+  const int of = blockIdx.y;
+  if ((of == 1 && !p.x16) || (of == 2 && !p.w16)) return;
+  const int64_t n8 = (of == 0 ? (int64_t)p.T * p.N : of == 1 ? (int64_t)p.T * p.Kd : (int64_t)p.N * p.Kd) / 8;
+  const elem* src = (const elem*)(of == 0 ? p.dy : of == 1 ? p.X : p.W);
   float m = 0.0f;
   auto take = [&](const fx8& d) {
 #pragma unroll
@@ -549,14 +551,15 @@ __global__ __launch_bounds__(256) void k_max(LinearGradParams p) {
     }
   };
   const int64_t step = (int64_t)gridDim.x * 256;
+#pragma unroll 4
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step) {
-    if (!of_x && p.dy32) take(load8((const float*)p.dy + 8 * i));
-    else take(widen<D>(*(const vec*)((const elem*)(of_x ? p.X : p.dy) + 8 * i)));
+    if (of == 0 && p.dy32) take(load8((const float*)p.dy + 8 * i));
+    else take(widen<D>(*(const vec*)(src + 8 * i)));
   }
   m = wave_max(m);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0) p.maxima[blockIdx.y * kMaxima + blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if (threadIdx.x == 0) p.maxima[of * kMaxima + blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
 
 // The exponent e of the scale that brings the largest of k_max's values into [2^13,
@@ -575,16 +578,13 @@ __device__ __forceinline__ int scale_of(const float* maxima, float (&red)[4]) {
   return min(max(14 - e, -126), 126);
 }
 
-// dz for dX and in two parts for dW, and the sums over a group of rows for dbias. A
+// dz in one or two parts, and the sums over a group of rows for dbias. A
 // thread has 8 columns, LC threads a row: whole waves where there are several groups,
 // whose sums k_dbias adds; 8 threads and 32 rows at a time where one group has all rows
 // and its sums are dbias (200 x 2048: one launch of 4 us for two of 4 and 3).
 template <class D, int LC>
 __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
-  typedef typename D::vec vec;
-  typedef typename D::elem elem;
   constexpr int R = 256 / LC;  // rows at a time
-  constexpr bool kHalf = std::is_same<D, F16>::value;
   __shared__ float red[R][8 * LC];
   __shared__ float s_max[4];
   const int col = 8 * (threadIdx.x % LC), slot = threadIdx.x / LC;
@@ -603,12 +603,11 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
       const size_t at = (size_t)t * p.N + n;
       const fx8 d = dz8<D>(p, at);
       sum += d;
-      const fx8 x = d * scale;
-      if (p.dz && p.dz != p.part1) *(vec*)((elem*)p.dz + at) = narrow<D>(kHalf ? x : d);
       if (p.part1) {
+        const fx8 x = d * scale;
         const hx8 h = narrow<F16>(x);
         *(hx8*)((_Float16*)p.part1 + at) = h;
-        *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
+        if (p.part2) *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
       }
     }
   }
@@ -627,19 +626,21 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
   }
 }
 
-// bf16 X as scaled fp16, and the factor that takes both scales out of dW. A value's 8
-// bits fit unless it is below 2^-30 of the largest.
-__global__ __launch_bounds__(256) void k_x16(LinearGradParams p) {
+// bf16 X (blockIdx.y 0) and W (1) as scaled fp16, and the factor that takes the scale
+// out again. A value's 8 bits fit unless it is below 2^-30 of the largest.
+__global__ __launch_bounds__(256) void k_half(LinearGradParams p) {
   __shared__ float s_max[4];
-  const int ez = scale_of(p.maxima, s_max), ex = scale_of(p.maxima + kMaxima, s_max);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.inv_scale[1] = ldexpf(1.0f, -ex);
-    p.inv_scale[2] = ldexpf(1.0f, -ez);
-  }
-  const float scale = ldexpf(1.0f, ex);
-  const int64_t n8 = (int64_t)p.T * p.Kd / 8, step = (int64_t)gridDim.x * 256;
+  const int of = 1 + blockIdx.y;
+  _Float16* to = (_Float16*)(of == 1 ? p.x16 : p.w16);
+  if (!to) return;
+  const int e = scale_of(p.maxima + of * kMaxima, s_max);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.inv_scale[of] = ldexpf(1.0f, -e);
+  const float scale = ldexpf(1.0f, e);
+  const __bf16* src = (const __bf16*)(of == 1 ? p.X : p.W);
+  const int64_t n8 = (int64_t)(of == 1 ? p.T : p.N) * p.Kd / 8, step = (int64_t)gridDim.x * 256;
+#pragma unroll 4
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step)
-    *(hx8*)((_Float16*)p.x16 + 8 * i) = narrow<F16>(widen<BF16>(*(const bx8*)((const __bf16*)p.X + 8 * i)) * scale);
+    *(hx8*)(to + 8 * i) = narrow<F16>(widen<BF16>(*(const bx8*)(src + 8 * i)) * scale);
 }
 
 // dbias: the groups' sums in their order.
@@ -706,20 +707,19 @@ hipError_t forward(const LinearProduct& p, float* ws, hipStream_t s) {
 
 template <class D>
 hipError_t gradients(LinearGradParams p, hipStream_t s) {
-  constexpr bool kHalf = std::is_same<D, F16>::value;
   hipError_t e = hipSuccess;
-  const bool formed = p.dz || p.part1;
+  const bool formed = p.part1 != nullptr;
   const int groups = (p.T + p.rows - 1) / p.rows;
   if (p.T > 0 && (formed || p.dbias)) {
-    if (p.maxima) {
-      k_max<D><<<dim3(kMaxima, p.x16 ? 2 : 1), 256, 0, s>>>(p);
+    if (formed) {
+      k_max<D><<<dim3(kMaxima, p.w16 ? 3 : p.x16 ? 2 : 1), 256, 0, s>>>(p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (groups == 1) k_dz<D, 8><<<(p.N + 63) / 64, 256, 0, s>>>(p);
     else k_dz<D, 64><<<dim3((p.N + 511) / 512, groups), 256, 0, s>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (p.x16) {
-      k_x16<<<2048, 256, 0, s>>>(p);
+    if (p.x16 || p.w16) {
+      k_half<<<dim3(1024, p.w16 ? 2 : 1), 256, 0, s>>>(p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }
@@ -727,25 +727,33 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
     k_dbias<<<(p.N + 63) / 64, 256, 0, s>>>(p.db_part, groups, p.N, p.dbias);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const bool scaled = p.maxima && p.T > 0;  // the scales are there
+  const bool scaled = formed && p.T > 0;  // the scales are there
+  LinearProduct g{};
+  g.out.N = g.ldb = p.Kd;
+  g.out.scale = scaled ? p.inv_scale : nullptr;
+  g.lda = p.N;
+  g.N = p.Kd;
+  g.A = g.A2 = formed ? p.part1 : p.dy;
   if (p.dX && p.T > 0) {
-    LinearProduct g{};
-    g.A = g.A2 = p.dz ? p.dz : p.dy; g.B = p.W; g.lda = p.N; g.ldb = p.Kd;
-    g.M = p.T; g.N = p.Kd; g.K = p.N;
-    g.out.y = p.dX; g.out.N = p.Kd;
-    g.out.scale = scaled && kHalf ? p.inv_scale : nullptr;
-    if ((e = launch_product<D, false, true, kGrad16>(g, linear_plan(g.M, g.N, g.K, 1), p.partial, s)) != hipSuccess) return e;
+    g.B = p.w16 ? p.w16 : p.W;
+    g.M = p.T; g.K = p.N;
+    g.out.y = p.dX;
+    g.out.scale2 = p.w16 ? p.inv_scale + 2 : nullptr;
+    const LinearPlan plan = linear_plan(g.M, g.N, g.K, 1);
+    // parts are fp16 whatever the activations are
+    if (p.w16) e = launch_product<F16, false, true, kGradBf>(g, plan, p.partial, s);
+    else e = launch_product<D, false, true, kGrad16>(g, plan, p.partial, s);
+    if (e != hipSuccess) return e;
   }
   if (p.dW) {
-    LinearProduct g{};
-    g.A = p.part1 ? p.part1 : p.dy; g.A2 = p.part1 ? p.part2 : p.dy; g.B = p.x16 ? p.x16 : p.X; g.lda = p.N; g.ldb = p.Kd;
-    g.M = p.N; g.N = p.Kd; g.K = p.T;
-    g.out.y = p.dW; g.out.N = p.Kd;
-    g.out.scale = scaled ? p.inv_scale + (p.x16 ? 1 : 0) : nullptr;
-    g.out.scale2 = scaled && p.x16 ? p.inv_scale + 2 : nullptr;
-    const LinearPlan plan = linear_plan(g.M, g.N, g.K, p.part1 ? 2 : 1);
-    // two parts are fp16 whatever the activations are
-    e = p.part1 ? launch_product<F16, true, true, kGrad32>(g, plan, p.partial, s) : launch_product<D, true, true, kGrad32>(g, plan, p.partial, s);
+    if (formed) g.A2 = p.part2;
+    g.B = p.x16 ? p.x16 : p.X;
+    g.M = p.N; g.K = p.T;
+    g.out.y = p.dW;
+    g.out.scale2 = scaled && p.x16 ? p.inv_scale + 1 : nullptr;
+    const LinearPlan plan = linear_plan(g.M, g.N, g.K, formed ? 2 : 1);
+    if (formed) e = launch_product<F16, true, true, kGrad32>(g, plan, p.partial, s);
+    else e = launch_product<D, true, true, kGrad32>(g, plan, p.partial, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -54,10 +54,10 @@ size_t partial_bytes(const mpb::LinearPlan& p, int64_t M, int64_t N) {
   return p.splits > 1 ? up((size_t)p.splits * M * N * sizeof(float)) : 0;
 }
 
-// Regions of moe_linear_grad's workspace. dz is formed where it is not dy itself: as
-// activations for dX, and for dW as two fp16 parts, of which fp16 shares the first.
+// Regions of moe_linear_grad's workspace. dz is formed where it is not dy itself, as
+// fp16 parts, and bf16 X and W become fp16 beside them.
 struct GradWs {
-  size_t dz, part1, part2, x16, maxima, inv_scale, db_part, partial, total;
+  size_t part1, part2, x16, w16, maxima, inv_scale, db_part, partial, total;
   int rows;
   bool formed;
 };
@@ -77,11 +77,11 @@ GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
     return o;
   };
   const size_t part = (size_t)T * N * 2;
-  w.dz = take(w.formed ? part : 0);
-  w.part1 = bf16 ? take(w.formed ? part : 0) : w.dz;
+  w.part1 = take(w.formed ? part : 0);
   w.part2 = take(w.formed ? part : 0);
   w.x16 = take(w.formed && bf16 ? (size_t)T * Kd * 2 : 0);
-  w.maxima = take(2 * mpb::kMaxima * sizeof(float));
+  w.w16 = take(w.formed && bf16 && T > 0 ? (size_t)N * Kd * 2 : 0);
+  w.maxima = take(3 * mpb::kMaxima * sizeof(float));
   w.inv_scale = take(3 * sizeof(float));
   w.db_part = take((size_t)((T + w.rows - 1) / w.rows) * N * sizeof(float));
   const size_t px = T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, 1), T, Kd) : 0;
@@ -195,12 +195,12 @@ int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, 
   mpb::LinearGradParams p{};
   p.X = X_dev; p.W = W_dev; p.z = z_dev; p.dy = dy_dev;
   p.dX = dX_dev; p.dW = dW_dev; p.dbias = dbias_dev;
-  const bool parts = w.formed && dW_dev;
-  p.dz = w.formed && dX_dev ? ws + w.dz : nullptr;
+  const bool parts = w.formed && (dX_dev || dW_dev);
   p.part1 = parts ? ws + w.part1 : nullptr;
-  p.part2 = parts ? ws + w.part2 : nullptr;
-  p.x16 = parts && bf16 ? ws + w.x16 : nullptr;
-  p.maxima = parts || (p.dz && !bf16) ? (float*)(ws + w.maxima) : nullptr;
+  p.part2 = parts && dW_dev ? ws + w.part2 : nullptr;
+  p.x16 = parts && bf16 && dW_dev ? ws + w.x16 : nullptr;
+  p.w16 = parts && bf16 && dX_dev ? ws + w.w16 : nullptr;
+  p.maxima = (float*)(ws + w.maxima);
   p.inv_scale = (float*)(ws + w.inv_scale);
   p.db_part = (float*)(ws + w.db_part);
   p.partial = (float*)(ws + w.partial);

@@ -410,13 +410,13 @@ struct LinearGradParams {
   void* dX;                // [T][Kd] or null
   float* dW;               // [N][Kd] or null
   float* dbias;            // [N] or null
-  // workspace; the first three are null where dz is dy, or no product needs them
-  void* dz;                // [T][N] dz as activations (fp16: scaled)
-  void* part1;             // [T][N] dz as scaled fp16 (fp16: the same buffer as dz)
-  void* part2;             // [T][N] what its rounding left
-  void* x16;               // [T][Kd] bf16 X as scaled fp16 (with part1), or null
-  float* maxima;           // [2][kMaxima] of |dy| and |X|, or null (nothing is scaled)
-  float* inv_scale;        // [3] of dz; of X and of dz (with x16)
+  // workspace; the parts are null where dz is dy, or no product needs them
+  void* part1;             // [T][N] dz as scaled fp16
+  void* part2;             // [T][N] what its rounding left (with dW)
+  void* x16;               // [T][Kd] bf16 X as scaled fp16 (with dW), or null
+  void* w16;               // [N][Kd] bf16 W as scaled fp16 (with dX), or null
+  float* maxima;           // [3][kMaxima] of |dy|, |X| and |W|
+  float* inv_scale;        // [3] of dz, X and W
   float* db_part;          // [groups][N]
   float* partial;
   int T, Kd, N, act, dy32;

@@ -8,8 +8,9 @@ terms' absolute sum. An activation has slope at most 1.13 and is itself within
 8 u |z| + 16 u |y|: its sigmoid within 6 u, the argument of erfc or of the sigmoid
 within 8 u of itself, which changes x f(x) by at most |z| max|x f'(x)| 8 u < 4 u |z|.
 Its derivative, a sum of two such terms, is within 32 u (1 + |z|). A value rounded to
-a 16-bit type is off by eps / 2 of itself and half the smallest step; dz in two fp16 parts
-by 2^-22 of itself and 2^-38 of the largest |dy|, bf16 X beside them by 2^-38 of its largest."""
+a 16-bit type is off by eps / 2 of itself and half the smallest step; dz in one fp16 part by
+2^-11 of itself, in two by 2^-22, and by 2^-38 of the largest |dy|, bf16 X and W beside them
+by 2^-38 of their largest."""
 import math
 
 import pytest
@@ -191,14 +192,13 @@ def check_grad(d, dt, dy, act, out):
     own = dy.double().abs() * 32 * U * (1 + z.abs()) if act != "none" else torch.zeros_like(dz)  # dz's own error
     own = own + U * dz.abs()
     formed = act != "none" or dy.dtype is torch.float32
-    eps = torch.finfo(DT[dt]).eps / 2
     floor = 2.0 ** -38 * dy.double().abs().max() if formed and T else 0.0
-    hi = own + (1.01 * eps * dz.abs() + floor if formed else 0)
+    hi = own + (1.01 * 2.0 ** -11 * dz.abs() + floor if formed else 0)
     both = own + (1.01 * 2.0 ** -22 * dz.abs() + floor if formed else 0)
-    x_off = 2.0 ** -38 * X.abs().max() if formed and dt == "bf16" and T else 0.0
+    x_off, w_off = (2.0 ** -38 * v.abs().max() if formed and dt == "bf16" and T else 0.0 for v in (X, W))
     if out["dX"] is not None:
         ref = dz @ W
-        tol = (hi + E(N) * dz.abs()) @ W.abs()
+        tol = (hi + E(N) * dz.abs()) @ W.abs() + w_off * dz.abs().sum(1)[:, None]
         check(out["dX"], ref, tol + 1.01 * half_step(DT[dt], ref.abs() + tol), "dX")
     if out["dW"] is not None:
         check(out["dW"], dz.t() @ X, (both + E(2 * T) * dz.abs()).t() @ X.abs() + x_off * dz.abs().sum(0)[:, None] + 1e-44, "dW")
