@@ -116,7 +116,7 @@ template <class D, int NV, int KIND>
 struct Residual {
   typedef typename std::conditional<KIND == kGradBf, BF16, D>::type::elem elem;
   typedef elem evec __attribute__((ext_vector_type(NV)));
-  typedef float fvec __attribute__((ext_vector_type(NV)));
+  typedef float fvec __attribute__((ext_vector_type(NV), aligned(16)));  // rows are 16-byte aligned
   evec narrow_;
   fvec wide_;
   __device__ __forceinline__ void load(const LinearOut& o, int64_t m, int n) {

@@ -221,6 +221,29 @@ def test_gradients(T, Hq, Hk, D, Dr, pairs, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("side", ["gq", "gk"])
+def test_gradients_with_a_norm_on_one_side(side):
+    d = inputs(70, 5, 3, 96, 64, "bf16", A=2, seed=4)
+    d[side] = None
+    out = run_grad(d, "bf16")
+    check_grad(d, "bf16", out)
+    assert out[side] is None
+
+
+@pytest.mark.gpu
+def test_many_heads_and_raw_bits():
+    """1024 query heads, and activations handed over as int16 bits."""
+    M = lib_m()
+    d = inputs(3, 1024, 1, 32, 32, "f16", seed=5)
+    want = run_fwd(d, "f16")
+    check_fwd(d, "f16", *want)
+    check_grad(d, "f16", run_grad(d, "f16"))
+    q, k = torch.zeros(3, 1024, 32, dtype=torch.int16, device="cuda"), torch.zeros(3, 1, 32, dtype=torch.int16, device="cuda")
+    M.moe_head_norm(d["q"].view(torch.int16), d["k"].view(torch.int16), M.MPB_F16, d["gq"], d["gk"], EPS, *rot(d), q, k)
+    assert torch.equal(q.view(torch.float16), want[0]) and torch.equal(k.view(torch.float16), want[1])
+
+
+@pytest.mark.gpu
 def test_gradients_are_those_of_differences():
     d = inputs(3, 2, 1, 32, 16, "bf16", seed=2)
     out, h = run_grad(d, "bf16"), 2.0 ** -12

@@ -285,6 +285,48 @@ def test_gradients_are_those_of_differences():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_operands_of_many_magnitudes(dt):
+    """Rows of X, W and dy spread over orders of magnitude: the scales of the fp16 parts follow the largest."""
+    d = inputs(200, 256, 264, dt, seed=9)
+    spread = lambda n: 10.0 ** torch.linspace(-3, 2 if dt == "f16" else 8, n, device="cuda")[torch.randperm(n, device="cuda")]  # noqa: E731
+    d["X"] *= spread(200)[:, None]
+    d["W"] *= spread(264)[:, None]
+    dy = gradient_of(200, 264, "f32", d["g"], 1.0) * spread(200)[:, None]
+    if dt == "f16":
+        dy *= 2.0 ** -12  # dX stays in range
+    for act in ("none", "silu"):
+        check_grad(d, dt, dy, act, run_grad(d, dt, dy, act))
+
+
+@pytest.mark.gpu
+def test_infinite_gradients_reach_what_they_touch_and_no_more():
+    d = inputs(150, 128, 264, "bf16", seed=10)
+    dy = gradient_of(150, 264, "bf16", d["g"])
+    clean = run_grad(d, "bf16", dy, "silu")
+    dy = dy.clone()
+    dy[7, 9] = float("inf")
+    d["z"][7, 9] = 1.0
+    out = run_grad(d, "bf16", dy, "silu")
+    rows = [t for t in range(150) if t != 7]
+    assert not out["dX"][7].isfinite().any() and out["dX"][rows].isfinite().all()
+    assert not out["dW"][9].isfinite().any() and out["db"][9] == float("inf")
+    cols = [c for c in range(264) if c != 9]
+    assert torch.equal(out["dW"][cols], clean["dW"][cols]) and torch.equal(out["dX"][rows], clean["dX"][rows])
+
+
+@pytest.mark.gpu
+def test_raw_bits():
+    M = lib_m()
+    d = inputs(20, 128, 72, "bf16", seed=11)
+    want = run_fwd(d, "bf16", "bf16", "gelu")
+    i = torch.int16
+    y, z = torch.zeros(20, 72, dtype=i, device="cuda"), torch.zeros(20, 72, dtype=i, device="cuda")
+    M.moe_linear(d["X"].view(i), M.MPB_BF16, d["W"].view(i), d["b"], M.MPB_ACT_GELU, None, z, y, torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(y.view(torch.bfloat16), want[0]) and torch.equal(z.view(torch.bfloat16), want[1])
+
+
+@pytest.mark.gpu
 def test_empty_batches():
     M = lib_m()
     d = inputs(0, 128, 72, "f16")
