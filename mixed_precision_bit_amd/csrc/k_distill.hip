@@ -370,10 +370,9 @@ __global__ __launch_bounds__(1024) void k_distill_sum(DistillParams p) {
   __shared__ double red[16];
   const int tid = threadIdx.x;
   double s = 0.0;
-  for (int t = tid; t < p.T; t += 1024) {
-    const float w = p.weight ? p.weight[t] : 1.0f / (float)p.T;
-    if (w != 0.0f) s += (double)w * (double)p.kl[t];
-  }
+#pragma unroll 4
+  for (int t = tid; t < p.T; t += 1024)  // kl is 0 where the weight is
+    s += (double)(p.weight ? p.weight[t] : 1.0f / (float)p.T) * (double)p.kl[t];
   s = wave_sum(s);
   if ((tid & 63) == 0) red[tid >> 6] = s;
   __syncthreads();

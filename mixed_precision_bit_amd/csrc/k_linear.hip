@@ -235,8 +235,9 @@ __device__ __forceinline__ int unit(int b, int n) {
   return x * q + min(x, r) + (b >> 3);
 }
 
+// The share of workgroup `block` of `blocks` in product p.
 template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT, int KIND>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearProduct p) {
+__device__ __forceinline__ void product_tile(const LinearProduct& p, int block, int blocks, char* smem) {
   typedef typename D::vec vec;
   constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, MF = WM / 16, NF = WN / 16;
   constexpr int kStages = 5;  // buffers
@@ -245,9 +246,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
   // columns of one row of C. Turned operands come in 16 consecutive columns.
   constexpr int SHB = NF == 4 ? 4 : 3;
   static_assert(NF == 4 || NF == 2, "");
-  extern __shared__ __align__(16) char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int id = unit(blockIdx.x, gridDim.x), tiles = p.tm * p.tn;
+  const int id = unit(block, blocks), tiles = p.tm * p.tn;
   const int split = id / tiles, tile = id - split * tiles;
   const int grp = tile / (8 * p.tn), rest = tile - grp * 8 * p.tn, gm = min(8, p.tm - 8 * grp);
   const int64_t m0 = (int64_t)(8 * grp + rest % gm) * BM;
@@ -419,6 +419,22 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
       finish<D, NV, KIND>(p.out, m + 16 * i, (int)column(k), v, res[i & 1][k]);
     }
   }
+}
+
+template <class D, int BM, int BN, int WM, int WN, bool AT, bool BT, int KIND>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearProduct p) {
+  extern __shared__ __align__(16) char smem[];
+  product_tile<D, BM, BN, WM, WN, AT, BT, KIND>(p, blockIdx.x, gridDim.x, smem);
+}
+
+// dX and dW in one launch, where both have small tiles: neither fills the chip alone
+// (200 x 2048 x 2048: TODO).
+template <class D, int KIND>
+__global__ __launch_bounds__(256) void k_gradients(LinearProduct x, LinearProduct w, int blocks_x) {
+  extern __shared__ __align__(16) char smem[];
+  const int b = blockIdx.x;
+  if (b < blocks_x) product_tile<D, 128, 128, 64, 64, false, true, KIND>(x, b, blocks_x, smem);
+  else product_tile<D, 128, 128, 64, 64, true, true, kGrad32>(w, b - blocks_x, gridDim.x - blocks_x, smem);
 }
 
 // Adds the partial sums of a split reduction in their order, 8 columns a thread.
@@ -668,8 +684,8 @@ hipError_t launch_tiles(LinearProduct& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class D, bool AT, bool BT, int KIND>
-hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partial, hipStream_t s) {
+// p with the plan's launch shape; a split reduction's sums go to `partial`.
+void set_plan(LinearProduct& p, const LinearPlan& plan, float* partial) {
   p.tm = plan.tm;
   p.tn = plan.tn;
   p.per = plan.per;
@@ -677,13 +693,43 @@ hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partia
   p.stages = plan.stages;
   p.parts = plan.parts;
   p.partial = plan.splits > 1 ? partial : nullptr;
+}
+
+template <class D, int KIND>
+hipError_t join(const LinearProduct& p, hipStream_t s) {
+  if (p.splits == 1) return hipSuccess;
+  const int64_t n = p.M * (p.N / 8);
+  k_join<D, KIND><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, p.splits);
+  return hipGetLastError();
+}
+
+template <class D, bool AT, bool BT, int KIND>
+hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partial, hipStream_t s) {
+  set_plan(p, plan, partial);
   const hipError_t e = plan.rows == 256   ? launch_tiles<D, 256, 256, 128, 64, AT, BT, KIND>(p, s)
                        : plan.rows == 192 ? launch_tiles<D, 192, 256, 96, 64, AT, BT, KIND>(p, s)
                                           : launch_tiles<D, 128, 128, 64, 64, AT, BT, KIND>(p, s);
-  if (e != hipSuccess || plan.splits == 1) return e;
-  const int64_t n = p.M * (p.N / 8);
-  k_join<D, KIND><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.splits);
-  return hipGetLastError();
+  return e != hipSuccess ? e : join<D, KIND>(p, s);
+}
+
+// dX and dW, in one launch where both have small tiles.
+template <class D, int KIND>
+hipError_t launch_gradients(LinearProduct x, const LinearPlan& px, LinearProduct w, const LinearPlan& pw, float* partial_x,
+                            float* partial_w, hipStream_t s) {
+  if (px.rows != 128 || pw.rows != 128) {
+    const hipError_t e = launch_product<D, false, true, KIND>(x, px, partial_x, s);
+    return e != hipSuccess ? e : launch_product<D, true, true, kGrad32>(w, pw, partial_w, s);
+  }
+  set_plan(x, px, partial_x);
+  set_plan(w, pw, partial_w);
+  static unsigned long long raised = 0;
+  constexpr int lds = 5 * 64 * 256;
+  hipError_t e = raise_lds_limit((const void*)&k_gradients<D, KIND>, lds, raised);
+  if (e != hipSuccess) return e;
+  const int bx = x.tm * x.tn * x.splits, bw = w.tm * w.tn * w.splits;
+  k_gradients<D, KIND><<<bx + bw, 256, lds, s>>>(x, w, bx);
+  if ((e = hipGetLastError()) != hipSuccess || (e = join<D, KIND>(x, s)) != hipSuccess) return e;
+  return join<D, kGrad32>(w, s);
 }
 
 template <class D, int KIND>
@@ -734,28 +780,26 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
   g.lda = p.N;
   g.N = p.Kd;
   g.A = g.A2 = formed ? p.part1 : p.dy;
-  if (p.dX && p.T > 0) {
-    g.B = p.w16 ? p.w16 : p.W;
-    g.M = p.T; g.K = p.N;
-    g.out.y = p.dX;
-    g.out.scale2 = p.w16 ? p.inv_scale + 2 : nullptr;
-    const LinearPlan plan = linear_plan(g.M, g.N, g.K, 1);
-    // parts are fp16 whatever the activations are
-    if (p.w16) e = launch_product<F16, false, true, kGradBf>(g, plan, p.partial, s);
-    else e = launch_product<D, false, true, kGrad16>(g, plan, p.partial, s);
-    if (e != hipSuccess) return e;
+  LinearProduct x = g, w = g;
+  x.B = p.w16 ? p.w16 : p.W;
+  x.M = p.T; x.K = p.N;
+  x.out.y = p.dX;
+  x.out.scale2 = p.w16 ? p.inv_scale + 2 : nullptr;
+  if (formed) w.A2 = p.part2;
+  w.B = p.x16 ? p.x16 : p.X;
+  w.M = p.N; w.K = p.T;
+  w.out.y = p.dW;
+  w.out.scale2 = scaled && p.x16 ? p.inv_scale + 1 : nullptr;
+  const LinearPlan pw = linear_plan(w.M, w.N, w.K, formed ? 2 : 1);
+  const bool dx = p.dX && p.T > 0;
+  const LinearPlan px = dx ? linear_plan(x.M, x.N, x.K, 1) : pw;
+  // parts are fp16 whatever the activations are
+  if (dx && p.dW) {
+    if (p.w16) return launch_gradients<F16, kGradBf>(x, px, w, pw, p.partial_x, p.partial_w, s);
+    return launch_gradients<D, kGrad16>(x, px, w, pw, p.partial_x, p.partial_w, s);
   }
-  if (p.dW) {
-    if (formed) g.A2 = p.part2;
-    g.B = p.x16 ? p.x16 : p.X;
-    g.M = p.N; g.K = p.T;
-    g.out.y = p.dW;
-    g.out.scale2 = scaled && p.x16 ? p.inv_scale + 1 : nullptr;
-    const LinearPlan plan = linear_plan(g.M, g.N, g.K, formed ? 2 : 1);
-    if (formed) e = launch_product<F16, true, true, kGrad32>(g, plan, p.partial, s);
-    else e = launch_product<D, true, true, kGrad32>(g, plan, p.partial, s);
-    if (e != hipSuccess) return e;
-  }
+  if (dx) return p.w16 ? launch_product<F16, false, true, kGradBf>(x, px, p.partial_x, s) : launch_product<D, false, true, kGrad16>(x, px, p.partial_x, s);
+  if (p.dW) return formed ? launch_product<F16, true, true, kGrad32>(w, pw, p.partial_w, s) : launch_product<D, true, true, kGrad32>(w, pw, p.partial_w, s);
   return hipSuccess;
 }
 
@@ -773,7 +817,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int parts) {
   q.stages = (int)((K + 31) / 32);
   q.parts = parts;
   const int64_t total = (int64_t)q.stages * parts;
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };  // M and N are positive
   auto rounds = [](int64_t n, int64_t a) { return (n + a - 1) / a; };
   const int64_t c256 = rounds(tiles(256, 256), 256) * 256 * 256, c192 = rounds(tiles(192, 256), 256) * 192 * 256;
   int64_t splits = 256 / tiles(128, 128);

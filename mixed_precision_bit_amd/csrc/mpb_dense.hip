@@ -57,7 +57,7 @@ size_t partial_bytes(const mpb::LinearPlan& p, int64_t M, int64_t N) {
 // Regions of moe_linear_grad's workspace. dz is formed where it is not dy itself, as
 // fp16 parts, and bf16 X and W become fp16 beside them.
 struct GradWs {
-  size_t part1, part2, x16, w16, maxima, inv_scale, db_part, partial, total;
+  size_t part1, part2, x16, w16, maxima, inv_scale, db_part, partial_x, partial_w, total;
   int rows;
   bool formed;
 };
@@ -84,9 +84,8 @@ GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
   w.maxima = take(3 * mpb::kMaxima * sizeof(float));
   w.inv_scale = take(3 * sizeof(float));
   w.db_part = take((size_t)((T + w.rows - 1) / w.rows) * N * sizeof(float));
-  const size_t px = T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, 1), T, Kd) : 0;
-  const size_t pw = partial_bytes(mpb::linear_plan(N, Kd, T, w.formed ? 2 : 1), N, Kd);
-  w.partial = take(px > pw ? px : pw);
+  w.partial_x = take(T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, 1), T, Kd) : 0);
+  w.partial_w = take(partial_bytes(mpb::linear_plan(N, Kd, T, w.formed ? 2 : 1), N, Kd));
   w.total = at;
   return w;
 }
@@ -203,7 +202,8 @@ int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, 
   p.maxima = (float*)(ws + w.maxima);
   p.inv_scale = (float*)(ws + w.inv_scale);
   p.db_part = (float*)(ws + w.db_part);
-  p.partial = (float*)(ws + w.partial);
+  p.partial_x = (float*)(ws + w.partial_x);
+  p.partial_w = (float*)(ws + w.partial_w);
   p.T = T; p.Kd = Kd; p.N = N; p.act = act; p.dy32 = dy_dtype == MPB_F32;
   p.rows = w.rows;
   const hipError_t e = mpb::launch_linear_grad(p, bf16, (hipStream_t)stream);

@@ -418,7 +418,8 @@ struct LinearGradParams {
   float* maxima;           // [3][kMaxima] of |dy|, |X| and |W|
   float* inv_scale;        // [3] of dz, X and W
   float* db_part;          // [groups][N]
-  float* partial;
+  float* partial_x;        // of dX's and dW's split reductions
+  float* partial_w;
   int T, Kd, N, act, dy32;
   int rows;                // tokens of a group of k_dz
 };
