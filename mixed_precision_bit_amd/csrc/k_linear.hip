@@ -427,14 +427,144 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
   product_tile<D, BM, BN, WM, WN, AT, BT, KIND>(p, blockIdx.x, gridDim.x, smem);
 }
 
-// dX and dW in one launch, where both have small tiles: neither fills the chip alone
-// (200 x 2048 x 2048: TODO).
+// ---------------------------------------------------------------- dz
+// dy act'(z) of 8 consecutive elements.
+template <class D>
+__device__ __forceinline__ fx8 dz8(const LinearGradParams& p, size_t at) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
+  fx8 d = p.dy32 ? load8((const float*)p.dy + at) : widen<D>(*(const vec*)((const elem*)p.dy + at));
+  if (p.act != MPB_ACT_NONE) {
+    const fx8 z = widen<D>(*(const vec*)((const elem*)p.z + at));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] *= act_grad(z[i], p.act);
+  }
+  return d;
+}
+
+// The largest finite |v| of each workgroup's share of dy (blockIdx.y 0), and of X (1)
+// and W (2) where they are to become fp16.
+template <class D>
+__global__ __launch_bounds__(256) void k_max(LinearGradParams p) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
+  __shared__ float red[4];
+  const int of = blockIdx.y;
+  if ((of == 1 && !p.x16) || (of == 2 && !p.w16)) return;
+  const int64_t n8 = (of == 0 ? (int64_t)p.T * p.N : of == 1 ? (int64_t)p.T * p.Kd : (int64_t)p.N * p.Kd) / 8;
+  const elem* src = (const elem*)(of == 0 ? p.dy : of == 1 ? p.X : p.W);
+  float m = 0.0f;
+  auto take = [&](const fx8& d) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(d[j]);
+      if (a < INFINITY) m = fmaxf(m, a);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * 256;
+#pragma unroll 4
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step) {
+    if (of == 0 && p.dy32) take(load8((const float*)p.dy + 8 * i));
+    else take(widen<D>(*(const vec*)(src + 8 * i)));
+  }
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) p.maxima[of * kMaxima + blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+// The exponent e of the scale that brings the largest of k_max's values into [2^13,
+// 2^14): an activation's slope of up to 1.13 and the rounding to fp16 stay in range.
+__device__ __forceinline__ int scale_of(const float* maxima, float (&red)[4]) {
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < kMaxima; i += 256) m = fmaxf(m, maxima[i]);
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  __syncthreads();
+  if (m == 0.0f) return 0;
+  int e = 0;
+  (void)frexpf(m, &e);  // m = f 2^e, f in [1/2, 1)
+  return min(max(14 - e, -126), 126);
+}
+
+// dz in one or two parts, and the sums over a group of rows for dbias. A
+// thread has 8 columns, LC threads a row: whole waves where there are several groups,
+// whose sums k_dbias adds; 4 threads and 64 rows at a time where one group has all rows
+// and its sums are dbias.
+template <class D, int LC>
+__device__ __forceinline__ void dz_rows(const LinearGradParams& p, int bx, int by, int groups, float* smem) {
+  constexpr int R = 256 / LC;  // rows at a time
+  float(*red)[8 * LC] = (float(*)[8 * LC])smem;  // [R]
+  const int col = 8 * (threadIdx.x % LC), slot = threadIdx.x / LC;
+  const int64_t n = (int64_t)bx * (8 * LC) + col;
+  float scale = 1.0f;
+  if (p.part1) {
+    const int e = scale_of(p.maxima, *(float(*)[4])smem);
+    scale = ldexpf(1.0f, e);
+    if (bx == 0 && by == 0 && threadIdx.x == 0) p.inv_scale[0] = ldexpf(1.0f, -e);
+  }
+  fx8 sum = (fx8)(0.0f);
+  if (n < p.N) {
+    const int t0 = by * p.rows, t1 = min(p.T, t0 + p.rows);
+#pragma unroll 4
+    for (int t = t0 + slot; t < t1; t += R) {
+      const size_t at = (size_t)t * p.N + n;
+      const fx8 d = dz8<D>(p, at);
+      sum += d;
+      if (p.part1) {
+        const fx8 x = d * scale;
+        const hx8 h = narrow<F16>(x);
+        *(hx8*)((_Float16*)p.part1 + at) = h;
+        if (p.part2) *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
+      }
+    }
+  }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[slot][col + i] = sum[i];
+  __syncthreads();
+  float* to = groups == 1 ? p.dbias : p.db_part + (size_t)by * p.N;
+  if constexpr (LC < 64) {  // 8 threads a column, then those 8
+    const int c = threadIdx.x & 31, part = threadIdx.x >> 5;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) s += red[part * (R / 8) + i][c];
+    __syncthreads();
+    red[part][c] = s;
+    __syncthreads();
+    const int64_t at = (int64_t)bx * 32 + c;
+    if (part == 0 && at < p.N) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) s += red[i][c];
+      to[at] = s;
+    }
+  } else {
+    for (int c = threadIdx.x; c < 512; c += 256) {
+      const int64_t at = (int64_t)bx * 512 + c;
+      if (at < p.N) to[at] = red[0][c] + red[1][c] + red[2][c] + red[3][c];
+    }
+  }
+}
+
+template <class D, int LC>
+__global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
+  __shared__ __align__(16) float smem[2048];
+  dz_rows<D, LC>(p, blockIdx.x, blockIdx.y, gridDim.y, smem);
+}
+
+// dX and dW in one launch, where both have small tiles and neither fills the chip
+// alone, and dbias of a few tokens (blocks_b workgroups): 200 x 2048 x 2048 with its
+// join 24 us, in a launch each 36.
 template <class D, int KIND>
-__global__ __launch_bounds__(256) void k_gradients(LinearProduct x, LinearProduct w, int blocks_x) {
+__global__ __launch_bounds__(256) void k_gradients(LinearProduct x, LinearProduct w, LinearGradParams p, int blocks_x,
+                                                   int blocks_b) {
   extern __shared__ __align__(16) char smem[];
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, bw = gridDim.x - blocks_x - blocks_b;
   if (b < blocks_x) product_tile<D, 128, 128, 64, 64, false, true, KIND>(x, b, blocks_x, smem);
-  else product_tile<D, 128, 128, 64, 64, true, true, kGrad32>(w, b - blocks_x, gridDim.x - blocks_x, smem);
+  else if (b < blocks_x + bw) product_tile<D, 128, 128, 64, 64, true, true, kGrad32>(w, b - blocks_x, bw, smem);
+  else dz_rows<D, 4>(p, b - blocks_x - bw, 0, 1, (float*)smem);
 }
 
 // Adds the partial sums of a split reduction in their order, 8 columns a thread.
@@ -532,116 +662,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
   }
 }
 
-// ---------------------------------------------------------------- dz
-// dy act'(z) of 8 consecutive elements.
-template <class D>
-__device__ __forceinline__ fx8 dz8(const LinearGradParams& p, size_t at) {
-  typedef typename D::vec vec;
-  typedef typename D::elem elem;
-  fx8 d = p.dy32 ? load8((const float*)p.dy + at) : widen<D>(*(const vec*)((const elem*)p.dy + at));
-  if (p.act != MPB_ACT_NONE) {
-    const fx8 z = widen<D>(*(const vec*)((const elem*)p.z + at));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] *= act_grad(z[i], p.act);
-  }
-  return d;
-}
-
-// The largest finite |v| of each workgroup's share of dy (blockIdx.y 0), and of X (1)
-// and W (2) where they are to become fp16.
-template <class D>
-__global__ __launch_bounds__(256) void k_max(LinearGradParams p) {
-  typedef typename D::vec vec;
-  typedef typename D::elem elem;
-  __shared__ float red[4];
-  const int of = blockIdx.y;
-  if ((of == 1 && !p.x16) || (of == 2 && !p.w16)) return;
-  const int64_t n8 = (of == 0 ? (int64_t)p.T * p.N : of == 1 ? (int64_t)p.T * p.Kd : (int64_t)p.N * p.Kd) / 8;
-  const elem* src = (const elem*)(of == 0 ? p.dy : of == 1 ? p.X : p.W);
-  float m = 0.0f;
-  auto take = [&](const fx8& d) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(d[j]);
-      if (a < INFINITY) m = fmaxf(m, a);
-    }
-  };
-  const int64_t step = (int64_t)gridDim.x * 256;
-#pragma unroll 4
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += step) {
-    if (of == 0 && p.dy32) take(load8((const float*)p.dy + 8 * i));
-    else take(widen<D>(*(const vec*)(src + 8 * i)));
-  }
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) p.maxima[of * kMaxima + blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-}
-
-// The exponent e of the scale that brings the largest of k_max's values into [2^13,
-// 2^14): an activation's slope of up to 1.13 and the rounding to fp16 stay in range.
-__device__ __forceinline__ int scale_of(const float* maxima, float (&red)[4]) {
-  float m = 0.0f;
-  for (int i = threadIdx.x; i < kMaxima; i += 256) m = fmaxf(m, maxima[i]);
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  __syncthreads();
-  if (m == 0.0f) return 0;
-  int e = 0;
-  (void)frexpf(m, &e);  // m = f 2^e, f in [1/2, 1)
-  return min(max(14 - e, -126), 126);
-}
-
-// dz in one or two parts, and the sums over a group of rows for dbias. A
-// thread has 8 columns, LC threads a row: whole waves where there are several groups,
-// whose sums k_dbias adds; 8 threads and 32 rows at a time where one group has all rows
-// and its sums are dbias (200 x 2048: one launch of 4 us for two of 4 and 3).
-template <class D, int LC>
-__global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
-  constexpr int R = 256 / LC;  // rows at a time
-  __shared__ float red[R][8 * LC];
-  __shared__ float s_max[4];
-  const int col = 8 * (threadIdx.x % LC), slot = threadIdx.x / LC;
-  const int64_t n = (int64_t)blockIdx.x * (8 * LC) + col;
-  float scale = 1.0f;
-  if (p.maxima) {
-    const int e = scale_of(p.maxima, s_max);
-    scale = ldexpf(1.0f, e);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.inv_scale[0] = ldexpf(1.0f, -e);
-  }
-  fx8 sum = (fx8)(0.0f);
-  if (n < p.N) {
-    const int t0 = blockIdx.y * p.rows, t1 = min(p.T, t0 + p.rows);
-#pragma unroll 4
-    for (int t = t0 + slot; t < t1; t += R) {
-      const size_t at = (size_t)t * p.N + n;
-      const fx8 d = dz8<D>(p, at);
-      sum += d;
-      if (p.part1) {
-        const fx8 x = d * scale;
-        const hx8 h = narrow<F16>(x);
-        *(hx8*)((_Float16*)p.part1 + at) = h;
-        if (p.part2) *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
-      }
-    }
-  }
-  if (!p.dbias) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) red[slot][col + i] = sum[i];
-  __syncthreads();
-  float* to = gridDim.y == 1 ? p.dbias : p.db_part + (size_t)blockIdx.y * p.N;
-  for (int c = threadIdx.x; c < 8 * LC; c += 256) {
-    const int64_t at = (int64_t)blockIdx.x * (8 * LC) + c;
-    if (at >= p.N) break;
-    float s = red[0][c];
-#pragma unroll
-    for (int i = 1; i < R; ++i) s += red[i][c];
-    to[at] = s;
-  }
-}
-
+// ---------------------------------------------------------------- fp16 operands
 // bf16 X (blockIdx.y 0) and W (1) as scaled fp16, and the factor that takes the scale
 // out again. A value's 8 bits fit unless it is below 2^-30 of the largest.
 __global__ __launch_bounds__(256) void k_half(LinearGradParams p) {
@@ -714,20 +735,20 @@ hipError_t launch_product(LinearProduct p, const LinearPlan& plan, float* partia
 
 // dX and dW, in one launch where both have small tiles.
 template <class D, int KIND>
-hipError_t launch_gradients(LinearProduct x, const LinearPlan& px, LinearProduct w, const LinearPlan& pw, float* partial_x,
-                            float* partial_w, hipStream_t s) {
+hipError_t launch_gradients(LinearProduct x, const LinearPlan& px, LinearProduct w, const LinearPlan& pw,
+                            const LinearGradParams& p, bool with_dbias, hipStream_t s) {
   if (px.rows != 128 || pw.rows != 128) {
-    const hipError_t e = launch_product<D, false, true, KIND>(x, px, partial_x, s);
-    return e != hipSuccess ? e : launch_product<D, true, true, kGrad32>(w, pw, partial_w, s);
+    const hipError_t e = launch_product<D, false, true, KIND>(x, px, p.partial_x, s);
+    return e != hipSuccess ? e : launch_product<D, true, true, kGrad32>(w, pw, p.partial_w, s);
   }
-  set_plan(x, px, partial_x);
-  set_plan(w, pw, partial_w);
+  set_plan(x, px, p.partial_x);
+  set_plan(w, pw, p.partial_w);
   static unsigned long long raised = 0;
   constexpr int lds = 5 * 64 * 256;
   hipError_t e = raise_lds_limit((const void*)&k_gradients<D, KIND>, lds, raised);
   if (e != hipSuccess) return e;
-  const int bx = x.tm * x.tn * x.splits, bw = w.tm * w.tn * w.splits;
-  k_gradients<D, KIND><<<bx + bw, 256, lds, s>>>(x, w, bx);
+  const int bx = x.tm * x.tn * x.splits, bw = w.tm * w.tn * w.splits, bb = with_dbias ? (p.N + 31) / 32 : 0;
+  k_gradients<D, KIND><<<bx + bw + bb, 256, lds, s>>>(x, w, p, bx, bb);
   if ((e = hipGetLastError()) != hipSuccess || (e = join<D, KIND>(x, s)) != hipSuccess) return e;
   return join<D, kGrad32>(w, s);
 }
@@ -754,14 +775,17 @@ hipError_t forward(const LinearProduct& p, float* ws, hipStream_t s) {
 template <class D>
 hipError_t gradients(LinearGradParams p, hipStream_t s) {
   hipError_t e = hipSuccess;
-  const bool formed = p.part1 != nullptr;
+  const bool formed = p.part1 != nullptr, dx = p.dX && p.T > 0;
   const int groups = (p.T + p.rows - 1) / p.rows;
-  if (p.T > 0 && (formed || p.dbias)) {
+  const LinearPlan pw = linear_plan(p.N, p.Kd, p.T, formed ? 2 : 1), px = dx ? linear_plan(p.T, p.Kd, p.N, 1) : pw;
+  // dbias of a few tokens beside the products
+  const bool beside = p.dbias && !formed && groups == 1 && dx && p.dW && px.rows == 128 && pw.rows == 128;
+  if (p.T > 0 && (formed || (p.dbias && !beside))) {
     if (formed) {
       k_max<D><<<dim3(kMaxima, p.w16 ? 3 : p.x16 ? 2 : 1), 256, 0, s>>>(p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (groups == 1) k_dz<D, 8><<<(p.N + 63) / 64, 256, 0, s>>>(p);
+    if (groups == 1) k_dz<D, 4><<<(p.N + 31) / 32, 256, 0, s>>>(p);
     else k_dz<D, 64><<<dim3((p.N + 511) / 512, groups), 256, 0, s>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (p.x16 || p.w16) {
@@ -790,13 +814,10 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
   w.M = p.N; w.K = p.T;
   w.out.y = p.dW;
   w.out.scale2 = scaled && p.x16 ? p.inv_scale + 1 : nullptr;
-  const LinearPlan pw = linear_plan(w.M, w.N, w.K, formed ? 2 : 1);
-  const bool dx = p.dX && p.T > 0;
-  const LinearPlan px = dx ? linear_plan(x.M, x.N, x.K, 1) : pw;
   // parts are fp16 whatever the activations are
   if (dx && p.dW) {
-    if (p.w16) return launch_gradients<F16, kGradBf>(x, px, w, pw, p.partial_x, p.partial_w, s);
-    return launch_gradients<D, kGrad16>(x, px, w, pw, p.partial_x, p.partial_w, s);
+    if (p.w16) return launch_gradients<F16, kGradBf>(x, px, w, pw, p, false, s);
+    return launch_gradients<D, kGrad16>(x, px, w, pw, p, beside, s);
   }
   if (dx) return p.w16 ? launch_product<F16, false, true, kGradBf>(x, px, p.partial_x, s) : launch_product<D, false, true, kGrad16>(x, px, p.partial_x, s);
   if (p.dW) return formed ? launch_product<F16, true, true, kGrad32>(w, pw, p.partial_w, s) : launch_product<D, true, true, kGrad32>(w, pw, p.partial_w, s);
