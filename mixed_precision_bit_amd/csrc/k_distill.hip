@@ -17,6 +17,12 @@
 // Nothing is written twice: the pass over the row leaves the entries out, and each
 // entry's lane writes its own.
 //
+// The loss alone is bound by HBM (1021 x 65536 fp16 29 us, 4.7 TB/s). With the gradient a row is
+// read twice, the second time backwards and mostly from the Infinity Cache, and
+// written once: 2048 x 151677 bf16 296 us, 4.2 TB/s of one read and the write (302
+// forwards). 9 x 32003 fp32 takes 7.4 + 1.6 us, a chain of latencies; a wave each for
+// every step of the end of a row, with eight barriers and fp64 exponentials, took 10.3.
+//
 // Rows may begin at any element: up to 7 elements before the first 16-byte
 // boundary and after the last are taken one by one.
 #include <cfloat>

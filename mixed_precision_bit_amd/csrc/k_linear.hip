@@ -7,14 +7,22 @@
 // One product kernel, C[m][n] = sum_k A(m, k) B(n, k), for all three: an operand
 // lies with its reduction contiguous (X and W forward, dz in dX) or as the rows of
 // the other index (W in dX, dz and X in dW), which LDS's transposing reads turn on
-// the way into the registers. Tiles of 64 of the reduction go straight from memory to LDS, two buffers,
-// one barrier a step; a wave holds its part of the output in registers and
+// the way into the registers. Stages of 32 of the reduction go straight from memory to
+// LDS, four in flight, and a wave holds its part of the output in registers and
 // multiplies 16 x 16 x 32 at a time. Accumulation is fp32, every sum has a fixed
 // order (reductions split over workgroups leave partial sums that a second launch
 // adds in order).
 //
-// A batch of up to 16 tokens reads W once and has nothing to share: k_skinny, W
-// straight into the registers.
+// Large products are bound by the matrix cores under the card's power (they are busy 61 %
+// of dX's cycles, at 2 GHz): 8192 x 4096 x 4096 bf16 takes dX 221 us and dW 233, 1.24 and
+// 1.18 PFLOP/s, where a library product of those layouts takes 254 and 286, one of 8192^3 reaches 1.39
+// PFLOP/s. What did not help: one buffer of 64 ahead instead of four of 32 (dX 236), reads
+// interleaved with the products in every wave instead of halves of the waves in turn
+// (232), waves of 128 x 128, one a SIMD (252), two workgroups of 128 x 256 a CU with three
+// buffers each (312).
+//
+// A batch of few tokens reads W once and has little to share: k_skinny, W straight
+// into the registers.
 //
 // dz is formed once for both gradients. Where it is not exactly dy (an activation, or
 // fp32 dy) it becomes fp16 parts, whatever the activations are, scaled by a power of two
@@ -600,7 +608,8 @@ constexpr int kSkinnyWaves = 16;
 // 16 rows of W a workgroup and up to 16 MF tokens; its 16 waves take every 16th piece
 // of 64 of the reduction (whole 128-byte lines of W, once), both operands straight into
 // registers, U halves of pieces in flight. Their sums meet in LDS: waves 8 to 15
-// hand theirs to waves 0 to 7, whose sums are added in wave order.
+// hand theirs to waves 0 to 7, whose sums are added in wave order. Bound by HBM: one
+// token of 16384 x 4096 27 us (4.9 TB/s), of 4096 x 4096 8.9 (3.8: the launch and one chain of latencies).
 template <class D, int KIND, int MF>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
   typedef typename D::vec vec;
