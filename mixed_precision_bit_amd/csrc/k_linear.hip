@@ -297,6 +297,9 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
     if (left >= 32) {
       issue_whole(lds);
     } else {  // the reduction ends inside the stage: zeros behind its end
+      // arrived_but counts whole stages only; this one has no direct loads, and waves
+      // all of whose pieces lie behind the end would not wait at all
+      loads_but<0>();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (SPARE && i == NP - 1 && wave >= SPARE) break;
@@ -316,8 +319,8 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
       pb = OB::first(p.B, n0, sb);
     }
   };
-  // All but the last N stages that the wave issued have arrived. (One that ends the
-  // reduction has no direct loads, and its own came after every earlier one.)
+  // All but the last N stages that the wave issued have arrived (those before one that
+  // ends the reduction had when that was issued).
   auto arrived_but = [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (SPARE == 0 || wave < SPARE)

@@ -236,6 +236,17 @@ def test_gradients_through_an_activation(T, Kd, N, dt, dyt, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [33, 1025, 2017, 4097])
+def test_gradients_of_one_token_past_a_stage(T):
+    """Reductions that end one index into a stage of 32, once and in the middle of two parts."""
+    for Kd, N in ((128, 264), (4160, 2824)) if T == 4097 else ((128, 264),):
+        d = inputs(T, Kd, N, "bf16", seed=12)
+        dy = gradient_of(T, N, "bf16", d["g"])
+        for act in ("none", "silu"):
+            check_grad(d, "bf16", dy, act, run_grad(d, "bf16", dy, act))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("std", [1e-9, 1e-30, 1e5])
 def test_gradients_out_of_range_of_fp16(std):
     """fp32 gradients of a mean over a batch, and a large loss scale: dW and dbias keep their bits."""
