@@ -285,7 +285,9 @@ class DeviceLayer:
         [1], kl [T], with grad the gradient dS (with S's row stride, zeros between the rows), and what distill_grad
         needs. S may be the first V columns of wider logits."""
         T, f32 = S.shape[0], dict(dtype=torch.float32, device=self.device)
-        sd = {torch.float16: M.MPB_F16, torch.bfloat16: M.MPB_BF16, torch.float32: M.MPB_F32}[S.dtype]
+        sd = {torch.float16: M.MPB_F16, torch.bfloat16: M.MPB_BF16, torch.float32: M.MPB_F32}.get(S.dtype)
+        if sd is None:
+            raise M.MpbError("distill", -1, f"S is {S.dtype}, not fp16, bf16 or fp32")
         with self._on(stream):
             s = {"stats": torch.empty((T, 4), **f32), "kl": torch.empty(T, **f32), "loss": torch.empty(1, **f32),
                  "dS": self._like_logits(S) if grad else None, "args": (S, sd, ids, teacher, teacher_lse, weight, tau)}
