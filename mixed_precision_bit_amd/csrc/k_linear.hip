@@ -249,11 +249,12 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
   typedef typename D::vec vec;
   constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, MF = WM / 16, NF = WN / 16;
   constexpr int kStages = 5;  // buffers
-  // Rows of B within a wave's fragments: fragment j's row r is column 4 NF (r / 4) +
-  // 4 j + r % 4 of the wave's part, so that a lane ends up with 4 NF consecutive
-  // columns of one row of C. Turned operands come in 16 consecutive columns.
-  constexpr int SHB = NF == 4 ? 4 : 3;
-  static_assert(NF == 4 || NF == 2, "");
+  // Rows of B within a wave's fragments: fragment j's row r is column 32 (j / 2) + 8 (r / 4)
+  // + 4 (j % 2) + r % 4 of the wave's part, so that a lane ends up with 8 consecutive columns
+  // of a row of C for every two fragments, and 4 lanes with 32. Turned operands come in 16
+  // consecutive columns.
+  constexpr int SHB = 3;
+  static_assert(NF % 2 == 0, "");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int id = unit(block, blocks), tiles = p.tm * p.tn;
   const int split = id / tiles, tile = id - split * tiles;
@@ -343,7 +344,7 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
 #pragma unroll
     for (int j = 0; j < NF; ++j) fb[j] = kA + 2 * BN * kk + 32 * ((wn / 16 + j) ^ OB::swz_k(kk)) + 8 * (r & 3);
   } else {
-    fb[0] = kA + 64 * (wn + 4 * NF * (r >> 2) + (r & 3)) + 16 * (g ^ (r >> 1 & 3));
+    fb[0] = kA + 64 * (wn + 8 * (r >> 2) + (r & 3)) + 16 * (g ^ (r >> 1 & 3));
   }
 
   acc4 acc[MF][NF];
@@ -362,7 +363,7 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
   uint32_t buf = lds0, free = lds0 + kAhead * kStage;  // of stage s, of stage s - 1
   auto stage = [&](auto steady, int s) {
 #pragma unroll
-    for (int j = 0; j < NF; ++j) b[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]), 8 * BN) : read_rows(at(buf, fb[0]) + 256 * j);
+    for (int j = 0; j < NF; ++j) b[j] = BT ? read_turned(at(buf, fb[BT ? j : 0]), 8 * BN) : read_rows(at(buf, fb[0]) + 2048 * (j / 2) + 256 * (j % 2));
 #pragma unroll
     for (int i = 0; i < MF; ++i) a[i] = AT ? read_turned(at(buf, fa[AT ? i : 0]), 8 * BM) : read_rows(at(buf, fa[0]) + 1024 * i);
     if (steady) issue_whole(free);
@@ -395,10 +396,10 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
     if (kTwoHalves && wave < NW / 2) __syncthreads();
   }
 
-  // lane (r, g): row r of each 16, columns 4 NF g ... (rows) or 16 j + 4 g ... (turned)
+  // lane (r, g): row r of each 16, columns 32 k + 8 g ... (rows) or 16 k + 4 g ... (turned)
   constexpr int NV = BT ? 4 : 8, NG = WN / 4 / NV;  // columns of a group, groups of a row
   const int64_t m = m0 + wm + r;
-  auto column = [&](int k) { return n0 + wn + (BT ? 16 * k + 4 * g : 4 * NF * g + 8 * k); };
+  auto column = [&](int k) { return n0 + wn + (BT ? 16 * k + 4 * g : 32 * k + 8 * g); };
   if (p.partial) {
 #pragma unroll
     for (int i = 0; i < MF; ++i)
