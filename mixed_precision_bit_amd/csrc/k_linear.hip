@@ -249,10 +249,13 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
   typedef typename D::vec vec;
   constexpr int NWN = BN / WN, NW = (BM / WM) * NWN, MF = WM / 16, NF = WN / 16;
   constexpr int kStages = 5;  // buffers
-  // Rows of B within a wave's fragments: fragment j's row r is column 32 (j / 2) + 8 (r / 4)
-  // + 4 (j % 2) + r % 4 of the wave's part, so that a lane ends up with 8 consecutive columns
-  // of a row of C for every two fragments, and 4 lanes with 32. Turned operands come in 16
-  // consecutive columns.
+  // Columns of C in a lane (row r of 16, g of 4) once its products are done: 8 in a row for
+  // every two fragments of B, 32 with its neighbours, so that what a wave stores in two
+  // instructions at most are whole lines of fp32 and half lines of 16 bits. Where B lies in rows, fragment j's
+  // row r is column 32 (j / 2) + 8 (r / 4) + 4 (j % 2) + r % 4; where it is turned, a
+  // fragment is 16 consecutive columns, and lanes 16 apart exchange theirs at the end.
+  // 4096 x 8192 x 2048 with fp32 y takes 150 us, 163 with 4 columns a lane, 253 with 16;
+  // 8192 x 4096 x 4096 dX 211, 219 with 4.
   constexpr int SHB = 3;
   static_assert(NF % 2 == 0, "");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -396,22 +399,35 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
     if (kTwoHalves && wave < NW / 2) __syncthreads();
   }
 
-  // lane (r, g): row r of each 16, columns 32 k + 8 g ... (rows) or 16 k + 4 g ... (turned)
-  constexpr int NV = BT ? 4 : 8, NG = WN / 4 / NV;  // columns of a group, groups of a row
   const int64_t m = m0 + wm + r;
-  auto column = [&](int k) { return n0 + wn + (BT ? 16 * k + 4 * g : 32 * k + 8 * g); };
   if (p.partial) {
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        if (m + 16 * i >= p.M || column(k) >= p.N) continue;
-        float* to = p.partial + ((size_t)split * p.M + m + 16 * i) * p.N + column(k);
-#pragma unroll
-        for (int e = 0; e < NV / 4; ++e) *(acc4*)(to + 4 * e) = acc[i][k * (NV / 4) + e];
+      for (int j = 0; j < NF; ++j) {
+        const int64_t n = n0 + wn + (BT ? 16 * j + 4 * g : 32 * (j / 2) + 8 * g + 4 * (j % 2));
+        if (m + 16 * i < p.M && n < p.N) *(acc4*)(p.partial + ((size_t)split * p.M + m + 16 * i) * p.N + n) = acc[i][j];
       }
     return;
   }
+  constexpr int NV = 8, NG = NF / 2;  // columns of a group, groups of a lane's row
+  if constexpr (BT) {
+    // of fragments 2 k and 2 k + 1, lanes of even g keep the first and get their neighbour's
+    // four columns of it, those of odd g the second's
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; j += 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][e]), __float_as_uint(acc[i][j + 1][e]), false, false);
+          acc[i][j][e] = __uint_as_float(v[0]);
+          acc[i][j + 1][e] = __uint_as_float(v[1]);
+        }
+  }
+  auto column = [&](int k) {
+    return n0 + wn + 32 * k + (BT ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
+  };
   Residual<D, NV, KIND> res[2][NG];
   auto load_row = [&](int i) {
 #pragma unroll
@@ -427,7 +443,7 @@ __device__ __forceinline__ void product_tile(const LinearProduct& p, int block, 
       if (m + 16 * i >= p.M || column(k) >= p.N) continue;
       float v[NV];
 #pragma unroll
-      for (int e = 0; e < NV; ++e) v[e] = acc[i][k * (NV / 4) + e / 4][e & 3];
+      for (int e = 0; e < NV; ++e) v[e] = acc[i][2 * k + e / 4][e & 3];
       finish<D, NV, KIND>(p.out, m + 16 * i, (int)column(k), v, res[i & 1][k]);
     }
   }
