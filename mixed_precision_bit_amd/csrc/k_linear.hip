@@ -456,20 +456,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_product(LinearPr
 }
 
 // ---------------------------------------------------------------- dz
-// dy act'(z) of 8 consecutive elements.
-template <class D>
-__device__ __forceinline__ fx8 dz8(const LinearGradParams& p, size_t at) {
-  typedef typename D::vec vec;
-  typedef typename D::elem elem;
-  fx8 d = p.dy32 ? load8((const float*)p.dy + at) : widen<D>(*(const vec*)((const elem*)p.dy + at));
-  if (p.act != MPB_ACT_NONE) {
-    const fx8 z = widen<D>(*(const vec*)((const elem*)p.z + at));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] *= act_grad(z[i], p.act);
-  }
-  return d;
-}
-
 // The largest finite |v| of each workgroup's share of dy (blockIdx.y 0), and of X (1)
 // and W (2) where they are to become fp16.
 template <class D>
@@ -523,6 +509,8 @@ __device__ __forceinline__ int scale_of(const float* maxima, float (&red)[4]) {
 // and its sums are dbias.
 template <class D, int LC>
 __device__ __forceinline__ void dz_rows(const LinearGradParams& p, int bx, int by, int groups, float* smem) {
+  typedef typename D::vec vec;
+  typedef typename D::elem elem;
   constexpr int R = 256 / LC;  // rows at a time
   float(*red)[8 * LC] = (float(*)[8 * LC])smem;  // [R]
   const int col = 8 * (threadIdx.x % LC), slot = threadIdx.x / LC;
@@ -534,19 +522,52 @@ __device__ __forceinline__ void dz_rows(const LinearGradParams& p, int bx, int b
     if (bx == 0 && by == 0 && threadIdx.x == 0) p.inv_scale[0] = ldexpf(1.0f, -e);
   }
   fx8 sum = (fx8)(0.0f);
-  if (n < p.N) {
+  // U rows a thread are loaded before the first is worked on (none is behind the last);
+  // left to the compiler, the loads of one waited for the stores of the one before
+  constexpr int U = 4;
+  auto rows = [&](auto wide, auto with_z) {
     const int t0 = by * p.rows, t1 = min(p.T, t0 + p.rows);
-#pragma unroll 4
-    for (int t = t0 + slot; t < t1; t += R) {
-      const size_t at = (size_t)t * p.N + n;
-      const fx8 d = dz8<D>(p, at);
-      sum += d;
-      if (p.part1) {
-        const fx8 x = d * scale;
-        const hx8 h = narrow<F16>(x);
-        *(hx8*)((_Float16*)p.part1 + at) = h;
-        if (p.part2) *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
+    for (int t = t0 + slot; t < t1; t += U * R) {
+      fx8 dy32[U];
+      vec dy[U], z[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const size_t at = (size_t)min(t + u * R, t1 - 1) * p.N + n;
+        if constexpr (wide) dy32[u] = load8((const float*)p.dy + at);
+        else dy[u] = *(const vec*)((const elem*)p.dy + at);
+        if constexpr (with_z) z[u] = *(const vec*)((const elem*)p.z + at);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u * R >= t1) break;
+        fx8 d;
+        if constexpr (wide) d = dy32[u];
+        else d = widen<D>(dy[u]);
+        if constexpr (with_z) {
+          const fx8 x = widen<D>(z[u]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] *= act_grad(x[i], p.act);
+        }
+        sum += d;
+        if constexpr (wide || with_z) {
+          if (!p.part1) continue;
+          const size_t at = (size_t)(t + u * R) * p.N + n;
+          const fx8 x = d * scale;
+          const hx8 h = narrow<F16>(x);
+          *(hx8*)((_Float16*)p.part1 + at) = h;
+          if (p.part2) *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
+        }
+      }
+    }
+  };
+  if (n < p.N) {
+    using std::false_type, std::true_type;
+    if (p.act != MPB_ACT_NONE) {
+      if (p.dy32) rows(true_type(), true_type());
+      else rows(false_type(), true_type());
+    } else {
+      if (p.dy32) rows(true_type(), false_type());
+      else rows(false_type(), false_type());
     }
   }
   if (!p.dbias) return;
@@ -584,7 +605,7 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
 
 // dX and dW in one launch, where both have small tiles and neither fills the chip
 // alone, and dbias of a few tokens (blocks_b workgroups): 200 x 2048 x 2048 with its
-// join 24 us, in a launch each 36.
+// join 23 us, in a launch each 36.
 template <class D, int KIND>
 __global__ __launch_bounds__(256) void k_gradients(LinearProduct x, LinearProduct w, LinearGradParams p, int blocks_x,
                                                    int blocks_b) {
