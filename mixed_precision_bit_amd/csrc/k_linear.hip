@@ -13,13 +13,13 @@
 // order (reductions split over workgroups leave partial sums that a second launch
 // adds in order).
 //
-// Large products are bound by the matrix cores under the card's power (they are busy 61 %
-// of dX's cycles, at 2 GHz): 8192 x 4096 x 4096 bf16 takes dX 221 us and dW 233, 1.24 and
-// 1.18 PFLOP/s, where a library product of those layouts takes 254 and 286, one of 8192^3 reaches 1.39
-// PFLOP/s. What did not help: one buffer of 64 ahead instead of four of 32 (dX 236), reads
-// interleaved with the products in every wave instead of halves of the waves in turn
-// (232), waves of 128 x 128, one a SIMD (252), two workgroups of 128 x 256 a CU with three
-// buffers each (312).
+// Large products are bound by the matrix cores under the card's power (they are busy 64 %
+// of dX's cycles, at 2 GHz): 8192 x 4096 x 4096 bf16 takes dX 210 us and dW 221, 1.31 and
+// 1.24 PFLOP/s, where a library product of those layouts takes 252 and 284, one of 8192^3 reaches 1.39
+// PFLOP/s. What did not help, against dX of 221 to 227 at the time: one buffer of 64 ahead
+// instead of four of 32 (236), reads interleaved with the products in every wave instead
+// of halves of the waves in turn (232), waves of 128 x 128, one a SIMD (252), two
+// workgroups of 128 x 256 a CU with three buffers each (312).
 //
 // A batch of few tokens reads W once and has little to share: k_skinny, W straight
 // into the registers.
