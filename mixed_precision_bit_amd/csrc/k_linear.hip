@@ -67,6 +67,37 @@ __device__ __forceinline__ float sigmoid16(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269502f * x));
 }
 
+// Phi(-a) for a >= 0, given e = exp(-a^2 / 2): e t Q(t) with t = 1 / (1 + C a), where
+// Phi(-a) / (e t) is so smooth in t that a polynomial, fitted for the least largest
+// relative error over a in [0, 20], stays within 2^-17 of it (degree 5, for results of 16
+// bits) or 2^-25 (degree 8). With the roundings of fp32 the latter is within 2^-20
+// of itself up to a = 4, 2^-17 up to 13, where e leaves the range of fp32. dz of 4093 x
+// 2816 24 us, 33 to 40 with erfcf; 4093 x 5632 x 2816 forward with gelu 138, 156 with it.
+template <bool NARROW>
+__device__ __forceinline__ float normal_tail(float a, float e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(NARROW ? 0.311126977f : 0.268700570f, a, 1.0f));
+  float q;
+  if constexpr (NARROW) {
+    q = fmaf(-0.0719563290f, t, 0.172309935f);
+    q = fmaf(q, t, 0.0234833770f);
+    q = fmaf(q, t, 0.130294949f);
+    q = fmaf(q, t, 0.121615790f);
+    q = fmaf(q, t, 0.124253877f);
+  } else {
+    q = fmaf(0.0290484875f, t, -0.129195794f);
+    q = fmaf(q, t, 0.178268000f);
+    q = fmaf(q, t, -0.0769507661f);
+    q = fmaf(q, t, 0.112688191f);
+    q = fmaf(q, t, 0.0701929182f);
+    q = fmaf(q, t, 0.101762444f);
+    q = fmaf(q, t, 0.106982090f);
+    q = fmaf(q, t, 0.107204415f);
+  }
+  return e * (t * q);
+}
+// exp(-z^2 / 2)
+__device__ __forceinline__ float bell(float z) { return __builtin_amdgcn_exp2f(-0.721347520f * (z * z)); }
+
 // gelu_tanh is z sigmoid(2 u), u = a (z + b z^3): 1 + tanh(u) = 2 sigmoid(2 u),
 // which keeps its relative accuracy where tanh is close to -1.
 template <bool NARROW>
@@ -75,7 +106,11 @@ __device__ __forceinline__ float act_of(float z, int act) {
   switch (act) {
     case MPB_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
     case MPB_ACT_SILU: return z * sig(z);
-    case MPB_ACT_GELU: return 0.5f * z * erfcf(-z * kSqrtHalf);
+    case MPB_ACT_GELU: {
+      if constexpr (!NARROW) return 0.5f * z * erfcf(-z * kSqrtHalf);
+      const float tail = normal_tail<true>(fabsf(z), bell(z));
+      return z * (z > 0.0f ? 1.0f - tail : tail);
+    }
     case MPB_ACT_GELU_TANH: return z * sig(2.0f * kTanhA * (z + kTanhB * z * z * z));
     default: return z;
   }
@@ -102,7 +137,8 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     }
     case MPB_ACT_GELU: {
       const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f);
-      return 0.5f * erfcf(-x * kSqrtHalf) + x * kInvSqrt2Pi * expf(-0.5f * x * x);
+      const float e = bell(x), tail = normal_tail<false>(fabsf(x), e);
+      return fmaf(x * kInvSqrt2Pi, e, x > 0.0f ? 1.0f - tail : tail);
     }
     case MPB_ACT_GELU_TANH: {
       const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f), x2 = x * x;
