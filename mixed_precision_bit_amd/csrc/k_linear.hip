@@ -72,7 +72,7 @@ __device__ __forceinline__ float sigmoid16(float x) {
 // relative error over a in [0, 20], stays within 2^-17 of it (degree 5, for results of 16
 // bits) or 2^-25 (degree 8). With the roundings of fp32 the latter is within 2^-20
 // of itself up to a = 4, 2^-17 up to 13, where e leaves the range of fp32. dz of 4093 x
-// 2816 24 us, 33 to 40 with erfcf; 4093 x 5632 x 2816 forward with gelu 138, 156 with it.
+// 2816 24 us, 36 to 40 with erfcf; 4093 x 5632 x 2816 forward with gelu 138, 156 with it.
 template <bool NARROW>
 __device__ __forceinline__ float normal_tail(float a, float e) {
   const float t = __builtin_amdgcn_rcpf(fmaf(NARROW ? 0.311126977f : 0.268700570f, a, 1.0f));
