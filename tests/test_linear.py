@@ -168,6 +168,24 @@ def test_activations_far_out():
         check(y[0], ref, 8 * U * z.double().abs().clamp(max=100) + 64 * U * ref.abs() + 1e-38, act)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ("f16", "bf16"))
+def test_gelu_tail(dt):
+    """gelu keeps its relative accuracy where Phi is small: the fit 2^-17, fp32's roundings of the
+    exponential's argument 2.5 x 2^-24 x a^2 / 2 (below 2^-16 at -12), the result half a step; below the smallest normal number half its last step."""
+    M = lib_m()
+    N, t = 4096, torch.float16 if dt == "f16" else torch.bfloat16
+    z = torch.linspace(-12, 12, N, device="cuda")
+    X, W = torch.zeros(1, 64, dtype=t, device="cuda"), torch.zeros(N, 64, dtype=t, device="cuda")
+    y = torch.empty(1, N, dtype=t, device="cuda")
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    M.moe_linear(X, xd(dt), W, z, ACTS.index("gelu"), None, None, y, ws)
+    ref = act64(z.double().cpu(), "gelu")[0]
+    f = torch.finfo(t)
+    tol = ref.abs() * (f.eps / 2 + 1.01 * (2.0**-16 + 2.0**-17)) + f.tiny * f.eps / 2
+    assert bool(((y[0].double().cpu() - ref).abs() <= tol).all())
+
+
 # ------------------------------------------------------------------------------------------------ gradients
 def run_grad(d, dt, dy, act, stream=None, want=("dX", "dW", "db")):
     M = lib_m()
