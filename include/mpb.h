@@ -436,10 +436,9 @@ int moe_linear(const void* X_dev, int x_dtype, const void* W_dev, const float* b
  *   dX_dev      [T][Kd] x_dtype;  dW_dev [N][Kd] fp32;  dbias_dev [N] fp32; each
  *               may be NULL (W_dev is read for dX, X_dev for dW)
  * relu' is 0 at 0. Sums are fp32 in a fixed order (deterministic). Where dz is not
- * dy itself (an activation, or fp32 dy) the products take it in fp16 parts, bf16 X
- * and W as fp16 beside them: dX, which is rounded to 16 bits, from dz to 11 bits, dW from
- * dz to 22 bits, dbias from dz itself; dz is also off by 2^-38 of the largest |dy|, X
- * and W by 2^-38 of their largest.
+ * dy itself (an activation, or fp32 dy) the products take it in two fp16 parts, bf16 X
+ * and W as fp16 beside them: dX and dW from dz to 22 bits, dbias from dz itself; dz is
+ * also off by 2^-38 of the largest |dy|, X and W by 2^-38 of their largest.
  * fp16 parts carry a power of two, so that small gradients keep their bits whatever
  * their range; an infinite or NaN dz gives infinite or NaN sums. T == 0 zeroes dW
  * and dbias. ws_dev: at least moe_linear_grad_workspace_bytes(T, Kd, N, act, dy_dtype)

@@ -27,10 +27,12 @@
 // dz is formed once for both gradients. Where it is not exactly dy (an activation, or
 // fp32 dy) it becomes fp16 parts, whatever the activations are, scaled by a power of two
 // that brings the largest value to 2^13 (the gradients of a mean, below fp16's range,
-// keep their bits): one part of 11 bits for dX, whose result is rounded to 16 bits anyway,
-// two of 22 together for dW, whose result is fp32. bf16 X and W become scaled fp16 beside them.
-// bf16 parts cost the same and lose more: dX 2.3e-3 of its norm off with one instead of
-// 1.7e-3, dW 2.6e-6 with two instead of 7e-7 (an fp32 library product: 1.2e-6; 4093 tokens).
+// keep their bits): two parts, of 22 bits together, for dX and dW alike. bf16 X and W become
+// scaled fp16 beside them. dX could do with one part half the time, but not with its 11 bits:
+// fp16 dX would be 2.9e-4 of its norm off, its own rounding being 2.1e-4, and bf16 dX
+// 8.6e-4 of its norm from the product of the unrounded dz.
+// bf16 parts cost the same and lose more: dW 2.6e-6 with two instead of 7e-7 (an fp32
+// library product: 1.2e-6; 4093 tokens).
 #include <type_traits>
 
 #include "k_block_common.h"
@@ -591,7 +593,10 @@ __device__ __forceinline__ void dz_rows(const LinearGradParams& p, int bx, int b
           const fx8 x = d * scale;
           const hx8 h = narrow<F16>(x);
           *(hx8*)((_Float16*)p.part1 + at) = h;
-          if (p.part2) *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(x - widen<F16>(h));
+          fx8 left = x - widen<F16>(h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) left[i] = fabsf(x[i]) < INFINITY ? left[i] : 0.0f;  // inf - inf
+          *(hx8*)((_Float16*)p.part2 + at) = narrow<F16>(left);
         }
       }
     }
@@ -863,7 +868,8 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
   hipError_t e = hipSuccess;
   const bool formed = p.part1 != nullptr, dx = p.dX && p.T > 0;
   const int groups = (p.T + p.rows - 1) / p.rows;
-  const LinearPlan pw = linear_plan(p.N, p.Kd, p.T, formed ? 2 : 1), px = dx ? linear_plan(p.T, p.Kd, p.N, 1) : pw;
+  const int parts = formed ? 2 : 1;
+  const LinearPlan pw = linear_plan(p.N, p.Kd, p.T, parts), px = dx ? linear_plan(p.T, p.Kd, p.N, parts) : pw;
   // dbias of a few tokens beside the products
   const bool beside = p.dbias && !formed && groups == 1 && dx && p.dW && px.rows == 128 && pw.rows == 128;
   if (p.T > 0 && (formed || (p.dbias && !beside))) {
@@ -889,13 +895,13 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
   g.out.scale = scaled ? p.inv_scale : nullptr;
   g.lda = p.N;
   g.N = p.Kd;
-  g.A = g.A2 = formed ? p.part1 : p.dy;
+  g.A = formed ? p.part1 : p.dy;
+  g.A2 = formed ? p.part2 : p.dy;
   LinearProduct x = g, w = g;
   x.B = p.w16 ? p.w16 : p.W;
   x.M = p.T; x.K = p.N;
   x.out.y = p.dX;
   x.out.scale2 = p.w16 ? p.inv_scale + 2 : nullptr;
-  if (formed) w.A2 = p.part2;
   w.B = p.x16 ? p.x16 : p.X;
   w.M = p.N; w.K = p.T;
   w.out.y = p.dW;

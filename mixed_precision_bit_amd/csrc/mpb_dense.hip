@@ -77,6 +77,7 @@ GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
     return o;
   };
   const size_t part = (size_t)T * N * 2;
+  const int parts = w.formed ? 2 : 1;
   w.part1 = take(w.formed ? part : 0);
   w.part2 = take(w.formed ? part : 0);
   w.x16 = take(w.formed && bf16 ? (size_t)T * Kd * 2 : 0);
@@ -84,8 +85,8 @@ GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
   w.maxima = take(3 * mpb::kMaxima * sizeof(float));
   w.inv_scale = take(3 * sizeof(float));
   w.db_part = take((size_t)((T + w.rows - 1) / w.rows) * N * sizeof(float));
-  w.partial_x = take(T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, 1), T, Kd) : 0);
-  w.partial_w = take(partial_bytes(mpb::linear_plan(N, Kd, T, w.formed ? 2 : 1), N, Kd));
+  w.partial_x = take(T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, parts), T, Kd) : 0);
+  w.partial_w = take(partial_bytes(mpb::linear_plan(N, Kd, T, parts), N, Kd));
   w.total = at;
   return w;
 }
@@ -196,7 +197,7 @@ int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, 
   p.dX = dX_dev; p.dW = dW_dev; p.dbias = dbias_dev;
   const bool parts = w.formed && (dX_dev || dW_dev);
   p.part1 = parts ? ws + w.part1 : nullptr;
-  p.part2 = parts && dW_dev ? ws + w.part2 : nullptr;
+  p.part2 = parts ? ws + w.part2 : nullptr;
   p.x16 = parts && bf16 && dW_dev ? ws + w.x16 : nullptr;
   p.w16 = parts && bf16 && dX_dev ? ws + w.w16 : nullptr;
   p.maxima = (float*)(ws + w.maxima);

@@ -412,7 +412,7 @@ struct LinearGradParams {
   float* dbias;            // [N] or null
   // workspace; the parts are null where dz is dy, or no product needs them
   void* part1;             // [T][N] dz as scaled fp16
-  void* part2;             // [T][N] what its rounding left (with dW)
+  void* part2;             // [T][N] what its rounding left
   void* x16;               // [T][Kd] bf16 X as scaled fp16 (with dW), or null
   void* w16;               // [N][Kd] bf16 W as scaled fp16 (with dX), or null
   float* maxima;           // [3][kMaxima] of |dy|, |X| and |W|
