@@ -187,8 +187,12 @@ __device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, flo
   for (int i = 0; i < NV; ++i) w[i] = v[i];
   constexpr bool kNarrow = KIND != kGrad32 && KIND != kOut32;
   if constexpr (KIND <= kGrad32) {
-    if (o.scale) w *= *o.scale;
-    if (o.scale2) w *= *o.scale2;  // one after the other: their product may be out of range
+    if (o.exp2) {
+      // at once: 2 to one of them may be out of range, and so may the result in between
+      const int e = *o.exp2 + (o.exp2_b ? *o.exp2_b : 0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) w[i] = __builtin_ldexpf(w[i], e);
+    }
   } else {
     if (o.bias) w += *(const fvec*)(o.bias + n);
     if (o.z) *(evec*)((elem*)o.z + at) = __builtin_convertvector(w, evec);
@@ -557,7 +561,7 @@ __device__ __forceinline__ void dz_rows(const LinearGradParams& p, int bx, int b
   if (p.part1) {
     const int e = scale_of(p.maxima, *(float(*)[4])smem);
     scale = ldexpf(1.0f, e);
-    if (bx == 0 && by == 0 && threadIdx.x == 0) p.inv_scale[0] = ldexpf(1.0f, -e);
+    if (bx == 0 && by == 0 && threadIdx.x == 0) p.exp2[0] = -e;
   }
   fx8 sum = (fx8)(0.0f);
   // U rows a thread are loaded before the first is worked on (none is behind the last);
@@ -754,7 +758,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_skinny(LinearProduct p) {
 }
 
 // ---------------------------------------------------------------- fp16 operands
-// bf16 X (blockIdx.y 0) and W (1) as scaled fp16, and the factor that takes the scale
+// bf16 X (blockIdx.y 0) and W (1) as scaled fp16, and the exponent that takes the scale
 // out again. A value's 8 bits fit unless it is below 2^-30 of the largest.
 __global__ __launch_bounds__(256) void k_half(LinearGradParams p) {
   __shared__ float s_max[4];
@@ -762,7 +766,7 @@ __global__ __launch_bounds__(256) void k_half(LinearGradParams p) {
   _Float16* to = (_Float16*)(of == 1 ? p.x16 : p.w16);
   if (!to) return;
   const int e = scale_of(p.maxima + of * kMaxima, s_max);
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.inv_scale[of] = ldexpf(1.0f, -e);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.exp2[of] = -e;
   const float scale = ldexpf(1.0f, e);
   const __bf16* src = (const __bf16*)(of == 1 ? p.X : p.W);
   const int64_t n8 = (int64_t)(of == 1 ? p.T : p.N) * p.Kd / 8, step = (int64_t)gridDim.x * 256;
@@ -892,7 +896,7 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
   const bool scaled = formed && p.T > 0;  // the scales are there
   LinearProduct g{};
   g.out.N = g.ldb = p.Kd;
-  g.out.scale = scaled ? p.inv_scale : nullptr;
+  g.out.exp2 = scaled ? p.exp2 : nullptr;
   g.lda = p.N;
   g.N = p.Kd;
   g.A = formed ? p.part1 : p.dy;
@@ -901,11 +905,11 @@ hipError_t gradients(LinearGradParams p, hipStream_t s) {
   x.B = p.w16 ? p.w16 : p.W;
   x.M = p.T; x.K = p.N;
   x.out.y = p.dX;
-  x.out.scale2 = p.w16 ? p.inv_scale + 2 : nullptr;
+  x.out.exp2_b = p.w16 ? p.exp2 + 2 : nullptr;
   w.B = p.x16 ? p.x16 : p.X;
   w.M = p.N; w.K = p.T;
   w.out.y = p.dW;
-  w.out.scale2 = scaled && p.x16 ? p.inv_scale + 1 : nullptr;
+  w.out.exp2_b = scaled && p.x16 ? p.exp2 + 1 : nullptr;
   // parts are fp16 whatever the activations are
   if (dx && p.dW) {
     if (p.w16) return launch_gradients<F16, kGradBf>(x, px, w, pw, p, false, s);

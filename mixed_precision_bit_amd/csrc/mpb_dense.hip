@@ -57,7 +57,7 @@ size_t partial_bytes(const mpb::LinearPlan& p, int64_t M, int64_t N) {
 // Regions of moe_linear_grad's workspace. dz is formed where it is not dy itself, as
 // fp16 parts, and bf16 X and W become fp16 beside them.
 struct GradWs {
-  size_t part1, part2, x16, w16, maxima, inv_scale, db_part, partial_x, partial_w, total;
+  size_t part1, part2, x16, w16, maxima, exp2, db_part, partial_x, partial_w, total;
   int rows;
   bool formed;
 };
@@ -83,7 +83,7 @@ GradWs grad_ws(int T, int Kd, int N, int act, bool dy32, bool bf16) {
   w.x16 = take(w.formed && bf16 ? (size_t)T * Kd * 2 : 0);
   w.w16 = take(w.formed && bf16 && T > 0 ? (size_t)N * Kd * 2 : 0);
   w.maxima = take(3 * mpb::kMaxima * sizeof(float));
-  w.inv_scale = take(3 * sizeof(float));
+  w.exp2 = take(3 * sizeof(int32_t));
   w.db_part = take((size_t)((T + w.rows - 1) / w.rows) * N * sizeof(float));
   w.partial_x = take(T > 0 ? partial_bytes(mpb::linear_plan(T, Kd, N, parts), T, Kd) : 0);
   w.partial_w = take(partial_bytes(mpb::linear_plan(N, Kd, T, parts), N, Kd));
@@ -201,7 +201,7 @@ int moe_linear_grad(const void* X_dev, int x_dtype, const void* W_dev, int act, 
   p.x16 = parts && bf16 && dW_dev ? ws + w.x16 : nullptr;
   p.w16 = parts && bf16 && dX_dev ? ws + w.w16 : nullptr;
   p.maxima = (float*)(ws + w.maxima);
-  p.inv_scale = (float*)(ws + w.inv_scale);
+  p.exp2 = (int32_t*)(ws + w.exp2);
   p.db_part = (float*)(ws + w.db_part);
   p.partial_x = (float*)(ws + w.partial_x);
   p.partial_w = (float*)(ws + w.partial_w);

@@ -373,8 +373,8 @@ struct LinearOut {
   const void* res;         // [M][N] of y's type, or null
   void* z;                 // [M][N] activations, or null
   void* y;                 // [M][N] activations or fp32
-  const float* scale;      // device scalars that multiply the product, or null
-  const float* scale2;
+  const int32_t* exp2;     // the product is multiplied by 2 to the sum of these device scalars, or null
+  const int32_t* exp2_b;
   int act, y32;
   int64_t N;
 };
@@ -416,7 +416,7 @@ struct LinearGradParams {
   void* x16;               // [T][Kd] bf16 X as scaled fp16 (with dW), or null
   void* w16;               // [N][Kd] bf16 W as scaled fp16 (with dX), or null
   float* maxima;           // [3][kMaxima] of |dy|, |X| and |W|
-  float* inv_scale;        // [3] of dz, X and W
+  int32_t* exp2;           // [3] that take the scales of dz, X and W out again
   float* db_part;          // [groups][N]
   float* partial_x;        // of dX's and dW's split reductions
   float* partial_w;

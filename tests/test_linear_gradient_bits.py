@@ -75,3 +75,17 @@ def test_infinite_gradients_keep_their_sign(dyt):
     W, X = d["W"].double(), d["X"].double()
     assert torch.equal(out["dX"][3].double(), float("inf") * W[5]) and torch.equal(out["dX"][9].double(), -float("inf") * W[7])
     assert torch.equal(out["dW"][5].double(), float("inf") * X[3]) and torch.equal(out["dW"][7].double(), -float("inf") * X[9])
+
+
+@pytest.mark.parametrize("T,Kd,N", [(70, 128, 264), (4001, 2816, 72)])
+@pytest.mark.parametrize("up", [122, -100])
+def test_scales_far_apart(up, T, Kd, N):
+    """Gradients near one end of bf16's range with operands that bring the products back: no overflow on the way."""
+    d = TL.inputs(T, Kd, N, "bf16", seed=25)
+    other = 2.0 ** (-60 if up > 0 else 60)
+    d["X"] *= other
+    d["W"] *= other
+    dy = TL.gradient_of(T, N, "bf16", d["g"]) * 2.0 ** up  # of 0.1: the largest is near 2^(up - 1)
+    out = TL.run_grad(d, "bf16", dy, "silu", want=("dX", "dW"))
+    assert out["dX"].isfinite().all() and out["dW"].isfinite().all()
+    TL.check_grad(d, "bf16", dy, "silu", out)
