@@ -63,38 +63,30 @@ __device__ __forceinline__ acc4 product<BF16>(bx8 a, bx8 b, acc4 c) {
 constexpr float kSqrtHalf = 0.707106781f, kInvSqrt2Pi = 0.398942280f;
 constexpr float kTanhA = 0.797884561f, kTanhB = 0.044715f;  // sqrt(2 / pi)
 
-// For results of 16 bits: within |x| 2^-24 of itself, 2^-9 being asked, in half the
-// operations (4093 x 5632 x 2816 with gelu_tanh: 148 us with the other, 143 with this).
+// For results of 16 bits: within (6 + |x|) 2^-24 of itself (the roundings of the exponent, the
+// exponential and the reciprocal), in half the operations: 4093 x 5632 x 2816 with silu,
+// residual and z 136 us, 143 with the other. Below -88.7, where sigmoid is under 2^-128,
+// the exponential overflows and this is 0.
 __device__ __forceinline__ float sigmoid16(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269502f * x));
 }
 
 // Phi(-a) for a >= 0, given e = exp(-a^2 / 2): e t Q(t) with t = 1 / (1 + C a), where
-// Phi(-a) / (e t) is so smooth in t that a polynomial, fitted for the least largest
-// relative error over a in [0, 20], stays within 2^-17 of it (degree 5, for results of 16
-// bits) or 2^-25 (degree 8). With the roundings of fp32 the latter is within 2^-20
-// of itself up to a = 4, 2^-17 up to 13, where e leaves the range of fp32. dz of 4093 x
-// 2816 24 us, 36 to 40 with erfcf; 4093 x 5632 x 2816 forward with gelu 138, 156 with it.
-template <bool NARROW>
+// Phi(-a) / (e t) is so smooth in t that a polynomial of degree 8, fitted for the least
+// largest relative error over a in [0, 20], stays within 2^-25 of it. With the
+// roundings of fp32 it is within (18 + 1.1 a^2) 2^-24 of itself, up to 13, where e leaves the
+// range of fp32. dz of 4093 x 2816 24 us, 36 to 40 with erfcf; 4093 x 5632 x 2816
+// forward with gelu, residual and z 141, 156 with it.
 __device__ __forceinline__ float normal_tail(float a, float e) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(NARROW ? 0.311126977f : 0.268700570f, a, 1.0f));
-  float q;
-  if constexpr (NARROW) {
-    q = fmaf(-0.0719563290f, t, 0.172309935f);
-    q = fmaf(q, t, 0.0234833770f);
-    q = fmaf(q, t, 0.130294949f);
-    q = fmaf(q, t, 0.121615790f);
-    q = fmaf(q, t, 0.124253877f);
-  } else {
-    q = fmaf(0.0290484875f, t, -0.129195794f);
-    q = fmaf(q, t, 0.178268000f);
-    q = fmaf(q, t, -0.0769507661f);
-    q = fmaf(q, t, 0.112688191f);
-    q = fmaf(q, t, 0.0701929182f);
-    q = fmaf(q, t, 0.101762444f);
-    q = fmaf(q, t, 0.106982090f);
-    q = fmaf(q, t, 0.107204415f);
-  }
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.268700570f, a, 1.0f));
+  float q = fmaf(0.0290484875f, t, -0.129195794f);
+  q = fmaf(q, t, 0.178268000f);
+  q = fmaf(q, t, -0.0769507661f);
+  q = fmaf(q, t, 0.112688191f);
+  q = fmaf(q, t, 0.0701929182f);
+  q = fmaf(q, t, 0.101762444f);
+  q = fmaf(q, t, 0.106982090f);
+  q = fmaf(q, t, 0.107204415f);
   return e * (t * q);
 }
 // exp(-z^2 / 2)
@@ -110,7 +102,7 @@ __device__ __forceinline__ float act_of(float z, int act) {
     case MPB_ACT_SILU: return z * sig(z);
     case MPB_ACT_GELU: {
       if constexpr (!NARROW) return 0.5f * z * erfcf(-z * kSqrtHalf);
-      const float tail = normal_tail<true>(fabsf(z), bell(z));
+      const float tail = normal_tail(fabsf(z), bell(z));
       return z * (z > 0.0f ? 1.0f - tail : tail);
     }
     case MPB_ACT_GELU_TANH: return z * sig(2.0f * kTanhA * (z + kTanhB * z * z * z));
@@ -139,7 +131,7 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     }
     case MPB_ACT_GELU: {
       const float x = z != z ? z : fminf(fmaxf(z, -20.0f), 20.0f);
-      const float e = bell(x), tail = normal_tail<false>(fabsf(x), e);
+      const float e = bell(x), tail = normal_tail(fabsf(x), e);
       return fmaf(x * kInvSqrt2Pi, e, x > 0.0f ? 1.0f - tail : tail);
     }
     case MPB_ACT_GELU_TANH: {
