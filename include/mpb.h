@@ -532,7 +532,8 @@ int moe_head_norm_grad(const void* q_dev, int64_t q_stride, const void* k_dev, i
  * (masked): p_v = 0, and kl is infinite where the teacher gives such an id (or the
  * rest, if all of it is masked) weight. A row that is -inf throughout, or has no
  * entries, has kl 0 and a gradient of zeros. NaN and +inf logits give NaN. Exponentials
- * are summed in fp32 in a fixed order, sums over the entries and rows in fp64. dS may
+ * are fp32 and summed in fp32 in a fixed order, sums over the entries and rows are fp64;
+ * loss and kl have the same bits with and without dS. dS may
  * not overlap S otherwise and lies at the same offset from a 16-byte boundary. Needs
  * V in 1..400000, k in 1..256, tau in 1e-3..1e3, T <= 2^20; T == 0: loss 0. Errors:
  * MPB_E_ARG, MPB_E_SHAPE, MPB_E_HIP. Does not need mpb_init.

@@ -393,9 +393,11 @@ hipError_t launch(const DistillParams& p, bool loss, hipStream_t s) {
   if (p.T > 0) {
     // Up to 512 threads, four rows a CU, which hide each other's ends (1021 x 65536 fp16:
     // loss 34 us, 44 with 1024); 1024 where there are no four rows for every CU, or where
-    // their second reading would not find them in the 256 MB Infinity Cache (2048 x
-    // 151677 bf16 with the gradient: 304 us with 1024 threads, 347 with 512).
-    const bool wide = p.T <= 512 || (loss && p.dS && (double)p.V * sizeof(typename D::elem) * 1024 > 2e8);
+    // the gradient's second reading would not find them in the 256 MB Infinity Cache (2048 x
+    // 151677 bf16 with the gradient: 294 us with 1024 threads, 334 with 512). The loss alone
+    // takes as many threads as with its gradient, so that its bits are the same (2048 x 151677
+    // bf16 105 us with 1024, 110 with 512; 700 x 250001 68 and 64).
+    const bool wide = p.T <= 512 || (loss && (double)p.V * sizeof(typename D::elem) * 1024 > 2e8);
     const int n = (p.V + 31) / 32, most = wide ? 1024 : 512, nt = n >= most ? most : n <= 256 ? 256 : (n + 63) / 64 * 64;
     const size_t lds = 4 * (size_t)p.words;
     auto* k = loss ? (p.dS ? k_distill<D, true, true> : k_distill<D, true, false>) : k_distill<D, false, true>;
