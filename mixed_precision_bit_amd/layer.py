@@ -272,6 +272,8 @@ class DeviceLayer:
     def _like_logits(S):
         """A tensor with S's shape, row stride and place against a 16-byte boundary; zeros between the rows, so that
         the logits of a vocabulary padded for project_grad get a gradient of the padded width."""
+        if S.dim() != 2 or (S.shape[0] > 1 and S.stride(0) < S.shape[1]):
+            return torch.empty_like(S)  # which the call refuses
         (T, V), ld, at = S.shape, S.stride(0), S.data_ptr() % 16 // S.element_size()
         if T == 1 and not V <= ld <= 2 * V:  # one row's stride says nothing
             ld = V
