@@ -505,7 +505,9 @@ int moe_head_norm_grad(const void* q_dev, int64_t q_stride, const void* k_dev, i
 
 /*
  * Distillation of a teacher's stored top logits: what a model whose experts run at
- * lower bitwidths loses against the full one, and the gradient that wins it back.
+ * lower bitwidths loses against the full one, and its gradient, which trains what has a
+ * backward pass here: the output head, dense projections and norms (the packed experts
+ * and moe_adapters have none: past them it goes by the residual stream alone).
  * For every row, with p = softmax(s / tau) over the V student logits and k stored
  * teacher logits y_j at ids_j,
  *   q_j = exp(y_j / tau - L)

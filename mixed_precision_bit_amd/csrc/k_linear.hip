@@ -13,13 +13,15 @@
 // order (reductions split over workgroups leave partial sums that a second launch
 // adds in order).
 //
-// Large products are bound by the matrix cores under the card's power (they are busy 64 %
-// of dX's cycles, at 2 GHz): 8192 x 4096 x 4096 bf16 takes dX 210 us and dW 221, 1.31 and
-// 1.24 PFLOP/s, where a library product of those layouts takes 252 and 284, one of 8192^3 reaches 1.39
-// PFLOP/s. What did not help, against dX of 221 to 227 at the time: one buffer of 64 ahead
-// instead of four of 32 (236), reads interleaved with the products in every wave instead
-// of halves of the waves in turn (232), waves of 128 x 128, one a SIMD (252), two
-// workgroups of 128 x 256 a CU with three buffers each (312).
+// Large products are bound by the matrix cores under the card's power (they are busy 65 %
+// of dX's cycles): 8192 x 4096 x 4096 bf16 takes dX 200 us and dW 203, 1.37 and 1.35 PFLOP/s,
+// after 200 passes that settle the clock; a library product of those layouts takes 200
+// and 223 (with bf16 dW), the forward one 174 where this takes 202, and one of 8192^3 reaches
+// 1.64 PFLOP/s where this reaches 1.34. Figures that compare two variants of this file are of a
+// few passes, 5 to 13 % longer. What did not help, against dX of 221 to 227 at the time: one
+// buffer of 64 ahead instead of four of 32 (236), reads interleaved with the products in
+// every wave instead of halves of the waves in turn (232), waves of 128 x 128, one a SIMD
+// (252), two workgroups of 128 x 256 a CU with three buffers each (312).
 //
 // A batch of few tokens reads W once and has little to share: k_skinny, W straight
 // into the registers.
@@ -201,9 +203,10 @@ __device__ __forceinline__ void finish(const LinearOut& o, int64_t m, int n, flo
 // ---------------------------------------------------------------- operands in LDS
 // 16 bytes a lane from src + off to LDS at byte `lds` + 16 lane (src and lds are the
 // wave's). The load has no register of its own that could be reused early, and
-// its address registers are read when it issues; the caller waits for vmcnt(0) before the
-// barrier that hands the buffer over. The builtin of this load makes the compiler
-// wait for it before any transposing read of LDS, of the other buffer too. m0 is
+// its address registers are read when it issues; before the barrier that hands a buffer over
+// the caller waits until no more loads are outstanding than those of later buffers. The builtin
+// of this load makes the compiler wait for it before any transposing read of LDS, of the
+// other buffers too. m0 is
 // reserved to such instructions: nothing else in these kernels counts on its value.
 __device__ __forceinline__ void load_lds16(const char* src, uint32_t off, uint32_t lds) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot parse the operands
@@ -642,7 +645,7 @@ __global__ __launch_bounds__(256) void k_dz(LinearGradParams p) {
 
 // dX and dW in one launch, where both have small tiles and neither fills the chip
 // alone, and dbias of a few tokens (blocks_b workgroups): 200 x 2048 x 2048 with its
-// join 23 us, in a launch each 36.
+// join 21 us a pass, in a launch each 36.
 template <class D, int KIND>
 __global__ __launch_bounds__(256) void k_gradients(LinearProduct x, LinearProduct w, LinearGradParams p, int blocks_x,
                                                    int blocks_b) {
