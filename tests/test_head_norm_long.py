@@ -1,7 +1,7 @@
 """moe_head_norm_grad where a wave has several tokens: the gammas' gradients over the whole batch.
 
 Tolerance of dgamma, u = 2^-24, as in test_head_norm but for the chain of additions: up to 768 workgroups of 4 waves take
-every 3072nd token, 64 / NL heads at a time (NL lanes of 16 elements hold a head), so a lane adds the tokens of its wave
+every (4 x 768)th token, 64 / NL heads at a time (NL lanes of 16 elements hold a head), so a lane adds the tokens of its wave
 times their groups of heads; then come the lanes, the 4 waves, and the workgroups' rows in 16 chains."""
 import pytest
 
@@ -21,7 +21,7 @@ def check_dgamma(d, got_q, got_k, chunk=1 << 24):
         if got is None:
             continue
         H = x.shape[1]
-        adds = -(-T // 3072) * -(-H // (64 // nl)) + 6 + 4 + 48 + 16
+        adds = -(-T // (4 * 768)) * -(-H // (64 // nl)) + 6 + 4 + 48 + 16
         ref = terms = 0.0
         rows = max(1, chunk // (H * D))
         for t in range(0, T, rows):
@@ -35,7 +35,7 @@ def check_dgamma(d, got_q, got_k, chunk=1 << 24):
 
 # more tokens than waves; groups of heads that fill a wave, and that do not; lanes past the end of a head
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-@pytest.mark.parametrize("T,Hq,Hk,D,Dr,pairs", [(8191, 5, 3, 96, 64, 0), (8192, 16, 8, 256, 128, 1), (3073, 9, 1, 128, 128, 0),
+@pytest.mark.parametrize("T,Hq,Hk,D,Dr,pairs", [(8191, 5, 3, 96, 64, 0), (8192, 16, 8, 256, 128, 1), (3100, 9, 1, 128, 128, 0),
                                                 (6145, 3, 2, 512, 0, 0), (20000, 2, 1, 16, 16, 1), (9217, 33, 5, 32, 32, 0)])
 def test_gradients_of_several_tokens_a_wave(T, Hq, Hk, D, Dr, pairs, dt):
     d = TH.inputs(T, Hq, Hk, D, Dr, dt, A=2 if Dr > 16 else 1, pairs=pairs, seed=7)
