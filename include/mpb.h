@@ -417,8 +417,9 @@ int moe_adapters(const void* X_dev, int x_dtype, int T, int Kd, const void* A_de
  * Products are exact, sums fp32 in a fixed order (deterministic), and act is taken
  * of the unrounded z, in fp32: a sigmoid of x within (6 + |x|) 2^-24 of itself (for y of
  * 16 bits 0 below x = -88.7), Phi(-|z|) within (18 + 1.1 z^2) 2^-24 of itself (either
- * may be 0 where it is under 2^-126). Each output is rounded once. Needs Kd a multiple of 64 up to 65536, N a multiple of 8 up to
- * 524288, T <= 2^20, 16-byte aligned rows; T == 0 is a no-op. ws_dev (16-byte aligned): at least moe_linear_workspace_bytes(T, Kd, N)
+ * may be 0 where it is under 2^-126). Each output is rounded once. Needs Kd a multiple of
+ * 64 up to 65536, N a multiple of 8 up to 524288, T <= 2^20, 16-byte aligned rows; T == 0
+ * is a no-op. ws_dev (16-byte aligned): at least moe_linear_workspace_bytes(T, Kd, N)
  * bytes (for this T: a smaller batch may need more), contents not preserved; calls
  * that may overlap need a workspace each. Errors: MPB_E_ARG, MPB_E_SHAPE, MPB_E_WS,
  * MPB_E_HIP. Does not need mpb_init.
